@@ -32,6 +32,7 @@ SDP_ERR_OVERFLOW = -4
 SDP_ERR_CUDA = -5
 SDP_ERR_DEVICE_TIMEOUT = -6
 SDP_ERR_BAD_SEQLENS = -7
+SDP_ERR_BAD_PAGES = -8
 
 _DTYPE_CODE = {torch.float16: SDP_FP16, torch.bfloat16: SDP_BF16}
 
@@ -399,3 +400,9 @@ def noalloc_status(stream=None, device=None) -> int:
 fwd = sdp_fwd
 fwd_varlen = sdp_fwd_varlen
 merge = sdp_merge
+
+# The operators around the attention forward (they use this module's checks, so they come last).
+from . import serving  # noqa: E402
+from .serving import *  # noqa: E402,F401,F403
+
+__all__ += serving.__all__

@@ -1,0 +1,296 @@
+// sdp_qk_norm_rope: the norm of every query and key head and the rotation by position, in
+// one pass over both.
+//
+// For the row x of one token and head (D channels), with weight w (the norm is left out where
+// there is none):
+//
+//     y_c = x_c * w_c / sqrt(sum_j x_j^2 / D + eps)
+//
+// and for pair i of the first R channels, (y_i, y_{i + R/2}) or, interleaved, (y_2i, y_2i+1):
+//
+//     (a, b) -> m * (a cos t - b sin t, a sin t + b cos t),   t = position * f_i.
+//
+// Everything is in fp32, rounded once when the row is stored.
+//
+// Angles: fp32 products lose the angle at far positions (position 1e6 leaves an error of 0.06
+// rad), so the table holds each frequency in turns per position as a 64-bit binary fraction,
+// u_i = f_i / (2 pi) * 2^64: position * u_i modulo 2^64 is the fraction of a turn, exactly as
+// far as u_i is, and its upper 32 bits, read as a signed number, are the angle in units of
+// 2^-31 half turns for sincospif. The product costs three integer multiplications.
+//
+// The work is HBM-bound: each element is read and written once. A warp takes one token and a
+// run of its heads, D/8 lanes a row with one 16-byte load each, kPassUnroll rows' loads in
+// flight; the token's R/2 cosines and sines are computed once for the run, spread over the
+// lanes, and read back from shared memory (with every lane computing its own eight pairs, four
+// lanes would compute each of them at D = 128).
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sdp.h"
+#include "sdp_internal.h"
+#include "sixteen.cuh"
+
+namespace {
+
+using sdp::pack8;
+using sdp::unpack8;
+
+constexpr int kWarps = 4;
+constexpr int kPassUnroll = 4;
+constexpr unsigned FULL = 0xffffffffu;
+
+struct RopeParams {
+    const uint16_t *q, *k;
+    uint16_t *q_out, *k_out;
+    // strides in elements: batch, token, head
+    long long qs[3], ks[3], qos[3], kos[3];
+    const void *positions;
+    long long ps[2];  // batch, token
+    const unsigned long long *turns;
+    const void *wq, *wk;
+    float mscale, eps;
+    int S, Hq, Hkv, R;
+    int tokens;         // B * S
+    int rows_per_warp;  // heads a warp runs through, in passes of 32 / (D / 8) rows
+};
+
+// w: eight weights at channel c0 of `base`, 16-bit or fp32.
+template <bool BF16, bool W32>
+__device__ __forceinline__ void load_weights(const void *base, int c0, float (&w)[8])
+{
+    if constexpr (W32) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + c0));
+        const float4 b = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + c0 + 4));
+        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
+        unpack8<BF16>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + c0)), w);
+    }
+}
+
+template <int D, bool BF16, bool W32, bool POS64, bool INTERLEAVED>
+__global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopeParams p)
+{
+    constexpr int LPR = D / 8;     // lanes a row
+    constexpr int RPP = 32 / LPR;  // rows a pass
+    __shared__ float2 cs_all[kWarps][D / 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = p.Hq + p.Hkv;
+    const int runs = (heads + p.rows_per_warp - 1) / p.rows_per_warp;
+    const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
+    if (item >= static_cast<long long>(p.tokens) * runs)
+        return;
+    const int token = static_cast<int>(item / runs);
+    const int h0 = static_cast<int>(item - static_cast<long long>(token) * runs) * p.rows_per_warp;
+    const int h1 = min(heads, h0 + p.rows_per_warp);
+    const int b = token / p.S, s = token - b * p.S;
+    float2 *cs = cs_all[warp];
+
+    const int sub = lane / LPR, c0 = (lane % LPR) * 8;
+    const uint16_t *q = p.q + b * p.qs[0] + s * p.qs[1] + c0;
+    const uint16_t *k = p.k + b * p.ks[0] + s * p.ks[1] + c0;
+    uint16_t *qo = p.q_out + b * p.qos[0] + s * p.qos[1] + c0;
+    uint16_t *ko = p.k_out + b * p.kos[0] + s * p.kos[1] + c0;
+    auto src = [&](int h) {
+        return reinterpret_cast<const uint4 *>(h < p.Hq ? q + h * p.qs[2] : k + (h - p.Hq) * p.ks[2]);
+    };
+    auto dst = [&](int h) {
+        return reinterpret_cast<uint4 *>(h < p.Hq ? qo + h * p.qos[2] : ko + (h - p.Hq) * p.kos[2]);
+    };
+    // the first rows' loads run while the angles are computed
+    uint4 v[kPassUnroll];
+#pragma unroll
+    for (int i = 0; i < kPassUnroll; ++i) {
+        const int h = h0 + i * RPP + sub;
+        if (h < h1)
+            v[i] = *src(h);
+    }
+
+    const int half = p.R / 2;
+    if (half > 0) {
+        const long long at = b * p.ps[0] + s * p.ps[1];
+        const long long pos = POS64 ? static_cast<const long long *>(p.positions)[at]
+                                    : static_cast<const int *>(p.positions)[at];
+        for (int i = lane; i < half; i += 32) {
+            const unsigned long long turn = static_cast<unsigned long long>(pos) * __ldg(p.turns + i);
+            float sn, c;
+            sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);  // 2^-31
+            cs[i] = make_float2(c * p.mscale, sn * p.mscale);
+        }
+        __syncwarp();
+    }
+    // this lane's pairs: interleaved, pairs c0/2 .. +3 of its own channels; else pairs c0 .. +7 of
+    // its channels and those R/2 away, which lane +- R/16 of the same row holds
+    const bool turns_here = c0 < p.R;
+    const bool upper = c0 >= half;
+    float cc[8], sn[8];
+    if (turns_here) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 t = INTERLEAVED ? cs[c0 / 2 + e / 2] : cs[(upper ? c0 - half : c0) + e];
+            cc[e] = t.x;
+            // the partner's sign: - sin for a pair's first channel, + sin for its second
+            sn[e] = (INTERLEAVED ? (e & 1) : upper) ? t.y : -t.y;
+        }
+    }
+    const int partner = turns_here ? (upper ? lane - half / 8 : lane + half / 8) : lane;
+
+    for (int h = h0; h < h1; h += kPassUnroll * RPP) {
+        if (h != h0) {
+#pragma unroll
+            for (int i = 0; i < kPassUnroll; ++i) {
+                const int hr = h + i * RPP + sub;
+                if (hr < h1)
+                    v[i] = *src(hr);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPassUnroll; ++i) {
+            if (h + i * RPP >= h1)
+                break;  // the same for the whole warp
+            const int hr = h + i * RPP + sub;
+            const bool live = hr < h1;
+            float x[8];
+            unpack8<BF16>(live ? v[i] : make_uint4(0u, 0u, 0u, 0u), x);
+            const void *wb = hr < p.Hq ? p.wq : p.wk;
+            if (p.wq != nullptr || p.wk != nullptr) {
+                float ss = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+                for (int off = LPR / 2; off > 0; off >>= 1)
+                    ss += __shfl_xor_sync(FULL, ss, off);
+                if (wb != nullptr) {
+                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
+                    float w[8];
+                    load_weights<BF16, W32>(wb, c0, w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] *= r * w[e];
+                }
+            }
+            if (half > 0) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = INTERLEAVED ? x[e ^ 1] : __shfl_sync(FULL, x[e], partner);
+                if (turns_here) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        x[e] = fmaf(x[e], cc[e], y[e] * sn[e]);
+                }
+            }
+            if (live)
+                *dst(hr) = pack8<BF16>(x);
+        }
+    }
+}
+
+template <int D, bool BF16, bool W32, bool POS64>
+cudaError_t launch(const RopeParams &p, bool interleaved, unsigned blocks, cudaStream_t st)
+{
+    if (interleaved)
+        qk_norm_rope_kernel<D, BF16, W32, POS64, true><<<blocks, 32 * kWarps, 0, st>>>(p);
+    else
+        qk_norm_rope_kernel<D, BF16, W32, POS64, false><<<blocks, 32 * kWarps, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int D, bool BF16>
+cudaError_t launch(const RopeParams &p, bool w32, bool pos64, bool interleaved, unsigned blocks, cudaStream_t st)
+{
+    if (w32)
+        return pos64 ? launch<D, BF16, true, true>(p, interleaved, blocks, st)
+                     : launch<D, BF16, true, false>(p, interleaved, blocks, st);
+    return pos64 ? launch<D, BF16, false, true>(p, interleaved, blocks, st)
+                 : launch<D, BF16, false, false>(p, interleaved, blocks, st);
+}
+
+}  // namespace
+
+extern "C" int sdp_qk_norm_rope(const void *q, long long q_sb, long long q_ss, long long q_sh, const void *k,
+                                long long k_sb, long long k_ss, long long k_sh, void *q_out, long long qo_sb,
+                                long long qo_ss, long long qo_sh, void *k_out, long long ko_sb, long long ko_ss,
+                                long long ko_sh, const void *positions, long long p_sb, long long p_ss,
+                                int positions_64, const unsigned long long *turns, int rot_dim, float mscale,
+                                const void *q_weight, const void *k_weight, int weight_fp32, float eps,
+                                int interleaved, int B, int S, int Hq, int Hkv, int D, int dtype, void *stream)
+{
+    if (dtype != SDP_FP16 && dtype != SDP_BF16)
+        return SDP_ERR_UNSUPPORTED;
+    if (D != 128 && D != 256)
+        return SDP_ERR_UNSUPPORTED;
+    if (B < 0 || S < 0 || Hq < 0 || Hkv < 0 || rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0)
+        return SDP_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !(eps <= 3.0e38f) || !(mscale >= -3.0e38f && mscale <= 3.0e38f))
+        return SDP_ERR_INVALID_ARG;
+    if (B == 0 || S == 0 || Hq + static_cast<long long>(Hkv) == 0)
+        return SDP_OK;
+    if ((Hq > 0 && (q == nullptr || q_out == nullptr)) || (Hkv > 0 && (k == nullptr || k_out == nullptr)))
+        return SDP_ERR_INVALID_ARG;
+    if (rot_dim > 0 && (positions == nullptr || turns == nullptr))
+        return SDP_ERR_INVALID_ARG;
+    using sdp::is_aligned;
+    const long long strides[12] = {q_sb, q_ss, q_sh, k_sb, k_ss, k_sh, qo_sb, qo_ss, qo_sh, ko_sb, ko_ss, ko_sh};
+    for (long long s : strides)
+        if (s % 8 != 0)
+            return SDP_ERR_ALIGNMENT;
+    if (!is_aligned(q, 16) || !is_aligned(k, 16) || !is_aligned(q_out, 16) || !is_aligned(k_out, 16) ||
+        !is_aligned(q_weight, 16) || !is_aligned(k_weight, 16) || !is_aligned(turns, 8) ||
+        !is_aligned(positions, positions_64 ? 8 : 4))
+        return SDP_ERR_ALIGNMENT;
+    const long long tokens = static_cast<long long>(B) * S;
+    const long long heads = static_cast<long long>(Hq) + Hkv;
+    if (tokens > INT32_MAX || heads > INT32_MAX)
+        return SDP_ERR_OVERFLOW;
+    int dev = 0, sms = 0;
+    const int rc = sdp::current_device(&dev, &sms);
+    if (rc != SDP_OK)
+        return rc;
+
+    RopeParams p{};
+    p.q = static_cast<const uint16_t *>(q);
+    p.k = static_cast<const uint16_t *>(k);
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.k_out = static_cast<uint16_t *>(k_out);
+    for (int i = 0; i < 3; ++i) {
+        p.qs[i] = strides[i];
+        p.ks[i] = strides[3 + i];
+        p.qos[i] = strides[6 + i];
+        p.kos[i] = strides[9 + i];
+    }
+    p.positions = positions;
+    p.ps[0] = p_sb;
+    p.ps[1] = p_ss;
+    p.turns = turns;
+    p.wq = q_weight;
+    p.wk = k_weight;
+    p.mscale = mscale;
+    p.eps = eps;
+    p.S = S;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.R = rot_dim;
+    p.tokens = static_cast<int>(tokens);
+    // Rows a warp: one pass while that leaves SMs without a full set of warps, then as many as
+    // share a token's angles.
+    const int rpp = 256 / D;
+    const long long passes = (heads + rpp - 1) / rpp;
+    long long per = tokens * passes / (static_cast<long long>(sms) * 32);
+    per = per < 1 ? 1 : (per > passes ? passes : per);
+    p.rows_per_warp = static_cast<int>(per * rpp);
+    const long long runs = (heads + p.rows_per_warp - 1) / p.rows_per_warp;
+    const long long blocks = (tokens * runs + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX)
+        return SDP_ERR_OVERFLOW;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool w32 = weight_fp32 != 0, p64 = positions_64 != 0, il = interleaved != 0;
+    const unsigned g = static_cast<unsigned>(blocks);
+    cudaError_t e;
+    if (D == 128)
+        e = dtype == SDP_BF16 ? launch<128, true>(p, w32, p64, il, g, st) : launch<128, false>(p, w32, p64, il, g, st);
+    else
+        e = dtype == SDP_BF16 ? launch<256, true>(p, w32, p64, il, g, st) : launch<256, false>(p, w32, p64, il, g, st);
+    return e == cudaSuccess ? SDP_OK : sdp::record_cuda_error(e);
+}

@@ -13,6 +13,7 @@
 #include <unordered_map>
 
 #include "sdp.h"
+#include "sdp_internal.h"
 #include "sdp_launch.h"
 
 namespace {
@@ -482,7 +483,34 @@ int forward_with(const void *q, const void *k, const void *v, void *o, float *ls
 int status_code_of(unsigned int word)
 {
     g_last_detail.store(word);
-    return (word & 0xffu) == 7u ? SDP_ERR_BAD_SEQLENS : SDP_ERR_DEVICE_TIMEOUT;
+    const unsigned site = word & 0xffu;
+    return site == kBadSeqlens ? SDP_ERR_BAD_SEQLENS : site == kBadPages ? SDP_ERR_BAD_PAGES : SDP_ERR_DEVICE_TIMEOUT;
+}
+
+int record_cuda_error(cudaError_t e) { return cuda_fail(e); }
+
+int current_device(int *dev, int *sms)
+{
+    const cudaError_t e = cudaGetDevice(dev);
+    return e != cudaSuccess ? cuda_fail(e) : device_info(*dev, sms);
+}
+
+int status_word(int dev, unsigned int **status) { return device_state(dev, status, nullptr); }
+
+unsigned long long wait_timeout_ns() { return static_cast<unsigned long long>(g_timeout_ms.load()) * 1000000ull; }
+
+int debug_flags() { return g_debug_flags.load(); }
+
+int tensor_map(CUtensorMap *map, const void *base, int dtype, int D, long long rows, long long planes,
+               unsigned box_rows)
+{
+    return encode_map(map, base, dtype, D, rows, planes, box_rows);
+}
+
+int tensor_map_thd(CUtensorMap *map, const void *base, int dtype, int D, long long rows, long long heads,
+                   unsigned box_rows)
+{
+    return encode_map_thd(map, base, dtype, D, rows, heads, box_rows);
 }
 
 }  // namespace sdp
@@ -703,6 +731,8 @@ const char *sdp_strerror(int code)
     case SDP_ERR_BAD_SEQLENS:
         return "variable-length batch: sequence offsets out of range, decreasing, or longer than max_seqlen_q; "
                "those sequences were not written";
+    case SDP_ERR_BAD_PAGES:
+        return "paged cache: a block table names a page outside the pool";
     default:
         return "unknown status code";
     }

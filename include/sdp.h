@@ -38,7 +38,8 @@ extern "C" {
 #define SDP_ERR_OVERFLOW (-4)       /* index space does not fit the kernel's 32-bit tile and coordinate counters */
 #define SDP_ERR_CUDA (-5)           /* a CUDA runtime/driver call failed; sdp_last_cuda_error() gives the code */
 #define SDP_ERR_DEVICE_TIMEOUT (-6) /* a kernel gave up on a bounded wait and flagged its status word */
-#define SDP_ERR_BAD_SEQLENS (-7)    /* sdp_fwd_varlen: a kernel found bad sequence offsets (status word) */
+#define SDP_ERR_BAD_SEQLENS (-7)    /* a kernel found bad sequence offsets or lengths (status word) */
+#define SDP_ERR_BAD_PAGES (-8)      /* a kernel found a block table entry outside the pool (status word) */
 
 /*
  * sdp_fwd — O = softmax(Q K^T * scale) V and LSE, enqueued on `stream`.
@@ -245,10 +246,84 @@ int sdp_fwd_noalloc(const void *q, const void *k, const void *v, void *o, float 
 int sdp_fwd_noalloc_status(void *stream);
 
 /*
+ * sdp_qk_norm_rope — the norm of every query and key head and the rotation by
+ * position, in one pass over both (what the attention calls' q and k go through
+ * first). For the row x of a token and head, with the weight w of its tensor (no
+ * norm where the weight is NULL): y_c = x_c * w_c / sqrt(sum_j x_j^2 / D + eps).
+ * For pair i < rot_dim / 2 of the first rot_dim channels, (y_i, y_{i + rot_dim/2})
+ * or, interleaved != 0, (y_2i, y_{2i+1}):
+ *     (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),  t = position * f_i;
+ * the other channels are left as the norm gives them. Sums, angles and products in
+ * fp32 (the angle's fraction of a turn exactly, at any position), rounded once.
+ *
+ * q, q_out  device, dtype, rows of D at strides (batch, token, head) in elements,
+ *           multiples of 8; 16-byte aligned. q_out may be q with q's strides (in
+ *           place); other overlaps are undefined. k, k_out alike. Hq or Hkv 0
+ *           leaves a tensor out (its pointers may be NULL).
+ * positions device, int32 or (positions_64) int64, at strides (batch, token) in
+ *           elements, 0 allowed; any value. Not read when rot_dim is 0.
+ * turns     device, [rot_dim / 2]: f_i / (2 pi) * 2^64 modulo 2^64, f_i in rad per position
+ * rot_dim   a multiple of 16 in [0, D]
+ * q_weight, k_weight  device [D] of dtype or (weight_fp32) fp32, 16-byte aligned, or NULL
+ * eps >= 0 and mscale finite; D in {128, 256}. B, S, or Hq + Hkv of 0 does nothing.
+ * Errors and streams as sdp_fwd; nothing is allocated and no status word is used.
+ */
+int sdp_qk_norm_rope(const void *q, long long q_sb, long long q_ss, long long q_sh, const void *k, long long k_sb,
+                     long long k_ss, long long k_sh, void *q_out, long long qo_sb, long long qo_ss, long long qo_sh,
+                     void *k_out, long long ko_sb, long long ko_ss, long long ko_sh, const void *positions,
+                     long long p_sb, long long p_ss, int positions_64, const unsigned long long *turns, int rot_dim,
+                     float mscale, const void *q_weight, const void *k_weight, int weight_fp32, float eps,
+                     int interleaved, int B, int S, int Hq, int Hkv, int D, int dtype, void *stream);
+
+/*
+ * The paged cache held in 4 bits. A pool of num_pages pages of page_size tokens
+ * (a multiple of 16):
+ *     k_codes, v_codes    uint8 [num_pages, Hkv, page_size, D / 2]: channel 2i in the
+ *                         low, 2i + 1 in the high half of byte i
+ *     k_scales, v_scales  bf16 [num_pages, Hkv, page_size, D / 64, 2]: scale s and bias b
+ *                         of each 64 channels; code n stands for s * n + b
+ * (16-byte aligned, contiguous). Token t of sequence i is at place t % page_size of
+ * page block_table[i * table_stride + t / page_size] (device int32 [nseq, max_pages];
+ * entries past a sequence's last page are not read). Several sequences may share
+ * pages that none of them writes.
+ *
+ * sdp_cache4_append — quantises new rows into the cache: with x the 64 values of a
+ * group, b = bf16(min x), s = bf16(max(0, (max x - b) / 15)) and
+ * n = clamp(rint((x - b) / s), 0, 15), 0 where s = 0 (all in fp32, ties to even). A
+ * group that holds an infinity or a NaN reads back as NaN.
+ *   k, v        device, dtype [tokens, Hkv, D] at token and head strides in elements,
+ *               multiples of 8; 16-byte aligned
+ *   cu_seqlens  device int32 [nseq + 1], non-decreasing: sequence i brings rows
+ *               cu[i] .. cu[i + 1] - 1, its last tokens; rows in no sequence are left out
+ *   cache_lens  device int32 [nseq]: lengths WITH the new tokens, so row r of sequence i is
+ *               its token cache_lens[i] - (cu[i + 1] - cu[i]) + r - cu[i]
+ * A page that two sequences write at the same places holds either's rows, or a mixture.
+ *
+ * sdp_cache4_gather — reads sequences back as 16-bit rows (fp32 value, rounded once): row
+ * cu[i] + t of k and v becomes token t of sequence i. Rows in no sequence are not written.
+ * For a prefill over a cached prefix: gather, then attend over the packed rows.
+ *
+ * Offsets that decrease or leave [0, tokens], lengths below the new rows or past
+ * max_pages * page_size (SDP_ERR_BAD_SEQLENS) and pages outside the pool
+ * (SDP_ERR_BAD_PAGES) are found by the kernels: those rows are skipped and the next
+ * sdp_poll_status reports it. Errors, streams and the status word's first-call
+ * allocation as sdp_fwd.
+ */
+int sdp_cache4_append(void *k_codes, void *k_scales, void *v_codes, void *v_scales, int num_pages, int page_size,
+                      const int *block_table, long long table_stride, int max_pages, const void *k, long long k_st,
+                      long long k_sh, const void *v, long long v_st, long long v_sh, const int *cu_seqlens,
+                      const int *cache_lens, int nseq, int tokens, int Hkv, int D, int dtype, void *stream);
+int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales,
+                      int num_pages, int page_size, const int *block_table, long long table_stride, int max_pages,
+                      void *k, long long k_st, long long k_sh, void *v, long long v_st, long long v_sh,
+                      const int *cu_seqlens, int nseq, int tokens, int Hkv, int D, int dtype, void *stream);
+
+/*
  * sdp_poll_status — synchronise `stream`, then read and clear the current
  * device's status word. Returns SDP_OK, SDP_ERR_DEVICE_TIMEOUT (a kernel
  * abandoned a wait after the timeout and returned without writing its
- * tile), SDP_ERR_BAD_SEQLENS (sdp_fwd_varlen found bad offsets), or
+ * tile), SDP_ERR_BAD_SEQLENS (a kernel found bad offsets or lengths), SDP_ERR_BAD_PAGES
+ * (a block table entry outside the pool), or
  * SDP_ERR_CUDA (the synchronisation itself failed).
  */
 int sdp_poll_status(void *stream);
@@ -257,7 +332,7 @@ int sdp_poll_status(void *stream);
  * sdp_last_status_detail — the raw status word read by the last
  * sdp_poll_status() that found an error: bits 0-7 name the wait that timed
  * out (1 Q load, 2 KV slot empty, 3 KV slot full, 4 S ready, 5 P ready,
- * 6 O done) or 7 for bad sequence offsets, bits 8-31 the CTA index (saturating).
+ * 6 O done) or 7 for bad sequence offsets, 8 for bad pages, bits 8-31 the CTA index (saturating).
  */
 unsigned int sdp_last_status_detail(void);
 
