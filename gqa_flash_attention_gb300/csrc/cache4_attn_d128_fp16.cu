@@ -1,0 +1,11 @@
+// Instantiation of the 4-bit cache attention: head dim 128, fp16 I/O.
+#include "cache4_attn.cuh"
+
+namespace sdp {
+
+cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, cudaStream_t st)
+{
+    return wide ? launch_cache4_attn<128, false, 2>(p, st) : launch_cache4_attn<128, false, 1>(p, st);
+}
+
+}  // namespace sdp

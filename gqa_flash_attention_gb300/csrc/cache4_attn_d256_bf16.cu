@@ -1,0 +1,11 @@
+// Instantiation of the 4-bit cache attention: head dim 256, bf16 I/O.
+#include "cache4_attn.cuh"
+
+namespace sdp {
+
+cudaError_t cache4_attn_d256_bf16(const Cache4AttnParams &p, bool wide, cudaStream_t st)
+{
+    return wide ? launch_cache4_attn<256, true, 2>(p, st) : launch_cache4_attn<256, true, 1>(p, st);
+}
+
+}  // namespace sdp

@@ -2,7 +2,8 @@
 
 ``qk_norm_rope``: norms and position rotation of the query and key heads in one pass, with
 ``rope_inv_freq`` and ``rope_table`` for its frequencies. ``Cache4``: a paged cache held in 4 bits,
-written by ``cache4_append`` and read back by ``cache4_gather``.
+written by ``cache4_append`` and read back by ``cache4_gather``; ``fwd_cache4``: the attention of each
+sequence's last tokens over it.
 
 As in the rest of the package, these functions check and marshal arguments for the C ABI of
 ``include/sdp.h`` (which states layouts, ownership and errors), PyTorch supplies memory and
@@ -20,7 +21,7 @@ import torch
 from . import SDP_OK, _check, _DTYPE_CODE, _on, _stream_handle, lib
 
 __all__ = ["rope_inv_freq", "rope_table", "RopeTable", "qk_norm_rope", "Cache4", "cache4_empty", "cache4_append",
-           "cache4_gather", "CACHE4_GROUP"]
+           "cache4_gather", "CACHE4_GROUP", "fwd_cache4", "cache4_workspace_bytes"]
 
 CACHE4_GROUP = 64  # channels that share one scale and bias
 
@@ -41,6 +42,10 @@ def _lib() -> ctypes.CDLL:
         L.sdp_cache4_append.restype = i
         L.sdp_cache4_gather.argtypes = pool + [vp, ll, ll, vp, ll, ll, vp, i, i, i, i, i, vp]
         L.sdp_cache4_gather.restype = i
+        L.sdp_fwd_cache4_workspace_bytes.argtypes = [i, i, i, i, i, i]
+        L.sdp_fwd_cache4_workspace_bytes.restype = ll
+        L.sdp_fwd_cache4.argtypes = [vp, *pool, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, ctypes.c_ulonglong, vp]
+        L.sdp_fwd_cache4.restype = i
         _declared = L
     return _declared
 
@@ -50,6 +55,20 @@ def _no_grad(*tensors) -> None:
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise ValueError("forward only: detach the inputs or run under torch.no_grad()")
+
+
+def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
+    """A new tensor that work on `stream` may write at once: from that stream's own pool (a block of
+    the current stream's pool could still be in use there), and safe to free from the current one."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=dev) if stream else torch.cuda.default_stream(dev)
+    now = torch.cuda.current_stream(dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(now)
+    return t
 
 
 # ------------------------------------------------------------------ positions
@@ -149,7 +168,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
     if q.stride(-1) != 1:
         raise ValueError("the last dimension of q must be contiguous")
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = _empty(q.shape, q.dtype, dev, stream)
     elif q_out.shape != q.shape or q_out.dtype != q.dtype or q_out.get_device() != dev or q_out.stride(-1) != 1:
         raise ValueError("q_out must be shaped and typed like q, its last dimension contiguous")
     (ob, os_, oh), _ = _rows4(q_out, packed)
@@ -161,7 +180,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tenso
         if (Bk, Sk) != (B, S):
             raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            k_out = _empty(k.shape, k.dtype, dev, stream)
         elif k_out.shape != k.shape or k_out.dtype != k.dtype or k_out.get_device() != dev or k_out.stride(-1) != 1:
             raise ValueError("k_out must be shaped and typed like k, its last dimension contiguous")
         (pb_, ps_, ph_), _ = _rows4(k_out, packed)
@@ -307,9 +326,9 @@ def cache4_gather(cache: Cache4, cu_seqlens: torch.Tensor, block_table: torch.Te
     pool, nseq, Hkv, D = _pool(cache, block_table, dev)
     shape = (int(total), Hkv, D)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
+        k_out = _empty(shape, dtype, dev, stream)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.k_codes.device)
+        v_out = _empty(shape, dtype, dev, stream)
     for t in (k_out, v_out):
         if t.shape != shape or t.dtype != dtype or t.get_device() != dev or t.stride(2) != 1:
             raise ValueError(f"k_out and v_out must be {shape} of dtype, the last dimension contiguous")
@@ -321,3 +340,72 @@ def cache4_gather(cache: Cache4, cu_seqlens: torch.Tensor, block_table: torch.Te
     if rc != SDP_OK:
         _check(rc)
     return k_out, v_out
+
+
+def cache4_workspace_bytes(nseq: int, rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype) -> int:
+    """Bytes of workspace that fwd_cache4 needs for these sizes on the current device."""
+    rc = _lib().sdp_fwd_cache4_workspace_bytes(nseq, rows, Hq, Hkv, D, _DTYPE_CODE[dtype])
+    _check(min(rc, 0))
+    return rc
+
+
+def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_table: torch.Tensor,
+               scale: float | None = None, window: int = 0, sinks: int = 0, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None, return_lse: bool = True, workspace: torch.Tensor | None = None,
+               stream=None):
+    """Attention of each sequence's last rows over the 4-bit cache (decoding).
+
+    q: [nseq, Hq, D], or [nseq, rows, Hq, D] with up to 32 rows (drafted tokens): row i of sequence s
+    is its token cache_lens[s] - rows + i and sees the keys up to itself, already in the cache; with
+    window > 0 only the last `window` of them and the sequence's first `sinks`. Contiguous, fp16 or
+    bf16. cache_lens: int32 [nseq]; block_table: int32 [nseq, max_pages]. Returns (o like q, lse fp32
+    without the last dimension, or None); a row that sees no key gives 0 and -inf.
+
+    workspace: a contiguous CUDA tensor of cache4_workspace_bytes, not used by another call that may
+    overlap; when None it comes from torch's allocator. Enqueued on `stream` (default: the current
+    stream), not synchronised; bad lengths and pages show in poll_status().
+    """
+    shape = q.shape
+    if len(shape) == 3:
+        nseq, Hq, D = shape
+        rows = 1
+    elif len(shape) == 4:
+        nseq, rows, Hq, D = shape
+    else:
+        raise ValueError("q must be [nseq, Hq, D] or [nseq, rows, Hq, D]")
+    dev = q.get_device()
+    dt = _DTYPE_CODE.get(q.dtype)
+    if dev < 0 or dt is None or not q.is_contiguous():
+        raise ValueError("q must be a contiguous float16 or bfloat16 CUDA tensor")
+    _no_grad(q)
+    pool, ns, Hkv, Dc = _pool(cache, block_table, dev)
+    if ns != nseq or Dc != D:
+        raise ValueError(f"shape mismatch: q {tuple(shape)}, {ns} sequences of head dim {Dc} in the cache")
+    lens = _int32("cache_lens", cache_lens, nseq, dev)
+    if out is None:
+        out = _empty(shape, q.dtype, dev, stream)
+    elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out must be a contiguous tensor shaped and typed like q")
+    if lse is None:
+        if return_lse:
+            lse = _empty(shape[:-1], torch.float32, dev, stream)
+    elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
+        raise ValueError("lse must be a contiguous float32 tensor of q's shape without the last dimension")
+    if nseq == 0 or rows == 0:
+        return out, lse
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    with _on(dev):
+        if workspace is None:
+            need = _lib().sdp_fwd_cache4_workspace_bytes(nseq, rows, Hq, Hkv, D, dt)
+            _check(min(need, 0))
+            workspace = _empty((need,), torch.uint8, dev, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on q's device")
+        rc = _lib().sdp_fwd_cache4(
+            q.data_ptr(), *pool, lens, out.data_ptr(), 0 if lse is None else lse.data_ptr(), nseq, rows, Hq, Hkv, D,
+            scale, dt, window, sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+            _stream_handle(stream, dev))
+    if rc != SDP_OK:
+        _check(rc)
+    return out, lse

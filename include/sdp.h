@@ -319,6 +319,33 @@ int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_c
                       const int *cu_seqlens, int nseq, int tokens, int Hkv, int D, int dtype, void *stream);
 
 /*
+ * sdp_fwd_cache4 — attention of each sequence's last `rows` tokens (1 in plain decoding,
+ * a few when drafted tokens are verified; at most 32) over the 4-bit cache: row i of
+ * sequence s is at position p = cache_lens[s] - rows + i and sees keys j <= p; with
+ * window > 0 only those with j > p - window or j < sinks (window 0: all, sinks unused).
+ * A row that sees no key (an empty sequence, a position below 0) gets O = 0, LSE = -inf.
+ *
+ * q, o   device, dtype [nseq, rows, Hq, D] contiguous; lse fp32 [nseq, rows, Hq] or NULL.
+ *        The rows' own keys must be in the cache (append first).
+ * cache  as above, read only; keys a row does not see may hold anything
+ * workspace  device scratch of at least sdp_fwd_cache4_workspace_bytes, 16-byte aligned, not
+ *        overlapping the other buffers and not shared with a call that may overlap on
+ *        the GPU (two graphs replayed at once need two); its contents do not matter
+ *        before and are unspecified after.
+ * Scores, weights and sums in fp32; the products take the 4-bit codes as they are and the
+ * queries and weights in 16 bits (the weights as two bf16 parts). The same call gives the
+ * same bits. A bad length leaves that sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a
+ * page outside the pool leaves them unspecified (SDP_ERR_BAD_PAGES), a wait that runs out
+ * all rows (SDP_ERR_DEVICE_TIMEOUT). Two kernels are enqueued on `stream`. The workspace
+ * size depends on the current device; a negative value is a status code.
+ */
+long long sdp_fwd_cache4_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype);
+int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, const void *v_codes, const void *v_scales,
+                   int num_pages, int page_size, const int *block_table, long long table_stride, int max_pages,
+                   const int *cache_lens, void *o, float *lse, int nseq, int rows, int Hq, int Hkv, int D, float scale,
+                   int dtype, int window, int sinks, void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/*
  * sdp_poll_status — synchronise `stream`, then read and clear the current
  * device's status word. Returns SDP_OK, SDP_ERR_DEVICE_TIMEOUT (a kernel
  * abandoned a wait after the timeout and returned without writing its
