@@ -1,5 +1,5 @@
 // Entry points of the attention over the 4-bit paged cache (cache4_attn.cuh): checks, the launch
-// shape and the dispatch on (head dim, dtype, columns a CTA).
+// shape and the dispatch on (head dim, dtype, columns a warp).
 #include <cmath>
 
 #include "cache4_attn.cuh"
@@ -10,8 +10,8 @@ namespace {
 constexpr int kMaxRows = 32;
 
 struct Shape {
-    bool wide;  // 16 columns a CTA, else 8
-    int chunks, ctas;
+    bool wide;  // 16 columns a warp, else 8
+    int chunks, sms, part_cols;
     long long workspace_bytes;
 };
 
@@ -35,9 +35,14 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, Shape *sh)
     const int rc = sdp::current_device(&dev, &sms);
     if (rc != SDP_OK)
         return rc;
-    sh->ctas = sms;
-    // two parts a CTA: the problem it continues and the one it begins
-    sh->workspace_bytes = 2LL * sh->ctas * (sh->wide ? 16 : 8) * (D + 2) * 4;
+    sh->sms = sms;
+    const int most = sh->wide ? 16 : 8;
+    sh->part_cols = columns < most ? static_cast<int>(columns) : most;
+    // two parts a warp: the problem it continues and the one it begins
+    const int warps = D == 128 ? (sh->wide ? sdp::c4::Plan<128, 2>::WARPS : sdp::c4::Plan<128, 1>::WARPS)
+                               : (sh->wide ? sdp::c4::Plan<256, 2>::WARPS : sdp::c4::Plan<256, 1>::WARPS);
+    sh->workspace_bytes = 2LL * sms * warps * 4 *
+                          (D == 128 ? sdp::c4::part_floats<128>(sh->part_cols) : sdp::c4::part_floats<256>(sh->part_cols));
     return SDP_OK;
 }
 
@@ -109,14 +114,14 @@ extern "C" int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_
     p.window = window;
     p.sinks = sinks;
     p.chunks = sh.chunks;
-    p.ctas = sh.ctas;
+    p.part_cols = sh.part_cols;
     p.no_copies = sdp::debug_flags() & 1;
     p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (D == 128)
-        e = dtype == SDP_BF16 ? sdp::cache4_attn_d128_bf16(p, sh.wide, st) : sdp::cache4_attn_d128_fp16(p, sh.wide, st);
+        e = dtype == SDP_BF16 ? sdp::cache4_attn_d128_bf16(p, sh.wide, sh.sms, st) : sdp::cache4_attn_d128_fp16(p, sh.wide, sh.sms, st);
     else
-        e = dtype == SDP_BF16 ? sdp::cache4_attn_d256_bf16(p, sh.wide, st) : sdp::cache4_attn_d256_fp16(p, sh.wide, st);
+        e = dtype == SDP_BF16 ? sdp::cache4_attn_d256_bf16(p, sh.wide, sh.sms, st) : sdp::cache4_attn_d256_fp16(p, sh.wide, sh.sms, st);
     return e == cudaSuccess ? SDP_OK : sdp::record_cuda_error(e);
 }

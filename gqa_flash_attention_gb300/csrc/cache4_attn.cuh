@@ -25,16 +25,20 @@
 //   few columns fill the n side. p turns from S's layout (token rows) to P's (column rows) by
 //   movmatrix on the two halves of its 32 bits.
 //
-// Each warp streams 32-token tiles through a ring of its own (bulk copies of the codes' and scales'
-// contiguous runs, NSTAGE tiles in flight, one mbarrier a stage; no barrier with other warps) and
-// keeps its own running maximum, sum and O in registers. The maximum moves only when a score
-// exceeds it by more than 8 (base 2), found by a vote, so most tiles need no reduction.
+//   The bias terms of a score come from one more MMA, whose A operand is the (s, b) words as they lie
+//   in memory and whose B operand holds the group sums of q (times -128 for s in bf16) in bf16 parts.
 //
-// Work split: all sequences' tiles are numbered sequence by sequence, KV head by KV head, and cut
-// into equal runs, one a CTA (the lengths are on the device, so each CTA finds its run from them);
-// a run's tiles of one (sequence, KV head) go round the CTA's warps and their states are joined
-// through shared memory. A problem that lies in one CTA's run is written directly; the parts of
-// the others go to the workspace in fp32 and cache4_merge_kernel joins them in a fixed order.
+// Work split: all sequences' tiles of 32 tokens are numbered sequence by sequence, KV head by KV
+// head (each problem with OVERHEAD positions more for its start), and cut into equal runs, one a
+// warp: the lengths are on the device, so each warp finds its run from them. Warps share nothing:
+// each streams its K and V tiles through a ring of its own (bulk copies of the codes' and scales'
+// contiguous runs, one mbarrier a slot), keeps its own running maximum, sum and O in registers, and
+// so ragged batches of short sequences keep every warp busy. (With a CTA's warps going round one
+// problem's tiles and joining through shared memory, the 64 ragged sequences took 150 us: CTAs with
+// many short problems ran twice as long as the others.) The maximum moves only when a score exceeds
+// it by more than 8 (base 2), found by a vote, so most tiles need no reduction. A problem that lies
+// in one run is written directly; the parts of the others go to the workspace in fp32 and
+// cache4_merge_kernel joins them in a fixed order.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -63,16 +67,17 @@ struct Cache4AttnParams {
     int nseq, n, Hq, Hkv, G;
     int window, sinks;  // window 0: every key
     int chunks;         // column chunks of 8 * NT
-    int ctas;           // CTAs that share the tiles (the merge sees the same number)
+    int runs;           // warps that share the tiles (the merge sees the same number)
+    int part_cols;      // columns of a part in the workspace: the live ones of a chunk
     int no_copies;      // test hook: no copy is issued, every wait runs out
     float c;            // scale * log2(e)
 };
 
 namespace c4 {
 
-constexpr int TILE = 32;  // tokens a warp step
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
+constexpr int TILE = 32;     // tokens a warp step
+constexpr int OVERHEAD = 1;  // tiles that a problem's start and end cost as much as
+constexpr int MERGE_WARPS = 8;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float RESCALE = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -102,96 +107,48 @@ __device__ __forceinline__ Span span_of(const Cache4AttnParams &p, int s)
     return r;
 }
 
-// Block-wide: the number of tiles of all problems (returned), and where the one numbered at(total)
-// lies: its sequence and its place among the sequence's tiles. scratch: WARPS + 2 words.
-template <class At>
-__device__ __forceinline__ long long find_place(const Cache4AttnParams &p, int per_tile, long long *scratch, At &&at,
-                                                int *s_out, long long *off_out)
+// Positions of one problem of a sequence, and of all its problems.
+__device__ __forceinline__ long long problem_length(const Span &sp) { return sp.count > 0 ? sp.count + OVERHEAD : 0; }
+
+// Runs with work: every one of them has at least a position.
+__device__ __forceinline__ int busy_runs(const Cache4AttnParams &p, long long total)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (p.nseq + THREADS - 1) / THREADS;
-    const long long first = static_cast<long long>(tid) * per;
-    const int s0 = static_cast<int>(min(static_cast<long long>(p.nseq), first));
-    const int s1 = static_cast<int>(min(static_cast<long long>(p.nseq), first + per));
-    long long sum = 0;
-    for (int s = s0; s < s1; ++s)
-        sum += span_of(p, s).count;
-    sum *= per_tile;
-    long long incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long x = __shfl_up_sync(FULL, incl, d);
-        if (lane >= d)
-            incl += x;
-    }
-    if (lane == 31)
-        scratch[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp)
-            before += scratch[w];
-        total += scratch[w];
-    }
-    incl += before;
-    long long excl = incl - sum;
-    const long long x = at(total);
-    if (x >= excl && x < incl) {
-        for (int s = s0; s < s1; ++s) {
-            const long long n = static_cast<long long>(span_of(p, s).count) * per_tile;
-            if (x < excl + n) {
-                scratch[WARPS] = s;
-                scratch[WARPS + 1] = x - excl;
-                break;
-            }
-            excl += n;
-        }
-    }
-    __syncthreads();
-    *s_out = static_cast<int>(scratch[WARPS]);
-    *off_out = scratch[WARPS + 1];
-    return total;
+    return total < p.runs ? static_cast<int>(total) : p.runs;
 }
 
-// First tile of CTA i's run.
+// First position of run i.
 __device__ __forceinline__ long long run_start(long long total, int i, int n) { return total * i / n; }
 
-// CTAs with work: every one of them has at least a tile.
-__device__ __forceinline__ int busy_ctas(const Cache4AttnParams &p, long long total)
+// Floats of one part in the workspace: O [columns][D], then m and l of each column, in all a
+// multiple of 4 (O is stored 16 bytes at a time) whatever the number of columns.
+template <int D>
+__host__ __device__ constexpr long long part_floats(int cols)
 {
-    return total < p.ctas ? static_cast<int>(total) : p.ctas;
+    return static_cast<long long>(cols) * (D + 4);
 }
 
-// Floats of one part in the workspace: O [columns][D], then m and l of each column.
+// Warps a CTA and ring slots a warp, by the registers and the shared memory that are left: O alone
+// takes D / 16 * NT * 4 registers a thread.
 template <int D, int NT>
-__host__ __device__ constexpr int part_floats()
-{
-    return 8 * NT * (D + 2);
-}
-
-template <int D, int NT>
-struct Smem {
+struct Plan {
     static constexpr int GQ = D / kCacheGroup;
+    static constexpr int WARPS = D == 128 ? (NT == 1 ? 16 : 12) : (NT == 1 ? 12 : 8);
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int COLS = 8 * NT;
     static constexpr int CODE = TILE * D / 2;    // bytes of a tile's K (or V) codes
     static constexpr int SCALE = TILE * GQ * 4;  // and of its scales
-    static constexpr int STAGE = 2 * (CODE + SCALE);
-    static constexpr int NSTAGE = D == 128 ? 4 : 2;
-    static constexpr int COLS = 8 * NT;
-    static constexpr int O_SLOT = COLS * D * 4;
-    static constexpr int O_SLOTS = WARPS / 2;
-    static constexpr int QF = (D / 16) * NT * 32 * 8;
-    static constexpr int RING = 0;
-    static constexpr int O_BUF = RING + WARPS * NSTAGE * STAGE;
-    static constexpr int Q_FRAG = O_BUF + O_SLOTS * O_SLOT;
-    static constexpr int QSUM = Q_FRAG + QF;         // [GQ][COLS] floats
-    static constexpr int ML = QSUM + GQ * COLS * 4;  // [2][WARPS][COLS] floats
-    static constexpr int SCRATCH = ML + 2 * WARPS * COLS * 4;
-    static constexpr int BARS = SCRATCH + 8 * (WARPS + 4);
-    static constexpr int FLAG = BARS + 8 * WARPS * NSTAGE;
-    static constexpr int BYTES = FLAG + 16;
+    static constexpr int SLOT = CODE + SCALE;
+    static constexpr int NSLOT = D == 128 ? (NT == 1 ? 5 : 6) : (NT == 1 ? 3 : 4);
+    static constexpr int KSTEPS = D / 16;
+    // bf16 parts of a group's sum of q: three where s is multiplied by -128 times it
+    static constexpr int BIAS_STEPS = GQ == 2 ? 1 : 2;
+    static constexpr int QF = (KSTEPS + BIAS_STEPS) * NT * 32 * 8;  // B fragments of a warp
+    static constexpr int Q_FRAG = WARPS * NSLOT * SLOT;
+    static constexpr int PREFIX = Q_FRAG + WARPS * QF;  // THREADS + WARPS long longs
+    static constexpr int BARS = PREFIX + 8 * (THREADS + WARPS);
+    static constexpr int BYTES = BARS + 8 * WARPS * NSLOT;
     static_assert(BYTES <= 227 * 1024, "shared memory");
-    static_assert(STAGE % 128 == 0 && O_BUF % 16 == 0 && Q_FRAG % 16 == 0 && SCRATCH % 8 == 0, "alignment");
+    static_assert(SLOT % 128 == 0 && Q_FRAG % 16 == 0 && PREFIX % 8 == 0, "alignment");
 };
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -254,43 +211,39 @@ __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes)
                  : "memory");
 }
 
-// A walk over a CTA's run, segment by segment (the run's tiles of one problem).
+// A walk over a run, segment by segment (the run's tiles of one problem). Segments without a tile
+// (the run ends inside a problem's start) are passed over.
 struct Walk {
     Span sp;
     int s, u;             // sequence; problem in it: KV head * chunks + chunk
     int e0, e1;           // tiles [e0, e1) of the problem
-    long long off, left;  // position in the sequence's tiles, tiles left in the run
-    __device__ __forceinline__ void segment(const Cache4AttnParams &p)
+    long long off, left;  // position in the sequence's problems, positions left in the run
+    __device__ __forceinline__ void find(const Cache4AttnParams &p)
     {
-        // empty sequences are passed over; `left` counts tiles that exist, so one follows
-        while (off >= static_cast<long long>(sp.count) * p.Hkv * p.chunks) {
-            off = 0;
-            sp = span_of(p, ++s);
+        while (left > 0) {
+            const long long len = problem_length(sp);
+            if (off >= len * p.Hkv * p.chunks) {  // `left` counts positions that exist: a sequence follows
+                off -= len * p.Hkv * p.chunks;
+                sp = span_of(p, ++s);
+                continue;
+            }
+            u = static_cast<int>(off / len);
+            const long long in = off - u * len, take = min(left, len - in);
+            e0 = static_cast<int>(max(0ll, in - OVERHEAD));
+            e1 = static_cast<int>(in + take - OVERHEAD);
+            off += take;
+            left -= take;
+            if (e1 > e0)
+                return;
         }
-        u = static_cast<int>(off / sp.count);
-        e0 = static_cast<int>(off - static_cast<long long>(u) * sp.count);
-        e1 = static_cast<int>(min(static_cast<long long>(sp.count), e0 + left));
+        e0 = e1 = 0;
+        s = -1;
     }
-    __device__ __forceinline__ void start(const Cache4AttnParams &p, int s_, long long off_, long long left_)
-    {
-        s = s_;
-        off = off_;
-        left = left_;
-        sp = span_of(p, s);
-        if (left > 0)
-            segment(p);
-    }
-    __device__ __forceinline__ void next(const Cache4AttnParams &p)
-    {
-        off += e1 - e0;
-        left -= e1 - e0;
-        if (left > 0)
-            segment(p);
-    }
+    __device__ __forceinline__ bool done() const { return s < 0; }
 };
 
 // Waits up to the limit for the phase of `bar`; false when it ran out.
-static __device__ __noinline__ bool wait_stage_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
+static __device__ __noinline__ bool wait_slot_slow(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
 {
     const uint64_t t0 = ptx::globaltimer_ns();
     while (!ptx::mbar_try_wait(bar, parity))
@@ -299,156 +252,23 @@ static __device__ __noinline__ bool wait_stage_slow(uint32_t bar, uint32_t parit
     return true;
 }
 
-__device__ __forceinline__ bool wait_stage(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
+__device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
 {
-    return ptx::mbar_try_wait(bar, parity) || wait_stage_slow(bar, parity, timeout_ns);
+    return ptx::mbar_try_wait(bar, parity) || wait_slot_slow(bar, parity, timeout_ns);
 }
 
 }  // namespace c4
 
+// One tile's scores to weights to O (see the top of the file). MASKED: some column does not see
+// some key of the tile, or the tile ends past the sequence.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(c4::THREADS, 1) cache4_attn_kernel(const Cache4AttnParams p)
-{
-    using namespace c4;
-    using M = Smem<D, NT>;
-    constexpr int GQ = M::GQ, COLS = M::COLS;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t sbase = ptx::smem_addr(smem);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row8 = lane >> 2, quad = lane & 3;  // an MMA fragment's row (or column n) and place in it
-    volatile int *failed = reinterpret_cast<volatile int *>(smem + M::FLAG);
-    long long *scratch = reinterpret_cast<long long *>(smem + M::SCRATCH);
-    float *qsum = reinterpret_cast<float *>(smem + M::QSUM);
-    float *m_all = reinterpret_cast<float *>(smem + M::ML), *l_all = m_all + WARPS * COLS;
-    const uint32_t ring = sbase + M::RING + warp * M::NSTAGE * M::STAGE;
-    const uint8_t *ring_p = smem + M::RING + warp * M::NSTAGE * M::STAGE;
-    const uint32_t bars = sbase + M::BARS + 8 * warp * M::NSTAGE;
+struct Tile {
+    using P = c4::Plan<D, NT>;
+    static constexpr int GQ = P::GQ;
+    float o[D / 16][NT][4], m[NT][2], l[NT][2], corr[NT][GQ];
 
-    if (tid == 0)
-        *failed = 0;
-    if (lane == 0) {
-        for (int i = 0; i < M::NSTAGE; ++i)
-            ptx::mbar_init(bars + 8 * i, 1);
-        ptx::fence_barrier_init();
-    }
-    // where this CTA's run of tiles starts
-    int s_first = 0;
-    long long off_first = 0;
-    const int per_tile = p.Hkv * p.chunks;
-    const long long total = find_place(
-        p, per_tile, scratch,
-        [&](long long t) -> long long {
-            const int n = busy_ctas(p, t);
-            return static_cast<int>(blockIdx.x) < n ? run_start(t, blockIdx.x, n) : -1;
-        },
-        &s_first, &off_first);
-    const int busy = busy_ctas(p, total);
-    if (static_cast<int>(blockIdx.x) >= busy)
-        return;
-    const long long run0 = run_start(total, blockIdx.x, busy);
-    const long long run_len = run_start(total, blockIdx.x + 1, busy) - run0;
-
-    // ---- copies: tile e of the walk's segment into stage `st`
-    auto issue = [&](const Walk &w, int e, int st) {
-        if (p.no_copies)
-            return;
-        const uint32_t bar = bars + 8 * st;
-        if (lane == 0)
-            expect_tx(bar, M::STAGE);
-        __syncwarp();
-        const int g = w.u / p.chunks;
-        const int tok0 = w.sp.tile(e) * TILE;
-        // a 32-token tile lies in one page where the page size is a multiple of 32, else in halves
-        const int pieces = (p.page_size & 31) == 0 ? 1 : 2;
-        if (lane < 4 * pieces) {
-            const int part = lane & 3, half = lane >> 2;  // K codes, K scales, V codes, V scales
-            const int tokens = TILE / pieces;
-            const int tok = tok0 + half * tokens;
-            const int slot = tok / p.page_size;
-            // a half behind the last page is copied from that page and masked
-            const int last = (w.sp.len - 1) / p.page_size;
-            int id = __ldg(p.table + w.s * p.table_stride + min(slot, last));
-            if (id < 0 || id >= p.num_pages) {
-                atomicCAS(p.status, 0u, kBadPages);
-                id = 0;
-            }
-            const long long row = (static_cast<long long>(id) * p.Hkv + g) * p.page_size + (tok - slot * p.page_size);
-            const uint32_t base = ring + st * M::STAGE + (part >= 2 ? M::CODE + M::SCALE : 0);
-            if (part & 1)
-                bulk_load(base + M::CODE + half * tokens * GQ * 4, (part == 1 ? p.k_scales : p.v_scales) + row * GQ,
-                          tokens * GQ * 4, bar);
-            else
-                bulk_load(base + half * tokens * (D / 2), (part == 0 ? p.k_codes : p.v_codes) + row * (D / 2),
-                          tokens * (D / 2), bar);
-        }
-    };
-
-    Walk ahead;  // the copies' place in the run
-    ahead.start(p, s_first, off_first, run_len);
-    int ae = ahead.e0 + warp;  // this warp's next tile to copy
-    auto next_ahead = [&]() -> bool {  // moves to a segment with a tile of this warp's
-        while (ahead.left > 0 && ae >= ahead.e1) {
-            ahead.next(p);
-            ae = ahead.e0 + warp;
-        }
-        return ahead.left > 0;
-    };
-    int in_flight = 0;
-    for (; in_flight < M::NSTAGE && next_ahead(); ++in_flight) {
-        issue(ahead, ae, in_flight);
-        ae += WARPS;
-    }
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    auto step_stage = [&]() {
-        if (++stage == M::NSTAGE) {
-            stage = 0;
-            phase ^= 1u;
-        }
-    };
-
-    Walk w;
-    w.start(p, s_first, off_first, run_len);
-    while (w.left > 0) {
-        const int g = w.u / p.chunks, chunk = w.u - g * p.chunks;
-        const int r_base = chunk * COLS, R = p.n * p.G;
-        auto row_of = [&](int r) {  // the (sequence, row, head) row of column r in q, o and lse
-            return (static_cast<long long>(w.s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
-        };
-        // ---- the queries as B fragments, and their sums over each group
-        {
-            uint2 *qf = reinterpret_cast<uint2 *>(smem + M::Q_FRAG);
-            for (int i = tid; i < (D / 16) * NT * 32; i += THREADS) {
-                const int ks = i / (NT * 32), nt = (i / 32) % NT, l = i & 31;
-                const int r = r_base + nt * 8 + (l >> 2);
-                uint2 f = make_uint2(0u, 0u);
-                if (r < R) {
-                    const int c0 = (ks / 4) * kCacheGroup + (l & 3) * 16 + ((ks & 3) / 2) * 8 + 2 * (ks & 1);
-                    const uint16_t *src = p.q + row_of(r) * D + c0;
-                    f.x = __ldg(src) | (static_cast<uint32_t>(__ldg(src + 4)) << 16);
-                    f.y = __ldg(src + 1) | (static_cast<uint32_t>(__ldg(src + 5)) << 16);
-                }
-                qf[i] = f;
-            }
-            for (int i = warp; i < COLS * GQ; i += WARPS) {
-                const int col = i / GQ, gq = i - col * GQ, r = r_base + col;
-                float v = 0.f;
-                if (r < R) {
-                    const float2 x = unpack16<BF16>(__ldg(
-                        reinterpret_cast<const uint32_t *>(p.q + row_of(r) * D + gq * kCacheGroup + 2 * lane)));
-                    v = x.x + x.y;
-                }
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    v += __shfl_xor_sync(FULL, v, o);
-                if (lane == 0)
-                    qsum[gq * COLS + col] = v;
-            }
-        }
-        __syncthreads();
-
-        float o[D / 16][NT][4], m[NT][2], l[NT][2], corr[NT][GQ];
+    __device__ __forceinline__ void clear()
+    {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
@@ -460,381 +280,538 @@ __global__ void __launch_bounds__(c4::THREADS, 1) cache4_attn_kernel(const Cache
             for (int i = 0; i < D / 16; ++i)
                 o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
         }
-        // positions of the chunk's first and last column
-        const int pos_lo = w.sp.len - p.n + r_base / p.G;
-        const int pos_hi = w.sp.len - p.n + min(p.n - 1, (r_base + COLS - 1) / p.G);
+    }
 
-        for (int e = w.e0 + warp; e < w.e1; e += WARPS) {
-            if (ok && !__all_sync(FULL, wait_stage(bars + 8 * stage, phase, p.timeout_ns))) {
-                ok = false;
-                *failed = 1;
-                if (lane == 0)
-                    atomicCAS(p.status, 0u, kSlotNeverFilled | (blockIdx.x << 8));
-                // this warp's copies land (waited for with a limit again) before the CTA may exit
-                for (; in_flight > 0 && !p.no_copies; --in_flight) {
-                    wait_stage(bars + 8 * stage, phase, p.timeout_ns);
-                    step_stage();
-                }
-            }
-            if (!ok)
-                continue;
-            const uint8_t *kc = ring_p + stage * M::STAGE, *vc = kc + M::CODE + M::SCALE;
-            const uint32_t *ksc = reinterpret_cast<const uint32_t *>(kc + M::CODE);
-            const uint32_t *vsc = reinterpret_cast<const uint32_t *>(vc + M::CODE);
-            const uint2 *qf = reinterpret_cast<const uint2 *>(smem + M::Q_FRAG);
-            const int tok0 = w.sp.tile(e) * TILE;
-            const bool whole = tok0 + TILE - 1 <= pos_lo &&
-                               (p.window == 0 || tok0 > pos_hi - p.window || tok0 + TILE <= p.sinks);
-            // MMA row r (and r + 8) of a 16-token chunk is token ta (and ta + 8), so that P's
-            // rows 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 are tokens quad + {0, 4, 8, 12}
-            const int ta = (row8 >> 1) + ((row8 & 1) << 2);
-
-            // ---- scores
-            float s[2][NT][4];
+    // s = scores in base 2 of the K tile at kc: rows ta, ta + 8 of each 16-token chunk, columns
+    // 2 quad, 2 quad + 1.
+    __device__ __forceinline__ void scores(float (&s)[2][NT][4], const uint8_t *kc, const uint2 *qf, int lane, float c)
+    {
+        using namespace c4;
+        const int row8 = lane >> 2, quad = lane & 3;
+        // MMA row r (and r + 8) of a 16-token chunk is token ta (and ta + 8), so that P's
+        // rows 2 quad, 2 quad + 1, 2 quad + 8, 2 quad + 9 are tokens quad + {0, 4, 8, 12}
+        const int ta = (row8 >> 1) + ((row8 & 1) << 2);
+        const uint32_t *ksc = reinterpret_cast<const uint32_t *>(kc + P::CODE);
+        // the bias terms
 #pragma unroll
-            for (int mc = 0; mc < 2; ++mc)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    s[mc][nt][0] = s[mc][nt][1] = s[mc][nt][2] = s[mc][nt][3] = 0.f;
-#pragma unroll
-            for (int gq = 0; gq < GQ; ++gq) {
-                float acc[2][NT][4];
-                uint2 wa[2], wb[2];
-#pragma unroll
-                for (int mc = 0; mc < 2; ++mc) {
-                    const uint8_t *at = kc + (mc * 16 + ta) * (D / 2) + gq * 32 + quad * 8;
-                    wa[mc] = *reinterpret_cast<const uint2 *>(at);
-                    wb[mc] = *reinterpret_cast<const uint2 *>(at + 8 * (D / 2));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        acc[mc][nt][0] = acc[mc][nt][1] = acc[mc][nt][2] = acc[mc][nt][3] = 0.f;
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint2 b[NT];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        b[nt] = qf[((gq * 4 + j) * NT + nt) * 32 + lane];
-#pragma unroll
-                    for (int mc = 0; mc < 2; ++mc) {
-                        const uint32_t x = j < 2 ? wa[mc].x : wa[mc].y, y = j < 2 ? wb[mc].x : wb[mc].y;
-                        constexpr uint32_t MAGIC = BF16 ? 0x43004300u : 0u;
-                        const int h = 2 * (j & 1);
-                        const uint32_t a0 = code_pair<MAGIC>(x, h), a1 = code_pair<MAGIC>(y, h);
-                        const uint32_t a2 = code_pair<MAGIC>(x, h + 1), a3 = code_pair<MAGIC>(y, h + 1);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if constexpr (BF16)
-                                mma_bf16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
-                            else
-                                mma_f16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int mc = 0; mc < 2; ++mc) {
-                    const uint32_t pa = ksc[(mc * 16 + ta) * GQ + gq], pb = ksc[(mc * 16 + ta + 8) * GQ + gq];
-                    float sa = scale_of(pa), ba = bias_of(pa), sb = scale_of(pb), bb = bias_of(pb);
-                    if constexpr (BF16) {
-                        ba = fmaf(-128.f, sa, ba);
-                        bb = fmaf(-128.f, sb, bb);
-                    } else {
-                        sa *= 16777216.f;  // 2^24
-                        sb *= 16777216.f;
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float2 qs = *reinterpret_cast<const float2 *>(qsum + gq * COLS + nt * 8 + 2 * quad);
-                        float(&d)[4] = s[mc][nt];
-                        d[0] = fmaf(sa, acc[mc][nt][0], fmaf(ba, qs.x, d[0]));
-                        d[1] = fmaf(sa, acc[mc][nt][1], fmaf(ba, qs.y, d[1]));
-                        d[2] = fmaf(sb, acc[mc][nt][2], fmaf(bb, qs.x, d[2]));
-                        d[3] = fmaf(sb, acc[mc][nt][3], fmaf(bb, qs.y, d[3]));
-                    }
-                }
-            }
-            // ---- base-2 scores; keys a column does not see drop out
+        for (int mc = 0; mc < 2; ++mc) {
+            const uint32_t wa = ksc[(mc * 16 + ta) * GQ + quad % GQ], wb = ksc[(mc * 16 + ta + 8) * GQ + quad % GQ];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+                s[mc][nt][0] = s[mc][nt][1] = s[mc][nt][2] = s[mc][nt][3] = 0.f;
 #pragma unroll
-                for (int mc = 0; mc < 2; ++mc)
+                for (int st = 0; st < P::BIAS_STEPS; ++st) {
+                    const uint2 b = qf[((P::KSTEPS + st) * NT + nt) * 32 + lane];
+                    mma_bf16(s[mc][nt], wa, wb, wa, wb, b.x, b.y);
+                }
+            }
+        }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        s[mc][nt][i] *= p.c;
-                if (!whole) {
+        for (int gq = 0; gq < GQ; ++gq) {
+            float acc[2][NT][4];
+            uint2 wa[2], wb[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r_base + nt * 8 + 2 * quad + i;
-                        const int at = w.sp.len - p.n + min(p.n - 1, r / p.G);
-                        const int from = p.window > 0 ? at - p.window : -1;  // keys past it are in the window
+            for (int mc = 0; mc < 2; ++mc) {
+                const uint8_t *at = kc + (mc * 16 + ta) * (D / 2) + gq * 32 + quad * 8;
+                wa[mc] = *reinterpret_cast<const uint2 *>(at);
+                wb[mc] = *reinterpret_cast<const uint2 *>(at + 8 * (D / 2));
 #pragma unroll
-                        for (int mc = 0; mc < 2; ++mc)
+                for (int nt = 0; nt < NT; ++nt)
+                    acc[mc][nt][0] = acc[mc][nt][1] = acc[mc][nt][2] = acc[mc][nt][3] = 0.f;
+            }
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int j = tok0 + mc * 16 + ta + 8 * x;
-                                if (j > at || (j <= from && j >= p.sinks))
-                                    s[mc][nt][i + 2 * x] = -INFINITY;
-                            }
+            for (int j = 0; j < 4; ++j) {
+                uint2 b[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    b[nt] = qf[((gq * 4 + j) * NT + nt) * 32 + lane];
+#pragma unroll
+                for (int mc = 0; mc < 2; ++mc) {
+                    const uint32_t x = j < 2 ? wa[mc].x : wa[mc].y, y = j < 2 ? wb[mc].x : wb[mc].y;
+                    constexpr uint32_t MAGIC = BF16 ? 0x43004300u : 0u;
+                    const int h = 2 * (j & 1);
+                    const uint32_t a0 = code_pair<MAGIC>(x, h), a1 = code_pair<MAGIC>(y, h);
+                    const uint32_t a2 = code_pair<MAGIC>(x, h + 1), a3 = code_pair<MAGIC>(y, h + 1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if constexpr (BF16)
+                            mma_bf16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
+                        else
+                            mma_f16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
                     }
                 }
             }
-            // ---- running maximum: moved when some score is more than RESCALE above it
-            bool over = false;
+#pragma unroll
+            for (int mc = 0; mc < 2; ++mc) {
+                float sa = scale_of(ksc[(mc * 16 + ta) * GQ + gq]), sb = scale_of(ksc[(mc * 16 + ta + 8) * GQ + gq]);
+                if constexpr (!BF16) {
+                    sa *= 16777216.f;  // 2^24
+                    sb *= 16777216.f;
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    s[mc][nt][0] = fmaf(sa, acc[mc][nt][0], s[mc][nt][0]);
+                    s[mc][nt][1] = fmaf(sa, acc[mc][nt][1], s[mc][nt][1]);
+                    s[mc][nt][2] = fmaf(sb, acc[mc][nt][2], s[mc][nt][2]);
+                    s[mc][nt][3] = fmaf(sb, acc[mc][nt][3], s[mc][nt][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int mc = 0; mc < 2; ++mc)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    over |= fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2])) >
-                            m[nt][i] + RESCALE;
-            if (__any_sync(FULL, over)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float a[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float x = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2]));
-#pragma unroll
-                        for (int off = 4; off < 32; off <<= 1)
-                            x = fmaxf(x, __shfl_xor_sync(FULL, x, off));
-                        const float next = fmaxf(m[nt][i], x);
-                        a[i] = next == m[nt][i] ? 1.f : ptx::ex2(m[nt][i] - next);
-                        m[nt][i] = next;
-                        l[nt][i] *= a[i];
-                    }
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        o[i][nt][0] *= a[0];
-                        o[i][nt][1] *= a[1];
-                        o[i][nt][2] *= a[0];
-                        o[i][nt][3] *= a[1];
-                    }
-                    // corr belongs to column row8, whose factor lanes with quad = row8 / 2 hold
-                    const float x0 = __shfl_sync(FULL, a[0], row8 >> 1), x1 = __shfl_sync(FULL, a[1], row8 >> 1);
-                    const float f = (row8 & 1) ? x1 : x0;
-#pragma unroll
-                    for (int gq = 0; gq < GQ; ++gq)
-                        corr[nt][gq] *= f;
-                }
-            }
-            // ---- weights, and their turn into P's layout
-            float pb[2][NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-                const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-#pragma unroll
-                for (int mc = 0; mc < 2; ++mc) {
-                    const float p0 = ptx::ex2(s[mc][nt][0] - m0), p1 = ptx::ex2(s[mc][nt][1] - m1);
-                    const float p2 = ptx::ex2(s[mc][nt][2] - m0), p3 = ptx::ex2(s[mc][nt][3] - m1);
-                    l[nt][0] += p0 + p2;
-                    l[nt][1] += p1 + p3;
-                    const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-                    const uint32_t u2 = __float_as_uint(p2), u3 = __float_as_uint(p3);
-                    const uint32_t l0 = movmatrix(__byte_perm(u0, u1, 0x5410));
-                    const uint32_t h0 = movmatrix(__byte_perm(u0, u1, 0x7632));
-                    const uint32_t l1 = movmatrix(__byte_perm(u2, u3, 0x5410));
-                    const uint32_t h1 = movmatrix(__byte_perm(u2, u3, 0x7632));
-                    pb[mc][nt][0] = __uint_as_float(__byte_perm(l0, h0, 0x5410));
-                    pb[mc][nt][1] = __uint_as_float(__byte_perm(l0, h0, 0x7632));
-                    pb[mc][nt][2] = __uint_as_float(__byte_perm(l1, h1, 0x5410));
-                    pb[mc][nt][3] = __uint_as_float(__byte_perm(l1, h1, 0x7632));
-                }
-            }
-            // ---- O += V^T P
-#pragma unroll
-            for (int mc = 0; mc < 2; ++mc) {
-#pragma unroll
-                for (int gq = 0; gq < GQ; ++gq) {
-                    uint32_t v[4];
-                    float sc[4], bi[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int t = mc * 16 + quad + 4 * i;
-                        v[i] = *reinterpret_cast<const uint32_t *>(vc + t * (D / 2) + gq * 32 + row8 * 4);
-                        const uint32_t pr = vsc[t * GQ + gq];
-                        sc[i] = scale_of(pr);
-                        bi[i] = fmaf(8.f, sc[i], bias_of(pr));
-                    }
-                    uint32_t hi[NT][2], lo[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float pi = pb[mc][nt][i];
-                            // a key that no column sees has weight 0, whatever its place in the pool holds
-                            const bool out = !whole && pi == 0.f;
-                            x[i] = out ? 0.f : pi * sc[i];
-                            corr[nt][gq] = out ? corr[nt][gq] : fmaf(pi, bi[i], corr[nt][gq]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            hi[nt][i] = pack16<true>(x[2 * i], x[2 * i + 1]);
-                            lo[nt][i] = pack16<true>(x[2 * i] - __uint_as_float(hi[nt][i] << 16),
-                                                     x[2 * i + 1] - __uint_as_float(hi[nt][i] & 0xffff0000u));
-                        }
-                    }
-                    // halves of the words: codes 0-3 of two tokens, codes 4-7 of two tokens
-                    const uint32_t x01 = __byte_perm(v[0], v[1], 0x5410), y01 = __byte_perm(v[0], v[1], 0x7632);
-                    const uint32_t x23 = __byte_perm(v[2], v[3], 0x5410), y23 = __byte_perm(v[2], v[3], 0x7632);
-#pragma unroll
-                    for (int mt = 0; mt < 4; ++mt) {
-                        const uint32_t w01 = mt < 2 ? x01 : y01, w23 = mt < 2 ? x23 : y23;
-                        const int h = 2 * (mt & 1);
-                        const uint32_t a0 = centred_pair(w01, h), a1 = centred_pair(w01, h + 1);
-                        const uint32_t a2 = centred_pair(w23, h), a3 = centred_pair(w23, h + 1);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                            mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
-                        }
-                    }
-                }
-            }
-            // ---- the stage is free: its next tile
-            __syncwarp();
-            if (next_ahead()) {
-                issue(ahead, ae, stage);
-                ae += WARPS;
-            } else {
-                --in_flight;
-            }
-            step_stage();
-        }
+                for (int i = 0; i < 4; ++i)
+                    s[mc][nt][i] *= c;
+    }
 
-        // ---- join the warps: maximum and sum of each column, then O
+    // Keys that a column does not see drop out: key tok0 + ... against positions first + r / G.
+    __device__ __forceinline__ void mask(float (&s)[2][NT][4], const Cache4AttnParams &p, int tok0, int first, int r_base,
+                                         int lane)
+    {
+        const int row8 = lane >> 2, quad = lane & 3, ta = (row8 >> 1) + ((row8 & 1) << 2);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
+                const int at = first + min(p.n - 1, (r_base + nt * 8 + 2 * quad + i) / p.G);
+                const int from = p.window > 0 ? at - p.window : -1;  // keys past it are in the window
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1)
-                    l[nt][i] += __shfl_xor_sync(FULL, l[nt][i], off);
-                if (row8 == 0) {
-                    m_all[warp * COLS + nt * 8 + 2 * quad + i] = m[nt][i];
-                    l_all[warp * COLS + nt * 8 + 2 * quad + i] = l[nt][i];
-                }
+                for (int mc = 0; mc < 2; ++mc)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int j = tok0 + mc * 16 + ta + 8 * x;
+                        if (j > at || (j <= from && j >= p.sinks))
+                            s[mc][nt][i + 2 * x] = -INFINITY;
+                    }
             }
-        __syncthreads();
-        const int parts = min(WARPS, w.e1 - w.e0);  // warps that had a tile
-        float *obuf = reinterpret_cast<float *>(smem + M::O_BUF);
-        if (warp < parts) {
+    }
+
+    // The running maximum moves when some score is more than RESCALE above it; then s becomes the
+    // weights in P's layout (rows quad + {0, 4, 8, 12} of each chunk, column row8).
+    __device__ __forceinline__ void weights(float (&s)[2][NT][4], int lane)
+    {
+        using namespace c4;
+        const int row8 = lane >> 2;
+        bool over = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                over |= fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2])) >
+                        m[nt][i] + RESCALE;
+        if (__any_sync(FULL, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float f[2], cg[GQ][2];
+                float a[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = -INFINITY;
-                    for (int x = 0; x < parts; ++x)
-                        mx = fmaxf(mx, m_all[x * COLS + nt * 8 + 2 * quad + i]);
-                    f[i] = m[nt][i] == -INFINITY ? 0.f : ptx::ex2(m[nt][i] - mx);
+                    float x = fmaxf(fmaxf(s[0][nt][i], s[0][nt][i + 2]), fmaxf(s[1][nt][i], s[1][nt][i + 2]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        x = fmaxf(x, __shfl_xor_sync(FULL, x, off));
+                    const float next = fmaxf(m[nt][i], x);
+                    a[i] = next == m[nt][i] ? 1.f : ptx::ex2(m[nt][i] - next);
+                    m[nt][i] = next;
+                    l[nt][i] *= a[i];
                 }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    o[i][nt][0] *= a[0];
+                    o[i][nt][1] *= a[1];
+                    o[i][nt][2] *= a[0];
+                    o[i][nt][3] *= a[1];
+                }
+                // corr belongs to column row8, whose factor lanes with quad = row8 / 2 hold
+                const float x0 = __shfl_sync(FULL, a[0], row8 >> 1), x1 = __shfl_sync(FULL, a[1], row8 >> 1);
+                const float f = (row8 & 1) ? x1 : x0;
+#pragma unroll
+                for (int gq = 0; gq < GQ; ++gq)
+                    corr[nt][gq] *= f;
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+            const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+#pragma unroll
+            for (int mc = 0; mc < 2; ++mc) {
+                const float p0 = ptx::ex2(s[mc][nt][0] - m0), p1 = ptx::ex2(s[mc][nt][1] - m1);
+                const float p2 = ptx::ex2(s[mc][nt][2] - m0), p3 = ptx::ex2(s[mc][nt][3] - m1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+                const uint32_t u2 = __float_as_uint(p2), u3 = __float_as_uint(p3);
+                const uint32_t l0 = movmatrix(__byte_perm(u0, u1, 0x5410));
+                const uint32_t h0 = movmatrix(__byte_perm(u0, u1, 0x7632));
+                const uint32_t l1 = movmatrix(__byte_perm(u2, u3, 0x5410));
+                const uint32_t h1 = movmatrix(__byte_perm(u2, u3, 0x7632));
+                s[mc][nt][0] = __uint_as_float(__byte_perm(l0, h0, 0x5410));
+                s[mc][nt][1] = __uint_as_float(__byte_perm(l0, h0, 0x7632));
+                s[mc][nt][2] = __uint_as_float(__byte_perm(l1, h1, 0x5410));
+                s[mc][nt][3] = __uint_as_float(__byte_perm(l1, h1, 0x7632));
+            }
+        }
+    }
+
+    // O += V^T P of the V tile at vc with the weights w. MASKED: a key that a column does not see has
+    // weight 0 there, whatever scale its place in the pool holds.
+    template <bool MASKED>
+    __device__ __forceinline__ void output(const float (&w)[2][NT][4], const uint8_t *vc, int lane)
+    {
+        using namespace c4;
+        const int row8 = lane >> 2, quad = lane & 3;
+        const uint32_t *vsc = reinterpret_cast<const uint32_t *>(vc + P::CODE);
+#pragma unroll
+        for (int mc = 0; mc < 2; ++mc) {
+#pragma unroll
+            for (int gq = 0; gq < GQ; ++gq) {
+                uint32_t v[4];
+                float sc[4], bi[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int t = mc * 16 + quad + 4 * i;
+                    v[i] = *reinterpret_cast<const uint32_t *>(vc + t * (D / 2) + gq * 32 + row8 * 4);
+                    const uint32_t pr = vsc[t * GQ + gq];
+                    sc[i] = scale_of(pr);
+                    bi[i] = fmaf(8.f, sc[i], bias_of(pr));
+                }
+                uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float pi = w[mc][nt][i];
+                        const bool out = MASKED && pi == 0.f;
+                        x[i] = out ? 0.f : pi * sc[i];
+                        corr[nt][gq] = out ? corr[nt][gq] : fmaf(pi, bi[i], corr[nt][gq]);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        hi[nt][i] = pack16<true>(x[2 * i], x[2 * i + 1]);
+                        lo[nt][i] = pack16<true>(x[2 * i] - __uint_as_float(hi[nt][i] << 16),
+                                                 x[2 * i + 1] - __uint_as_float(hi[nt][i] & 0xffff0000u));
+                    }
+                }
+                // halves of the words: codes 0-3 of two tokens, codes 4-7 of two tokens
+                const uint32_t x01 = __byte_perm(v[0], v[1], 0x5410), y01 = __byte_perm(v[0], v[1], 0x7632);
+                const uint32_t x23 = __byte_perm(v[2], v[3], 0x5410), y23 = __byte_perm(v[2], v[3], 0x7632);
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    const uint32_t w01 = mt < 2 ? x01 : y01, w23 = mt < 2 ? x23 : y23;
+                    const int h = 2 * (mt & 1);
+                    const uint32_t a0 = centred_pair(w01, h), a1 = centred_pair(w01, h + 1);
+                    const uint32_t a2 = centred_pair(w23, h), a3 = centred_pair(w23, h + 1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
+                        mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
+                    }
+                }
+            }
+        }
+    }
+};
+
+template <int D, bool BF16, int NT>
+__global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kernel(const Cache4AttnParams p)
+{
+    using namespace c4;
+    using P = Plan<D, NT>;
+    constexpr int GQ = P::GQ, WARPS = P::WARPS, THREADS = P::THREADS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row8 = lane >> 2, quad = lane & 3;  // an MMA fragment's row (or column n) and place in it
+    const uint32_t ring = sbase + warp * P::NSLOT * P::SLOT;
+    const uint8_t *ring_p = smem + warp * P::NSLOT * P::SLOT;
+    uint2 *qf = reinterpret_cast<uint2 *>(smem + P::Q_FRAG + warp * P::QF);
+    const uint32_t bars = sbase + P::BARS + 8 * warp * P::NSLOT;
+
+    if (lane == 0) {
+        for (int i = 0; i < P::NSLOT; ++i)
+            ptx::mbar_init(bars + 8 * i, 1);
+        ptx::fence_barrier_init();
+    }
+    // ---- where this warp's run starts: prefix sums of the sequences' positions, a few sequences a thread
+    Walk ahead;  // the copies' place in the run
+    {
+        long long *prefix = reinterpret_cast<long long *>(smem + P::PREFIX), *warp_sum = prefix + THREADS;
+        const int per_tile = p.Hkv * p.chunks;
+        const int per = (p.nseq + THREADS - 1) / THREADS;
+        const long long first = static_cast<long long>(tid) * per;
+        const int s0 = static_cast<int>(min(static_cast<long long>(p.nseq), first));
+        const int s1 = static_cast<int>(min(static_cast<long long>(p.nseq), first + per));
+        long long sum = 0;
+        for (int s = s0; s < s1; ++s)
+            sum += problem_length(span_of(p, s));
+        sum *= per_tile;
+        long long incl = sum;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long x = __shfl_up_sync(FULL, incl, d);
+            if (lane >= d)
+                incl += x;
+        }
+        prefix[tid] = incl - sum;  // within the warp
+        if (lane == 31)
+            warp_sum[warp] = incl;
+        __syncthreads();
+        long long total = 0;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w)
+            total += warp_sum[w];
+        const int busy = busy_runs(p, total);
+        // consecutive runs lie on different SMs, so that few runs use many
+        const int run = warp * gridDim.x + blockIdx.x;
+        if (run >= busy)
+            return;
+        const long long x = run_start(total, run, busy);
+        ahead.left = run_start(total, run + 1, busy) - x;
+        // the last thread whose sequences start at or before x
+        long long before = 0;
+        int w0 = 0;
+        while (before + warp_sum[w0] <= x)
+            before += warp_sum[w0++];
+        const unsigned at = __ballot_sync(FULL, before + prefix[w0 * 32 + lane] <= x);
+        const int owner = w0 * 32 + 31 - __clz(at);
+        ahead.off = x - before - prefix[owner];
+        ahead.s = owner * per;
+        ahead.sp = span_of(p, ahead.s);
+        ahead.find(p);  // passes over whole sequences where a thread has several
+    }
+    Walk w = ahead;
+
+    // ---- copies. A tile's K part, then its V part, go to the ring's next slot. The page id of the
+    // next tile is loaded a tile ahead, so that no copy waits for it.
+    const int pieces = (p.page_size & 31) == 0 ? 1 : 2;  // a 32-token tile lies in one page, or in halves
+    const int piece_tokens = TILE / pieces;
+    const int half = pieces == 1 ? 0 : (lane >> 1) & 1;  // lane: codes or scales (bit 0) of a piece (bit 1)
+    int ae = ahead.e0;                                   // the next tile to copy
+    int page_id = 0, page_off = 0;
+    auto look_up = [&]() {
+        if (ahead.done())
+            return;
+        const int tok = ahead.sp.tile(ae) * TILE + half * piece_tokens;
+        const int slot = tok / p.page_size;
+        page_off = tok - slot * p.page_size;
+        // a half behind the last page is copied from that page and masked
+        page_id = __ldg(p.table + ahead.s * p.table_stride + min(slot, (ahead.sp.len - 1) / p.page_size));
+    };
+    look_up();
+    bool is_v = false;  // the next part to copy
+    auto issue = [&](int slot) {
+        if (!p.no_copies) {
+            const uint32_t bar = bars + 8 * slot;
+            if (lane == 0)
+                expect_tx(bar, P::SLOT);
+            __syncwarp();
+            if (lane < 2 * pieces) {
+                int id = page_id;
+                if (id < 0 || id >= p.num_pages) {
+                    atomicCAS(p.status, 0u, kBadPages);
+                    id = 0;
+                }
+                const long long row =
+                    (static_cast<long long>(id) * p.Hkv + ahead.u / p.chunks) * p.page_size + page_off;
+                const uint32_t base = ring + slot * P::SLOT;
+                if (lane & 1)
+                    bulk_load(base + P::CODE + half * piece_tokens * GQ * 4, (is_v ? p.v_scales : p.k_scales) + row * GQ,
+                              piece_tokens * GQ * 4, bar);
+                else
+                    bulk_load(base + half * piece_tokens * (D / 2), (is_v ? p.v_codes : p.k_codes) + row * (D / 2),
+                              piece_tokens * (D / 2), bar);
+            }
+        }
+        if (is_v) {
+            if (++ae >= ahead.e1) {
+                ahead.find(p);
+                ae = ahead.e0;
+            }
+            look_up();
+        }
+        is_v = !is_v;
+    };
+    int in_flight = 0;
+    for (; in_flight < P::NSLOT && !ahead.done(); ++in_flight)
+        issue(in_flight);
+    int slot = 0;
+    uint32_t phase = 0;
+    auto step_slot = [&]() {
+        if (++slot == P::NSLOT) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    };
+    // the next part has landed; false (and the warp stops) when its wait ran out
+    auto landed = [&]() -> bool {
+        if (__all_sync(FULL, wait_slot(bars + 8 * slot, phase, p.timeout_ns)))
+            return true;
+        if (lane == 0)
+            atomicCAS(p.status, 0u, kSlotNeverFilled | (blockIdx.x << 8));
+        // this warp's copies land (waited for with a limit again) before the CTA may exit
+        for (; in_flight > 0 && !p.no_copies; --in_flight) {
+            wait_slot(bars + 8 * slot, phase, p.timeout_ns);
+            step_slot();
+        }
+        return false;
+    };
+    // the slot just read takes the next part
+    auto refill = [&]() {
+        __syncwarp();
+        if (!ahead.done())
+            issue(slot);
+        else
+            --in_flight;
+        step_slot();
+    };
+
+    const int run = warp * gridDim.x + blockIdx.x;
+    const int R = p.n * p.G;
+    Tile<D, BF16, NT> t;
+    for (; !w.done(); w.find(p)) {
+        const int g = w.u / p.chunks, r_base = (w.u - g * p.chunks) * P::COLS;
+        auto row_of = [&](int r) {  // the (sequence, row, head) row of column r in q, o and lse
+            return (static_cast<long long>(w.s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
+        };
+        // ---- the queries as B fragments: lane (column row8, quad) holds 16 channels of each group
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r_base + nt * 8 + row8;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (r < R ? row_of(r) : 0) * D) + quad * 2;
+            float sum[GQ];
+#pragma unroll
+            for (int gq = 0; gq < GQ; ++gq) {
+                uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+                if (r < R) {
+                    x[0] = __ldg(src + gq * 8);
+                    x[1] = __ldg(src + gq * 8 + 1);
+                }
+                float a = 0.f;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // channels (c, c + 4) pair up, as the codes of a word do
+                    qf[((gq * 4 + 2 * j) * NT + nt) * 32 + lane] =
+                        make_uint2(__byte_perm(x[j].x, x[j].z, 0x5410), __byte_perm(x[j].x, x[j].z, 0x7632));
+                    qf[((gq * 4 + 2 * j + 1) * NT + nt) * 32 + lane] =
+                        make_uint2(__byte_perm(x[j].y, x[j].w, 0x5410), __byte_perm(x[j].y, x[j].w, 0x7632));
+                    float f[8];
+                    unpack8<BF16>(x[j], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        a += f[i];
+                }
+                a += __shfl_xor_sync(FULL, a, 1);
+                sum[gq] = a + __shfl_xor_sync(FULL, a, 2);
+            }
+            // the bias step's B operand: k pair j holds (-128, 1) * part j / GQ of group j % GQ's sum
+#pragma unroll
+            for (int st = 0; st < P::BIAS_STEPS; ++st) {
+                uint32_t b[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int j = st * 8 + x * 4 + quad;
+                    float a = sum[0];
+#pragma unroll
+                    for (int gq = 1; gq < GQ; ++gq)
+                        a = j % GQ == gq ? sum[gq] : a;
+                    const int which = j / GQ;
+                    const float p0 = __bfloat162float(__float2bfloat16_rn(a));
+                    const float p1 = __bfloat162float(__float2bfloat16_rn(a - p0));
+                    const float part = which == 0 ? p0 : which == 1 ? p1 : which == 2 ? (a - p0) - p1 : 0.f;
+                    b[x] = pack16<true>(BF16 ? -128.f * part : 0.f, part);
+                }
+                qf[((P::KSTEPS + st) * NT + nt) * 32 + lane] = make_uint2(b[0], b[1]);
+            }
+        }
+        __syncwarp();
+
+        t.clear();
+        const int first = w.sp.len - p.n;  // position of row 0
+        const int pos_lo = first + r_base / p.G;
+        const int pos_hi = first + min(p.n - 1, (r_base + P::COLS - 1) / p.G);
+        for (int e = w.e0; e < w.e1; ++e) {
+            const int tok0 = w.sp.tile(e) * TILE;
+            const bool whole = tok0 + TILE - 1 <= pos_lo &&
+                               (p.window == 0 || tok0 > pos_hi - p.window || tok0 + TILE <= p.sinks);
+            float s[2][NT][4];
+            if (!landed())
+                return;
+            t.scores(s, ring_p + slot * P::SLOT, qf, lane, p.c);
+            refill();
+            if (!whole)
+                t.mask(s, p, tok0, first, r_base, lane);
+            t.weights(s, lane);
+            if (!landed())
+                return;
+            if (whole)
+                t.template output<false>(s, ring_p + slot * P::SLOT, lane);
+            else
+                t.template output<true>(s, ring_p + slot * P::SLOT, lane);
+            refill();
+        }
+
+        // ---- the segment's result: a lane holds channels 8 row8 .. + 7 of each group, of columns
+        // 2 quad and 2 quad + 1
+        const bool direct = w.e0 == 0 && w.e1 == w.sp.count;
+        // a part that continues a problem is this run's first segment, one that begins it its last
+        float *part = p.workspace + (static_cast<long long>(run) * 2 + (w.e0 == 0 ? 1 : 0)) * part_floats<D>(p.part_cols);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float sum = t.l[nt][i];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1)
+                    sum += __shfl_xor_sync(FULL, sum, off);
+                const int col = nt * 8 + 2 * quad + i, r = r_base + col;
+                const float inv = !direct ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key: 0 and -inf
 #pragma unroll
                 for (int gq = 0; gq < GQ; ++gq) {
-                    float c = corr[nt][gq];
+                    float c = t.corr[nt][gq];
                     c += __shfl_xor_sync(FULL, c, 1);
                     c += __shfl_xor_sync(FULL, c, 2);
-                    cg[gq][0] = __shfl_sync(FULL, c, 8 * quad);      // column 2 quad
-                    cg[gq][1] = __shfl_sync(FULL, c, 8 * quad + 4);  // column 2 quad + 1
-                }
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        o[i][nt][x] = (o[i][nt][x] + cg[i / 4][x & 1]) * f[x & 1];
-            }
-            if (warp >= M::O_SLOTS) {
-                float *dst = obuf + (warp - M::O_SLOTS) * COLS * D;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            dst[((i * NT + nt) * 4 + x) * 32 + lane] = o[i][nt][x];
-            }
-        }
-        if (parts > M::O_SLOTS)
-            __syncthreads();
-        if (warp < M::O_SLOTS && warp < parts) {
-            float *dst = obuf + warp * COLS * D;
-            const bool more = warp + M::O_SLOTS < parts;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        float *at = dst + ((i * NT + nt) * 4 + x) * 32 + lane;
-                        *at = more ? o[i][nt][x] + *at : o[i][nt][x];
-                    }
-        }
-        __syncthreads();
-        // ---- sum over the slots; eight channels of a column a thread
-        {
-            const long long unit0 = run0 + (run_len - w.left) - w.e0;  // the problem's first tile among all
-            const bool direct = w.e0 == 0 && w.e1 == w.sp.count;
-            // a part that continues a problem is this CTA's first segment, one that begins it its last
-            const int slot = unit0 < run0 ? 0 : 1;
-            float *part = p.workspace + (static_cast<long long>(blockIdx.x) * 2 + slot) * part_floats<D, NT>();
-            const int slots = min(parts, M::O_SLOTS);
-            for (int it = tid; it < GQ * NT * 64; it += THREADS) {
-                const int ln = it & 31, par = (it >> 5) & 1, nt = (it >> 6) % NT, gq = it / (64 * NT);
-                const int col = nt * 8 + 2 * (ln & 3) + par, r = r_base + col;
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    y[i] = 0.f;
-                for (int sl = 0; sl < slots; ++sl) {
-                    const float *src = obuf + sl * COLS * D + ln;
+                    c = __shfl_sync(FULL, c, 8 * quad + 4 * i);  // lanes with row8 = 2 quad + i hold this column's
+                    float y[8];
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            y[2 * mt + x] += src[(((gq * 4 + mt) * NT + nt) * 4 + 2 * x + par) * 32];
+                            y[2 * mt + x] = (t.o[gq * 4 + mt][nt][2 * x + i] + c) * inv;
+                    if (r >= R)
+                        continue;
+                    const int c0 = gq * kCacheGroup + row8 * 8;
+                    if (direct) {
+                        *reinterpret_cast<uint4 *>(p.o + row_of(r) * D + c0) = pack8<BF16>(y);
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(part + col * D + c0);
+                        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    }
                 }
-                if (r >= R || *failed)
-                    continue;
-                float mx = -INFINITY, sum = 0.f;
-                for (int x = 0; x < parts; ++x)
-                    mx = fmaxf(mx, m_all[x * COLS + col]);
-                for (int x = 0; x < parts; ++x) {
-                    const float mw = m_all[x * COLS + col];
-                    // a warp whose keys were all out of sight holds 0 (or, after a NaN score, NaN)
-                    sum += l_all[x * COLS + col] * (mw == -INFINITY ? 1.f : ptx::ex2(mw - mx));
-                }
-                const int c0 = gq * kCacheGroup + (ln >> 2) * 8;
-                if (direct) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key: 0 and -inf
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] *= inv;
-                    *reinterpret_cast<uint4 *>(p.o + row_of(r) * D + c0) = pack8<BF16>(y);
-                    if (c0 == 0 && p.lse != nullptr)
-                        p.lse[row_of(r)] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(part + col * D + c0);
-                    dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-                    dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-                    if (c0 == 0) {
-                        part[COLS * D + col] = mx;
-                        part[COLS * D + COLS + col] = sum;
+                if (r < R && row8 == 0) {
+                    if (!direct) {
+                        part[p.part_cols * D + col] = t.m[nt][i];
+                        part[p.part_cols * (D + 1) + col] = sum;
+                    } else if (p.lse != nullptr) {
+                        p.lse[row_of(r)] = sum == 0.f ? -INFINITY : (t.m[nt][i] + log2f(sum)) * kLn2;
                     }
                 }
             }
         }
-        __syncthreads();  // the buffers serve the next segment
-        w.next(p);
     }
 }
 
-// Joins the parts of every problem that more than one CTA worked on, in the order of the CTAs, and
+// Joins the parts of every problem that more than one run shares, in the order of the runs, and
 // writes the rows of empty sequences. One block a problem, one warp a column.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(c4::THREADS) cache4_merge_kernel(const Cache4AttnParams p)
+__global__ void __launch_bounds__(32 * c4::MERGE_WARPS) cache4_merge_kernel(const Cache4AttnParams p)
 {
     using namespace c4;
-    constexpr int COLS = 8 * NT, V = D / 32;
+    constexpr int COLS = 8 * NT, V = D / 32, WARPS = MERGE_WARPS, THREADS = 32 * WARPS;
     __shared__ long long both[2][WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per_seq = p.Hkv * p.chunks;
@@ -858,12 +835,12 @@ __global__ void __launch_bounds__(c4::THREADS) cache4_merge_kernel(const Cache4A
         }
         return;
     }
-    // tiles before this sequence, and in all
+    // positions before this sequence, and in all
     long long before = 0, total = 0;
     {
         long long a = 0, t = 0;
         for (int i = threadIdx.x; i < p.nseq; i += THREADS) {
-            const long long n = span_of(p, i).count;
+            const long long n = problem_length(span_of(p, i));
             t += n;
             a += i < s ? n : 0;
         }
@@ -885,20 +862,21 @@ __global__ void __launch_bounds__(c4::THREADS) cache4_merge_kernel(const Cache4A
     }
     before *= per_seq;
     total *= per_seq;
-    const long long u0 = before + static_cast<long long>(u) * sp.count, u1 = u0 + sp.count;
-    const int busy = busy_ctas(p, total);
-    // the CTA whose run holds tile x: the largest i with run_start(i) <= x
+    // the problem's tiles, behind its OVERHEAD
+    const long long u0 = before + u * problem_length(sp) + OVERHEAD, u1 = u0 + sp.count;
+    const int busy = busy_runs(p, total);
+    // the run that holds position x: the largest i with run_start(i) <= x
     const int i0 = static_cast<int>(((u0 + 1) * busy - 1) / total), i1 = static_cast<int>((u1 * busy - 1) / total);
     if (i0 == i1)
-        return;  // written by the CTA itself
-    constexpr int PART = part_floats<D, NT>();
-    // part x (CTA i0 + x): the first begins the problem (slot 1), the others continue it (slot 0)
-    auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * PART; };
+        return;  // written by the run's warp itself
+    // part x (run i0 + x): the first begins the problem (slot 1), the others continue it (slot 0)
+    auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * part_floats<D>(p.part_cols); };
+    const int pc = p.part_cols;
     const int parts = i1 - i0 + 1;
     for (int col = warp; col < COLS && r_base + col < R; col += WARPS) {
         float mx = -INFINITY;
         for (int x = lane; x < parts; x += 32)
-            mx = fmaxf(mx, part(x)[COLS * D + col]);
+            mx = fmaxf(mx, part(x)[pc * D + col]);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
@@ -909,9 +887,9 @@ __global__ void __launch_bounds__(c4::THREADS) cache4_merge_kernel(const Cache4A
         for (int x0 = 0; x0 < parts; x0 += 32) {
             float f = 0.f;
             if (x0 + lane < parts) {
-                const float mw = part(x0 + lane)[COLS * D + col];
+                const float mw = part(x0 + lane)[pc * D + col];
                 f = mw == -INFINITY ? 1.f : ptx::ex2(mw - mx);  // 1: the part holds 0, or NaN
-                sum += f * part(x0 + lane)[COLS * D + COLS + col];
+                sum += f * part(x0 + lane)[pc * (D + 1) + col];
             }
             const int end = min(32, parts - x0);
 #pragma unroll 4
@@ -943,25 +921,26 @@ __global__ void __launch_bounds__(c4::THREADS) cache4_merge_kernel(const Cache4A
 }
 
 template <int D, bool BF16, int NT>
-cudaError_t launch_cache4_attn(const Cache4AttnParams &p, cudaStream_t st)
+cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
 {
-    using M = c4::Smem<D, NT>;
+    using P = c4::Plan<D, NT>;
     static unsigned long long done = 0;
     auto kern = cache4_attn_kernel<D, BF16, NT>;
-    cudaError_t e = set_smem_once(kern, M::BYTES, done);
+    cudaError_t e = set_smem_once(kern, P::BYTES, done);
     if (e != cudaSuccess)
         return e;
-    kern<<<p.ctas, c4::THREADS, M::BYTES, st>>>(p);
+    p.runs = sms * P::WARPS;
+    kern<<<sms, P::THREADS, P::BYTES, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    cache4_merge_kernel<D, BF16, NT><<<p.nseq * p.Hkv * p.chunks, c4::THREADS, 0, st>>>(p);
+    cache4_merge_kernel<D, BF16, NT><<<p.nseq * p.Hkv * p.chunks, 32 * c4::MERGE_WARPS, 0, st>>>(p);
     return cudaGetLastError();
 }
 
 // One per (head dim, dtype): 8 or, wide, 16 columns a CTA.
-cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, cudaStream_t st);
-cudaError_t cache4_attn_d128_bf16(const Cache4AttnParams &p, bool wide, cudaStream_t st);
-cudaError_t cache4_attn_d256_fp16(const Cache4AttnParams &p, bool wide, cudaStream_t st);
-cudaError_t cache4_attn_d256_bf16(const Cache4AttnParams &p, bool wide, cudaStream_t st);
+cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d128_bf16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d256_fp16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d256_bf16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
 
 }  // namespace sdp

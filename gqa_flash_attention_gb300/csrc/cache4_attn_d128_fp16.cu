@@ -3,9 +3,9 @@
 
 namespace sdp {
 
-cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, cudaStream_t st)
+cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st)
 {
-    return wide ? launch_cache4_attn<128, false, 2>(p, st) : launch_cache4_attn<128, false, 1>(p, st);
+    return wide ? launch_cache4_attn<128, false, 2>(p, sms, st) : launch_cache4_attn<128, false, 1>(p, sms, st);
 }
 
 }  // namespace sdp
