@@ -28,7 +28,7 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, Shape *sh)
     const long long columns = static_cast<long long>(Hq / Hkv) * rows;
     sh->wide = columns > 8;
     const long long chunks = sh->wide ? (columns + 15) / 16 : 1;
-    if (static_cast<long long>(nseq) * Hkv > INT32_MAX || chunks * nseq * Hkv > INT32_MAX)
+    if (static_cast<long long>(nseq) * Hkv > INT32_MAX || chunks * 16 > INT32_MAX / (static_cast<long long>(nseq) * Hkv))
         return SDP_ERR_OVERFLOW;
     sh->chunks = static_cast<int>(chunks);
     int dev = 0, sms = 0;
@@ -120,8 +120,8 @@ extern "C" int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (D == 128)
-        e = dtype == SDP_BF16 ? sdp::cache4_attn_d128_bf16(p, sh.wide, sh.sms, st) : sdp::cache4_attn_d128_fp16(p, sh.wide, sh.sms, st);
+        e = dtype == SDP_BF16 ? sdp::cache4_attn_d128_bf16(p, sh.sms, st) : sdp::cache4_attn_d128_fp16(p, sh.sms, st);
     else
-        e = dtype == SDP_BF16 ? sdp::cache4_attn_d256_bf16(p, sh.wide, sh.sms, st) : sdp::cache4_attn_d256_fp16(p, sh.wide, sh.sms, st);
+        e = dtype == SDP_BF16 ? sdp::cache4_attn_d256_bf16(p, sh.sms, st) : sdp::cache4_attn_d256_fp16(p, sh.sms, st);
     return e == cudaSuccess ? SDP_OK : sdp::record_cuda_error(e);
 }

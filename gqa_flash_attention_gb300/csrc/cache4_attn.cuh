@@ -20,7 +20,10 @@
 //      n - 8 in bf16 is 128 + n less 136, exactly: O is a sum of many small terms of both signs, and
 //      with the 128 left in (and taken out at the end, as for a score) it lost up to 7e-3 of O over
 //      32768 keys. p_t s_t as two bf16 (high part and remainder, 2^-17 relative: fp16's range would
-//      not hold p s, and one bf16 would cost more than the output's rounding) in two MMAs.
+//      not hold p s, and one bf16 would cost more than the output's rounding): in two MMAs, or where
+//      the live columns fill only half of the eight (up to four, TWICE) in one, with the high parts
+//      in columns 0-3 and the remainders of the same queries in columns 4-7.
+//   These MMAs bound the kernel: mma.sync takes 32 cycles a scheduler for one m16n8k16 here.
 //   S = K Q^T with 16 tokens by 8 columns (m16n8k16), O = V^T P with 16 channels by 8 columns:
 //   few columns fill the n side. p turns from S's layout (token rows) to P's (column rows) by
 //   movmatrix on the two halves of its 32 bits.
@@ -77,7 +80,7 @@ namespace c4 {
 
 constexpr int TILE = 32;     // tokens a warp step
 constexpr int OVERHEAD = 1;  // tiles that a problem's start and end cost as much as
-constexpr int MERGE_WARPS = 8;
+constexpr int MERGE_THREADS = 256;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float RESCALE = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -261,7 +264,7 @@ __device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, unsigne
 
 // One tile's scores to weights to O (see the top of the file). MASKED: some column does not see
 // some key of the tile, or the tile ends past the sequence.
-template <int D, bool BF16, int NT>
+template <int D, bool BF16, int NT, bool TWICE>
 struct Tile {
     using P = c4::Plan<D, NT>;
     static constexpr int GQ = P::GQ;
@@ -375,7 +378,8 @@ struct Tile {
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int at = first + min(p.n - 1, (r_base + nt * 8 + 2 * quad + i) / p.G);
+                const int col = nt * 8 + 2 * quad + i;
+                const int at = first + min(p.n - 1, (r_base + (TWICE ? col & 3 : col)) / p.G);
                 const int from = p.window > 0 ? at - p.window : -1;  // keys past it are in the window
 #pragma unroll
                 for (int mc = 0; mc < 2; ++mc)
@@ -493,6 +497,8 @@ struct Tile {
                         hi[nt][i] = pack16<true>(x[2 * i], x[2 * i + 1]);
                         lo[nt][i] = pack16<true>(x[2 * i] - __uint_as_float(hi[nt][i] << 16),
                                                  x[2 * i + 1] - __uint_as_float(hi[nt][i] & 0xffff0000u));
+                        if (TWICE && row8 >= 4)
+                            hi[nt][i] = lo[nt][i];
                     }
                 }
                 // halves of the words: codes 0-3 of two tokens, codes 4-7 of two tokens
@@ -507,7 +513,8 @@ struct Tile {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                        mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
+                        if constexpr (!TWICE)
+                            mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
                     }
                 }
             }
@@ -515,7 +522,7 @@ struct Tile {
     }
 };
 
-template <int D, bool BF16, int NT>
+template <int D, bool BF16, int NT, bool TWICE>
 __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kernel(const Cache4AttnParams p)
 {
     using namespace c4;
@@ -670,7 +677,8 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
 
     const int run = warp * gridDim.x + blockIdx.x;
     const int R = p.n * p.G;
-    Tile<D, BF16, NT> t;
+    Tile<D, BF16, NT, TWICE> t;
+    static_assert(!TWICE || NT == 1, "eight columns");
     for (; !w.done(); w.find(p)) {
         const int g = w.u / p.chunks, r_base = (w.u - g * p.chunks) * P::COLS;
         auto row_of = [&](int r) {  // the (sequence, row, head) row of column r in q, o and lse
@@ -680,7 +688,7 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = r_base + nt * 8 + row8;
+            const int r = TWICE ? row8 & 3 : r_base + nt * 8 + row8;
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (r < R ? row_of(r) : 0) * D) + quad * 2;
             float sum[GQ];
 #pragma unroll
@@ -780,7 +788,12 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            y[2 * mt + x] = (t.o[gq * 4 + mt][nt][2 * x + i] + c) * inv;
+                        {
+                            float a = t.o[gq * 4 + mt][nt][2 * x + i];
+                            if constexpr (TWICE)  // columns + 4: the remainders
+                                a += __shfl_xor_sync(FULL, a, 2);
+                            y[2 * mt + x] = (a + c) * inv;
+                        }
                     if (r >= R)
                         continue;
                     const int c0 = gq * kCacheGroup + row8 * 8;
@@ -806,54 +819,58 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
 }
 
 // Joins the parts of every problem that more than one run shares, in the order of the runs, and
-// writes the rows of empty sequences. One block a problem, one warp a column.
+// writes the rows of empty sequences. One block a column of a problem: D / 4 threads hold its
+// channels, four each, and the block's THREADS / (D / 4) groups of them take every so-many-th part,
+// so that the parts of a long problem (57 at four sequences of 32768 keys) are read at once and not
+// one after the other.
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(32 * c4::MERGE_WARPS) cache4_merge_kernel(const Cache4AttnParams p)
+__global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const Cache4AttnParams p)
 {
     using namespace c4;
-    constexpr int COLS = 8 * NT, V = D / 32, WARPS = MERGE_WARPS, THREADS = 32 * WARPS;
+    constexpr int THREADS = MERGE_THREADS, WARPS = THREADS / 32, LANES = D / 4, GROUPS = THREADS / LANES;
     __shared__ long long both[2][WARPS];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ float4 y_all[GROUPS][LANES];
+    __shared__ float l_all[GROUPS];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per_seq = p.Hkv * p.chunks;
-    const int s = blockIdx.x / per_seq, u = blockIdx.x - s * per_seq;
-    const int g = u / p.chunks, chunk = u - g * p.chunks;
+    const int col = blockIdx.x % p.part_cols, problem = blockIdx.x / p.part_cols;
+    const int s = problem / per_seq, u = problem - s * per_seq;
+    const int g = u / p.chunks, r = (u - g * p.chunks) * 8 * NT + col;
+    if (r >= p.n * p.G)
+        return;
     const Span sp = span_of(p, s);
-    const int R = p.n * p.G, r_base = chunk * COLS;
-    auto row_of = [&](int r) { return (static_cast<long long>(s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G; };
+    const long long row = (static_cast<long long>(s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
     if (sp.count == 0) {
         if (sp.bad) {
-            if (threadIdx.x == 0)
+            if (tid == 0)
                 atomicCAS(p.status, 0u, kBadSeqlens);
             return;
         }
-        for (int col = warp; col < COLS && r_base + col < R; col += WARPS) {
-            const long long row = row_of(r_base + col);
-            for (int i = lane; i < D / 8; i += 32)
-                reinterpret_cast<uint4 *>(p.o + row * D)[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (lane == 0 && p.lse != nullptr)
-                p.lse[row] = -INFINITY;
-        }
+        if (tid < D / 8)
+            reinterpret_cast<uint4 *>(p.o + row * D)[tid] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0 && p.lse != nullptr)
+            p.lse[row] = -INFINITY;
         return;
     }
     // positions before this sequence, and in all
     long long before = 0, total = 0;
     {
-        long long a = 0, t = 0;
-        for (int i = threadIdx.x; i < p.nseq; i += THREADS) {
+        for (int i = tid; i < p.nseq; i += THREADS) {
             const long long n = problem_length(span_of(p, i));
-            t += n;
-            a += i < s ? n : 0;
+            total += n;
+            before += i < s ? n : 0;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) {
-            a += __shfl_xor_sync(FULL, a, off);
-            t += __shfl_xor_sync(FULL, t, off);
+            before += __shfl_xor_sync(FULL, before, off);
+            total += __shfl_xor_sync(FULL, total, off);
         }
         if (lane == 0) {
-            both[0][warp] = a;
-            both[1][warp] = t;
+            both[0][warp] = before;
+            both[1][warp] = total;
         }
         __syncthreads();
+        before = total = 0;
 #pragma unroll
         for (int i = 0; i < WARPS; ++i) {
             before += both[0][i];
@@ -869,63 +886,59 @@ __global__ void __launch_bounds__(32 * c4::MERGE_WARPS) cache4_merge_kernel(cons
     const int i0 = static_cast<int>(((u0 + 1) * busy - 1) / total), i1 = static_cast<int>((u1 * busy - 1) / total);
     if (i0 == i1)
         return;  // written by the run's warp itself
+    const int parts = i1 - i0 + 1, pc = p.part_cols;
     // part x (run i0 + x): the first begins the problem (slot 1), the others continue it (slot 0)
-    auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * part_floats<D>(p.part_cols); };
-    const int pc = p.part_cols;
-    const int parts = i1 - i0 + 1;
-    for (int col = warp; col < COLS && r_base + col < R; col += WARPS) {
-        float mx = -INFINITY;
-        for (int x = lane; x < parts; x += 32)
-            mx = fmaxf(mx, part(x)[pc * D + col]);
+    auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * part_floats<D>(pc); };
+    // every group finds the maximum for itself (its threads read the same words)
+    const int grp = tid / LANES, c4x = tid % LANES;
+    float mx = -INFINITY;
+    for (int x = lane; x < parts; x += 32)
+        mx = fmaxf(mx, part(x)[pc * D + col]);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
-        float sum = 0.f, y[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            y[i] = 0.f;
-        for (int x0 = 0; x0 < parts; x0 += 32) {
-            float f = 0.f;
-            if (x0 + lane < parts) {
-                const float mw = part(x0 + lane)[pc * D + col];
-                f = mw == -INFINITY ? 1.f : ptx::ex2(mw - mx);  // 1: the part holds 0, or NaN
-                sum += f * part(x0 + lane)[pc * (D + 1) + col];
-            }
-            const int end = min(32, parts - x0);
+    for (int off = 16; off > 0; off >>= 1)
+        mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
 #pragma unroll 4
-            for (int x = 0; x < end; ++x) {
-                const float fx = __shfl_sync(FULL, f, x);
-                const float4 *src = reinterpret_cast<const float4 *>(part(x0 + x) + col * D) + lane * (V / 4);
-#pragma unroll
-                for (int i = 0; i < V / 4; ++i) {
-                    const float4 t = src[i];
-                    y[4 * i] = fmaf(fx, t.x, y[4 * i]);
-                    y[4 * i + 1] = fmaf(fx, t.y, y[4 * i + 1]);
-                    y[4 * i + 2] = fmaf(fx, t.z, y[4 * i + 2]);
-                    y[4 * i + 3] = fmaf(fx, t.w, y[4 * i + 3]);
-                }
-            }
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1)
-            sum += __shfl_xor_sync(FULL, sum, off);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const long long row = row_of(r_base + col);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + row * D) + lane * (V / 2);
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i)
-            dst[i] = pack16<BF16>(y[2 * i] * inv, y[2 * i + 1] * inv);
-        if (lane == 0 && p.lse != nullptr)
-            p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
+    for (int x = grp; x < parts; x += GROUPS) {
+        const float *src = part(x);
+        const float4 t = reinterpret_cast<const float4 *>(src + col * D)[c4x];
+        const float mw = src[pc * D + col], lw = src[pc * (D + 1) + col];
+        const float f = mw == -INFINITY ? 1.f : ptx::ex2(mw - mx);  // 1: the part holds 0, or NaN
+        sum = fmaf(f, lw, sum);
+        y.x = fmaf(f, t.x, y.x);
+        y.y = fmaf(f, t.y, y.y);
+        y.z = fmaf(f, t.z, y.z);
+        y.w = fmaf(f, t.w, y.w);
     }
+    y_all[grp][c4x] = y;
+    if (c4x == 0)
+        l_all[grp] = sum;
+    __syncthreads();
+    if (grp != 0)
+        return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+        const float4 t = y_all[i][c4x];
+        y.x += t.x;
+        y.y += t.y;
+        y.z += t.z;
+        y.w += t.w;
+        sum += l_all[i];
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    reinterpret_cast<uint2 *>(p.o + row * D)[c4x] =
+        make_uint2(pack16<BF16>(y.x * inv, y.y * inv), pack16<BF16>(y.z * inv, y.w * inv));
+    if (c4x == 0 && p.lse != nullptr)
+        p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <int D, bool BF16, int NT>
+template <int D, bool BF16, int NT, bool TWICE>
 cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
 {
     using P = c4::Plan<D, NT>;
     static unsigned long long done = 0;
-    auto kern = cache4_attn_kernel<D, BF16, NT>;
+    auto kern = cache4_attn_kernel<D, BF16, NT, TWICE>;
     cudaError_t e = set_smem_once(kern, P::BYTES, done);
     if (e != cudaSuccess)
         return e;
@@ -933,14 +946,14 @@ cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
     kern<<<sms, P::THREADS, P::BYTES, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    cache4_merge_kernel<D, BF16, NT><<<p.nseq * p.Hkv * p.chunks, 32 * c4::MERGE_WARPS, 0, st>>>(p);
+    cache4_merge_kernel<D, BF16, NT><<<p.nseq * p.Hkv * p.chunks * p.part_cols, c4::MERGE_THREADS, 0, st>>>(p);
     return cudaGetLastError();
 }
 
-// One per (head dim, dtype): 8 or, wide, 16 columns a CTA.
-cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
-cudaError_t cache4_attn_d128_bf16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
-cudaError_t cache4_attn_d256_fp16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
-cudaError_t cache4_attn_d256_bf16(const Cache4AttnParams &p, bool wide, int sms, cudaStream_t st);
+// One per (head dim, dtype): 8 columns a warp up to that many, else 16.
+cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d128_bf16(const Cache4AttnParams &p, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d256_fp16(const Cache4AttnParams &p, int sms, cudaStream_t st);
+cudaError_t cache4_attn_d256_bf16(const Cache4AttnParams &p, int sms, cudaStream_t st);
 
 }  // namespace sdp
