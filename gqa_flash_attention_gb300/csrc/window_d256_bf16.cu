@@ -1,0 +1,12 @@
+// Instantiation of the sliding-window kernel: head dim 256, bf16 I/O.
+#include "window_kernel.cuh"
+#include "window_launch.h"
+
+namespace sdp {
+
+cudaError_t window_d256_bf16(const LaunchMaps &m, const WindowParams &p, cudaStream_t stream)
+{
+    return launch_window<256, true>(m, p, stream);
+}
+
+}  // namespace sdp

@@ -1,0 +1,667 @@
+// Attention with a sliding window and first tokens that stay visible (sdp_fwd_window,
+// sdp_fwd_varlen_window): a query row at position p of its sequence sees the keys j <= p with
+// j > p - W or j < sinks. A sequence's rows are its last sq positions (p = skv - sq + i), so the
+// same call serves a whole prompt and a chunk behind a cached prefix.
+//
+// Arithmetic and roles are those of the single-CTA kernel (sdp_fwd_kernel.cuh): 128-row query
+// tiles, 128-key tiles through a TMA ring, S = Q K^T and O += P V on tcgen05 with both
+// accumulators in tensor memory, one thread a row for the softmax with a lazily moved maximum.
+// What the window changes:
+//
+//  - A unit (query tile, head) reads only the tiles of the sinks and those from its first row's
+//    window start to its last row's own key: min(p, W) / 128 + 2 of them, whatever the length.
+//  - Units are short (W = 1024: 10 tiles), so set-up, tear-down and the first loads would take a
+//    third of the time: the kernel is persistent, one CTA an SM, with the next unit's Q and K/V
+//    loads and first scores running during the current unit's end (barrier phases and ring
+//    positions count across units). Units cost alike and neighbours share their K/V, so CTA c
+//    takes units c, c + C, c + 2C, ... with no counter to claim from, the same in a captured
+//    graph.
+//  - Only the tiles that cut a window or the diagonal (two or three a unit, plus the sinks') are
+//    masked, from four 32-bit words of visible keys a row; the others run without a test.
+//  - A row may see nothing in a tile, or at all (more rows than keys): its maximum stays -inf, its
+//    weights 0, and at the end O = 0 and LSE = -inf.
+//  - Masked weights are exactly 0, but 0 times an infinity or a NaN in V is NaN: a row whose O is
+//    not finite is computed again at the end from the keys it sees alone (recompute_row), so what
+//    lies outside a window stays outside. Rows that are finite pay one multiply-add an element.
+#pragma once
+
+#include "sdp_fwd_kernel.cuh"
+
+namespace sdp {
+
+struct WindowParams {
+    KernelParams k;  // as the other forward kernels take it (causal 0: the compact list in sequence order)
+    const void *q, *kk, *v;
+    // element strides of a plane (head) and of a row
+    long long q_plane, q_row, kv_plane, kv_row;
+    int window, sinks;
+    int pack_sq;  // > 0: a group's query heads run as one head of G * pack_sq rows
+};
+
+template <int D>
+struct WindowLayout {
+    using L = Layout<D>;
+    static constexpr int BAR_AREA = 512;
+    // Query tiles in shared memory: two at D=128 (the next unit's Q loads while this unit runs),
+    // one at D=256 (two would leave too few ring slots).
+    static constexpr int QB = D == 128 ? 2 : 1;
+    static constexpr int NSLOTS = (L::SMEM_LIMIT - BAR_AREA - 1024 - QB * L::Q_BYTES) / L::CHUNK_BYTES;
+    // q_full[QB], slot_full[NS], slot_empty[NS], s_full[NB], p_full[NB], o_done[ring], final[2],
+    // q_free[QB], o_free
+    static constexpr int NBARS = QB + 2 * NSLOTS + 2 * L::NSBUF + O_DONE_RING + 2 + QB + 1;
+    static constexpr int BAR_OFF = QB * L::Q_BYTES + NSLOTS * L::CHUNK_BYTES;
+    static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, then the abort flag
+    static constexpr int SMEM_BYTES = BAR_OFF + BAR_AREA + 1024;
+    static_assert(HOLDER_OFF + 8 <= BAR_OFF + BAR_AREA, "barrier area");
+    static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
+    // Ring parity across units of any lengths (global load positions): the S issuer waits for
+    // PV_{t-NSBUF} before its K slot and, with two chunks a tile, the PV issuer for P_j before its V
+    // chunks, which the persistent kernel of the dense forward has checked by enumeration.
+    static_assert(NSLOTS >= 4 && L::NSBUF <= 3, "ring parity soundness across units");
+};
+
+// Keys [0, n) of 32 as a bit mask.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// One row again, over the keys it sees alone: key ranges [0, a1) and [b0, b1) of the row's K/V plane.
+// Called by a whole warp (the rare path of rows whose O is not finite). 32 keys a step, one a lane, for
+// the scores; then each lane adds its D / 32 channels of their V rows.
+template <int D, bool BF16>
+static __device__ __noinline__ void recompute_row(const uint16_t *q, const uint16_t *k, const uint16_t *v, long long kv_row,
+                                                  int a1, int b0, int b1, float c, uint16_t *o, float *lse)
+{
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    float m = -INFINITY, l = 0.f, acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        acc[i] = 0.f;
+    const int n = a1 + max(0, b1 - b0);
+    for (int t = 0; t < n; t += 32) {
+        const int e = t + lane;
+        const bool live = e < n;
+        const long long key = e < a1 ? e : b0 + (e - a1);
+        float s = 0.f;
+        if (live) {
+            const uint4 *kr = reinterpret_cast<const uint4 *>(k + key * kv_row), *qr = reinterpret_cast<const uint4 *>(q);
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 x = __ldg(kr + i), y = __ldg(qr + i);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    float2 f, g;
+                    if constexpr (BF16) {
+                        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&xs[w]));
+                        g = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&ys[w]));
+                    } else {
+                        f = __half22float2(*reinterpret_cast<const __half2 *>(&xs[w]));
+                        g = __half22float2(*reinterpret_cast<const __half2 *>(&ys[w]));
+                    }
+                    s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+                }
+            }
+            s *= c;
+        }
+        float mx = live ? s : -INFINITY;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float next = fmaxf(m, mx);
+        const float ref = next == -INFINITY ? 0.f : next;
+        const float alpha = m == -INFINITY ? 0.f : ptx::ex2(m - ref);
+        m = next;
+        const float w = live ? ptx::ex2(s - ref) : 0.f;
+        float sum = w;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        l = (l == 0.f ? 0.f : l * alpha) + sum;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            acc[i] = t == 0 ? 0.f : acc[i] * alpha;
+        for (int x = 0; x < 32 && t + x < n; ++x) {
+            const float wx = __shfl_sync(0xffffffffu, w, x);
+            const long long kx = t + x < a1 ? t + x : b0 + (t + x - a1);
+            const uint16_t *vr = v + kx * kv_row + lane * V;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint16_t u = __ldg(vr + i);
+                float f;
+                if constexpr (BF16)
+                    f = __uint_as_float(static_cast<uint32_t>(u) << 16);
+                else
+                    f = __half2float(*reinterpret_cast<const __half *>(&u));
+                acc[i] = fmaf(wx, f, acc[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<uint32_t *>(o + lane * V + i) = pack2<BF16>(acc[i] / l, acc[i + 1] / l);
+    if (lane == 0 && lse != nullptr)
+        *lse = (m + ptx::lg2(l)) * LN2;
+}
+
+template <int D, bool BF16, bool VARLEN>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                  const __grid_constant__ CUtensorMap tm_v, const WindowParams wp)
+{
+    using L = Layout<D>;
+    using WL = WindowLayout<D>;
+    const KernelParams &p = wp.k;
+    constexpr int NS = WL::NSLOTS;
+    constexpr int NB = L::NSBUF;
+    constexpr int CPT = L::CHUNKS_PER_TILE;
+    constexpr int QB = WL::QB;
+    constexpr uint32_t IDESC_S = ptx::idesc_f16_f32acc(128, L::BN, BF16, false);
+    constexpr uint32_t IDESC_PV = ptx::idesc_f16_f32acc(128, 128, BF16, true);
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = ptx::smem_addr(smem_raw);
+    const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw_addr + pad;
+    const uint32_t s_q0 = sbase;  // query tile b at s_q0 + b * Q_BYTES
+    const uint32_t s_ring = sbase + QB * L::Q_BYTES;
+    const uint32_t bar0 = sbase + WL::BAR_OFF;
+    const uint32_t q_full0 = bar0;  // + 8 b
+    const uint32_t slot_full0 = bar0 + 8u * QB;
+    const uint32_t slot_empty0 = slot_full0 + 8u * NS;
+    const uint32_t s_full0 = slot_empty0 + 8u * NS;
+    const uint32_t p_full0 = s_full0 + 8u * NB;
+    const uint32_t o_done0 = p_full0 + 8u * NB;
+    const uint32_t final0 = o_done0 + 8u * O_DONE_RING;
+    const uint32_t q_free0 = final0 + 16u;  // + 8 b: the S MMAs that read query tile b last are done
+    const uint32_t o_free = q_free0 + 8u * QB;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + WL::HOLDER_OFF);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    // A unit's geometry: Q/O and K/V planes, its first row within its sequence (q0) and in the row
+    // coordinate (q_row), the first K/V row, the sequence's rows, the position of its row 0, and its
+    // tiles: ns of the sinks, then those from t_lo, n in all. n = 0: no key (zero: its rows get O = 0
+    // and LSE = -inf), a slot past the last tile, or (bad) invalid offsets.
+    struct Unit {
+        int z_q, z_kv, q0, q_row, kv_row0, sq, pos0, t_lo, ns, n;
+        bool zero, bad;
+        __device__ __forceinline__ int tile(int j) const { return j < ns ? j : t_lo + j - ns; }
+    };
+    auto unit_of = [&](int u) {
+        Unit r{};
+        const int hi = u % p.G;
+        u /= p.G;
+        if constexpr (VARLEN) {
+            if (p.n_tiles > 0 && (u = varlen_compact_unit(p, u)) < 0)
+                return r;  // a slot past the last query tile
+        }
+        const int qt = u % p.n_qtiles, bg = u / p.n_qtiles;
+        const int b = bg / p.Hkv, g = bg - b * p.Hkv;
+        r.z_q = VARLEN ? g * p.G + hi : b * p.Hq + g * p.G + hi;
+        r.z_kv = VARLEN ? g : bg;
+        r.q0 = qt * L::BM;
+        const SeqGeom sg = seq_geom(p, b);
+        if (!sg.ok) {
+            r.bad = true;
+            return r;
+        }
+        r.sq = sg.sq;
+        if (r.q0 >= sg.sq)
+            return r;  // a tile past the end of a shorter sequence
+        r.q_row = sg.q_row0 + r.q0;
+        r.kv_row0 = sg.kv_row0;
+        r.pos0 = sg.skv - (wp.pack_sq > 0 ? wp.pack_sq : sg.sq);
+        // positions of the tile's first and last row
+        const int p_lo = r.pos0 + (wp.pack_sq > 0 ? 0 : r.q0);
+        const int p_hi = r.pos0 + (wp.pack_sq > 0 ? wp.pack_sq - 1 : min(r.q0 + L::BM, sg.sq) - 1);
+        if (p_hi < 0) {
+            r.zero = true;
+            return r;
+        }
+        r.t_lo = max(0, p_lo - wp.window + 1) / L::BN;
+        r.ns = min((min(wp.sinks, p_hi + 1) + L::BN - 1) / L::BN, r.t_lo);
+        r.n = r.ns + p_hi / L::BN + 1 - r.t_lo;
+        return r;
+    };
+
+    if (threadIdx.x == 0) {
+        for (int b = 0; b < QB; ++b) {
+            ptx::mbar_init(q_full0 + 8u * b, 1);
+            ptx::mbar_init(q_free0 + 8u * b, 1);
+        }
+        for (int s = 0; s < NS; ++s) {
+            ptx::mbar_init(slot_full0 + 8u * s, 1);
+            ptx::mbar_init(slot_empty0 + 8u * s, 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            ptx::mbar_init(s_full0 + 8u * i, 1);
+            ptx::mbar_init(p_full0 + 8u * i, 128);
+        }
+        for (int i = 0; i < O_DONE_RING; ++i)
+            ptx::mbar_init(o_done0 + 8u * i, 1);
+        ptx::mbar_init(final0, 1);
+        ptx::mbar_init(final0 + 8u, 1);
+        ptx::mbar_init(o_free, 4);  // one arrival per softmax warp
+        *abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    if (warp == 4 && lane == 0) {
+        ptx::prefetch_tmap(&tm_q);
+        ptx::prefetch_tmap(&tm_k);
+        ptx::prefetch_tmap(&tm_v);
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    const WaitCtx cx{abort_flag, p.status, p.timeout_ns};
+    const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
+        return __all_sync(0xffffffffu, wait_bounded(bar, parity, cx, site));
+    };
+
+    // Every role walks the units first, first + step, ...; k counts those with tiles.
+    if (warp == 4) {
+        // ------------------------------------------------------ TMA producer
+        if (!(p.debug_flags & DEBUG_NO_LOADS)) {  // whole warp; one elected lane issues
+            int slot = 0, k = 0;
+            uint32_t ph = 0, armed_mask = 0, armed_par = 0, q_armed = 0, q_par = 0;
+            bool ok = true;
+            for (int u = first; ok && u < p.units; u += step) {
+                const Unit un = unit_of(u);
+                const int n = un.n;
+                if (n == 0)
+                    continue;
+                const int b = k % QB;
+                if (k >= QB && !(ok = wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL)))
+                    break;
+                ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, L::Q_BYTES);
+#pragma unroll
+                for (int c = 0; c < D / L::BOX_COLS; ++c)
+                    ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, &tm_q, q_full0 + 8u * b, c * L::BOX_COLS,
+                                       un.q_row, un.z_q);
+                q_armed |= 1u << b;
+                q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
+                auto load_tile = [&](const CUtensorMap *map, int j) -> bool {
+#pragma unroll
+                    for (int ch = 0; ch < CPT; ++ch) {
+                        const uint32_t full = slot_full0 + 8u * slot;
+                        if (!wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY))
+                            return false;
+                        ptx::mbar_arrive_expect_tx_w(full, L::CHUNK_BYTES);
+                        const uint32_t dst = s_ring + slot * L::CHUNK_BYTES;
+                        const int y = un.kv_row0 + un.tile(j) * L::BN;
+                        ptx::tma_load_3d_w(dst, map, full, ch * 128, y, un.z_kv);
+                        ptx::tma_load_3d_w(dst + L::BOX_BYTES, map, full, ch * 128 + L::BOX_COLS, y, un.z_kv);
+                        armed_mask |= 1u << slot;
+                        armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                        if (++slot == NS) {
+                            slot = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    return true;
+                };
+                ok = load_tile(&tm_k, 0);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n)
+                        ok = load_tile(&tm_k, j + 1);
+                    if (ok)
+                        ok = load_tile(&tm_v, j);
+                }
+                ++k;
+            }
+            // Every copy this thread issued lands before the CTA may exit.
+            for (int b = 0; b < QB; ++b)
+                if (q_armed & (1u << b))
+                    wait_drain(q_full0 + 8u * b, (q_par >> b) & 1u, p.timeout_ns);
+            for (int s = 0; s < NS; ++s)
+                if (armed_mask & (1u << s))
+                    wait_drain(slot_full0 + 8u * s, (armed_par >> s) & 1u, p.timeout_ns);
+        }
+    } else if (warp == 5) {
+        // ------------------------------------------- S = Q K^T issuer
+        const uint64_t dk = ptx::smem_desc_sw128(s_ring, 16, 1024);
+        bool issued = false, ok = true;
+        int g0 = 0, pos0 = 0, k = 0;  // tiles and ring chunks of the earlier units
+        for (int u = first; ok && u < p.units; u += step) {
+            const int n = unit_of(u).n;
+            if (n == 0)
+                continue;
+            const int b = k % QB;
+            const uint64_t dq = ptx::smem_desc_sw128(s_q0 + b * L::Q_BYTES, 16, 1024);
+            if (!(ok = wait_all(q_full0 + 8u * b, (k / QB) & 1, SITE_Q_FULL)))
+                break;
+            for (int t = 0; ok && t < n; ++t) {
+                const int gt = g0 + t;
+                const int p0 = pos0 + pos_k<CPT>(t);
+                if (gt >= NB) {  // buffer gt % NB held P of tile gt - NB: its PV must have read it
+                    const int pv = gt - NB;
+                    if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
+                        break;
+                }
+#pragma unroll
+                for (int ch = 0; ch < CPT; ++ch) {
+                    const int pos = p0 + ch;
+                    if (!(ok = wait_all(slot_full0 + 8u * (pos % NS), (pos / NS) & 1, SITE_SLOT_FULL)))
+                        break;
+                }
+                if (!ok)
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem + L::TM_S + (gt % NB) * L::BN;
+#pragma unroll
+                for (int ch = 0; ch < CPT; ++ch) {
+                    const int slot = (p0 + ch) % NS;
+                    const uint64_t kslot = dk + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                    const uint64_t qch = dq + static_cast<uint64_t>((2 * ch * L::BOX_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t off = ((kk >> 2) * L::BOX_BYTES + (kk & 3) * 32) >> 4;
+                        ptx::mma_ss_w(d_tmem, qch + off, kslot + off, IDESC_S, (ch | kk) != 0);
+                    }
+                    issued = true;
+                    ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                }
+                ptx::mma_commit_w(s_full0 + 8u * (gt % NB));
+            }
+            if (!ok)
+                break;
+            ptx::mma_commit_w(q_free0 + 8u * b);  // query tile b may take unit k + QB's Q
+            g0 += n;
+            pos0 += 2 * CPT * n;
+            ++k;
+        }
+        if (issued) {  // all of this thread's MMAs complete before TMEM is freed
+            ptx::mma_commit_w(final0);
+            wait_drain(final0, 0, p.timeout_ns);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------ O += P V issuer
+        const uint64_t dv = ptx::smem_desc_sw128(s_ring, L::BOX_BYTES, 1024);
+        bool issued = false, ok = true;
+        int g0 = 0, pos0 = 0, k = 0;
+        for (int u = first; ok && u < p.units; u += step) {
+            const int n = unit_of(u).n;
+            if (n == 0)
+                continue;
+            for (int j = 0; ok && j < n; ++j) {
+                const int gj = g0 + j;
+                const int buf = gj % NB;
+                const int p0 = pos0 + pos_v<CPT>(j, n);
+                if constexpr (CPT == 1) {  // V_j's slot first, off the P_j -> PV_j path
+                    if (!(ok = wait_all(slot_full0 + 8u * (p0 % NS), (p0 / NS) & 1, SITE_SLOT_FULL)))
+                        break;
+                }
+                if (!(ok = wait_all(p_full0 + 8u * buf, (gj / NB) & 1, SITE_P_FULL)))
+                    break;
+                // a unit's first PV overwrites O: the previous unit's epilogue must have read it
+                if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t a_tmem = tmem + L::TM_S + buf * L::BN;
+#pragma unroll
+                for (int ch = 0; ch < CPT; ++ch) {
+                    const int pos = p0 + ch;
+                    const int slot = pos % NS;
+                    if constexpr (CPT != 1) {
+                        if (!(ok = wait_all(slot_full0 + 8u * slot, (pos / NS) & 1, SITE_SLOT_FULL)))
+                            break;
+                        ptx::tc_fence_after();
+                    }
+                    const uint64_t vslot = dv + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
+                                      (j > 0) || (kk > 0));
+                    issued = true;
+                    ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                }
+                if (!ok)
+                    break;
+                ptx::mma_commit_w(o_done0 + 8u * (gj % O_DONE_RING));
+            }
+            g0 += n;
+            pos0 += 2 * CPT * n;
+            ++k;
+        }
+        if (issued) {
+            ptx::mma_commit_w(final0 + 8u);
+            wait_drain(final0 + 8u, 0, p.timeout_ns);
+        }
+    } else if (warp < 4) {
+        // --------------------------------------- softmax / correction / epilogue
+        const int row = threadIdx.x;  // query row within the tile = TMEM lane
+        const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+        const uint32_t t_s = tmem + lane_off + L::TM_S;
+        const uint32_t t_o = tmem + lane_off + L::TM_O;
+        const float c = p.c;
+        bool ok = true;
+        int g0 = 0;
+        for (int u = first; ok && u < p.units; u += step) {
+            const Unit un = unit_of(u);
+            const int n = un.n;
+            uint16_t *const o_row = static_cast<uint16_t *>(p.o) + un.z_q * wp.q_plane +
+                                    static_cast<long long>(un.q_row + row) * wp.q_row;
+            const bool row_ok = un.q0 + row < un.sq;
+            float *const lse_row =
+                p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(un.z_q) * p.Sq + un.q_row + row;
+            if (n == 0) {
+                if (un.bad && row == 0) {
+                    const uint32_t cta = blockIdx.x < 0xFFFFFFu ? blockIdx.x : 0xFFFFFFu;
+                    atomicCAS(p.status, 0u, SITE_SEQLENS | (cta << 8));
+                }
+                if (un.zero && row_ok) {
+                    for (int i = 0; i < D / 8; ++i)
+                        reinterpret_cast<uint4 *>(o_row)[i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (lse_row != nullptr)
+                        *lse_row = -INFINITY;
+                }
+                continue;
+            }
+            // this row's position; keys [0, pos] and (> pos - window or < sinks) are visible
+            const int pos = un.pos0 + (wp.pack_sq > 0 ? (un.q0 + row) % wp.pack_sq : un.q0 + row);
+            float m_used = -INFINITY, l = 0.f;
+            bool s_seen = false;  // S_j's barrier was seen complete while tile j-1 ended
+            for (int j = 0; j < n; ++j) {
+                const int gj = g0 + j;
+                const int buf = gj % NB;
+                if (!__all_sync(0xffffffffu, s_seen)) {
+                    if (!(ok = wait_all(s_full0 + 8u * buf, (gj / NB) & 1, SITE_S_FULL)))
+                        break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t ts = t_s + buf * L::BN;
+                uint32_t sr[128];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    ptx::tmem_ld32(ts + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
+                ptx::tmem_wait_ld();
+                float s[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    s[i] = __uint_as_float(sr[i]);
+
+                // Only a tile that holds a key some row of the warp must not see is masked: the
+                // masked scores come out scaled (-inf where not seen), the others as they are.
+                const int k0 = un.tile(j) * L::BN;
+                const int hi = pos + 1 - k0, lo = pos - wp.window + 1 - k0, sk = wp.sinks - k0;  // i < hi && (i >= lo || i < sk)
+                const bool masked = __any_sync(0xffffffffu, hi < L::BN || (lo > 0 && sk < L::BN));
+                if (masked) {
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t vis = below(hi - 32 * w) & (~below(lo - 32 * w) | below(sk - 32 * w));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            s[32 * w + i] = (vis & (1u << i)) ? s[32 * w + i] * c : -INFINITY;
+                    }
+                }
+                const float ce = masked ? 1.f : c;
+                float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+                if (ce >= 0.f) {
+#pragma unroll
+                    for (int i = 4; i < 124; i += 8) {
+                        mx0 = ptx::max3(mx0, s[i], s[i + 1]);
+                        mx1 = ptx::max3(mx1, s[i + 2], s[i + 3]);
+                        mx2 = ptx::max3(mx2, s[i + 4], s[i + 5]);
+                        mx3 = ptx::max3(mx3, s[i + 6], s[i + 7]);
+                    }
+                    mx0 = ptx::max3(mx0, s[124], s[125]);
+                    mx1 = ptx::max3(mx1, s[126], s[127]);
+                    mx0 = ptx::max3(mx0, mx1, fmaxf(mx2, mx3));
+                } else {
+#pragma unroll
+                    for (int i = 4; i < 124; i += 8) {
+                        mx0 = ptx::min3(mx0, s[i], s[i + 1]);
+                        mx1 = ptx::min3(mx1, s[i + 2], s[i + 3]);
+                        mx2 = ptx::min3(mx2, s[i + 4], s[i + 5]);
+                        mx3 = ptx::min3(mx3, s[i + 6], s[i + 7]);
+                    }
+                    mx0 = ptx::min3(mx0, s[124], s[125]);
+                    mx1 = ptx::min3(mx1, s[126], s[127]);
+                    mx0 = ptx::min3(mx0, mx1, fminf(mx2, mx3));
+                }
+                // -inf while the row has seen no key (and its weights are 2^(-inf - 0) = 0)
+                const float m_tile = mx0 * ce;
+                const float m_new = m_tile > m_used + RESCALE_THRESHOLD ? m_tile : m_used;
+                const float alpha = m_new == m_used ? 1.f : ptx::ex2(m_used - m_new);
+                const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
+
+                uint32_t pk[64];
+                const uint64_t c2 = ptx::f2_pack(ce, ce), negm2 = ptx::f2_pack(neg_m, neg_m);
+                uint64_t sum01 = ptx::f2_pack(0.f, 0.f), sum23 = sum01;
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    float x0, x1, x2, x3;
+                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[2 * i], s[2 * i + 1]), c2, negm2), x0, x1);
+                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[2 * i + 2], s[2 * i + 3]), c2, negm2), x2, x3);
+                    const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1), p2 = ptx::ex2(x2), p3 = ptx::ex2(x3);
+                    sum01 = ptx::f2_add(sum01, ptx::f2_pack(p0, p1));
+                    sum23 = ptx::f2_add(sum23, ptx::f2_pack(p2, p3));
+                    pk[i] = pack2<BF16>(p0, p1);
+                    pk[i + 1] = pack2<BF16>(p2, p3);
+                }
+                // Poll S_{j+1}'s barrier now (same unit), so the answer returns while P_j is
+                // stored and handed off.
+                s_seen = j + 1 < n && ptx::mbar_test_wait(s_full0 + 8u * ((gj + 1) % NB), ((gj + 1) / NB) & 1);
+                float sum0, sum1, sum2, sum3;
+                ptx::f2_unpack(sum01, sum0, sum1);
+                ptx::f2_unpack(sum23, sum2, sum3);
+                ptx::tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                ptx::tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                ptx::tmem_wait_st();
+                l = fmaf(l, alpha, (sum0 + sum1) + (sum2 + sum3));
+
+                // Rescale O only in warps where some row's maximum moved (they wait for PV_{gj-1}).
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    const int pv = gj - 1;
+                    if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
+                        break;
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int cc = 0; cc < D / 32; ++cc) {
+                        uint32_t o[32];
+                        ptx::tmem_ld32(t_o + 32 * cc, o);
+                        ptx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        ptx::tmem_st32(t_o + 32 * cc, o);
+                    }
+                    ptx::tmem_wait_st();
+                }
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(p_full0 + 8u * buf);
+                m_used = m_new;
+            }
+            if (!ok)
+                break;
+
+            // ---------------------------------------------------------- epilogue
+            // O rows straight from registers to global memory, then O's tensor memory is released
+            // to the next unit's first PV.
+            {
+                const int pv = g0 + n - 1;
+                if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
+                    break;
+            }
+            ptx::tc_fence_after();
+            const bool none = l == 0.f;  // the row saw no key
+            const float inv_l = none ? 0.f : 1.f / l;
+            float probe = 0.f;  // NaN once an element of the row is not finite
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                ptx::tmem_ld32(t_o + 32 * cc, o);
+                ptx::tmem_wait_ld();
+                uint32_t pk[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float a = __uint_as_float(o[2 * i]), b = __uint_as_float(o[2 * i + 1]);
+                    probe = fmaf(a, 0.f, fmaf(b, 0.f, probe));
+                    pk[i] = none ? 0u : pack2<BF16>(a * inv_l, b * inv_l);
+                }
+                if (row_ok) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        reinterpret_cast<uint4 *>(o_row)[4 * cc + x] =
+                            make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+                }
+            }
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                ptx::mbar_arrive(o_free);
+            if (lse_row != nullptr && row_ok)
+                *lse_row = none ? -INFINITY : (m_used + ptx::lg2(l)) * LN2;
+            g0 += n;
+
+            unsigned again = __ballot_sync(0xffffffffu, row_ok && !none && probe != 0.f);
+            while (again != 0u) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1u;
+                const int r = warp * 32 + src;
+                const int at = __shfl_sync(0xffffffffu, pos, src);
+                const int b0 = max(0, at - wp.window + 1);
+                const long long q_off = un.z_q * wp.q_plane + static_cast<long long>(un.q_row + r) * wp.q_row;
+                const long long kv_off = un.z_kv * wp.kv_plane + static_cast<long long>(un.kv_row0) * wp.kv_row;
+                __syncwarp();  // the row's first stores before those that replace them
+                recompute_row<D, BF16>(static_cast<const uint16_t *>(wp.q) + q_off,
+                                       static_cast<const uint16_t *>(wp.kk) + kv_off,
+                                       static_cast<const uint16_t *>(wp.v) + kv_off, wp.kv_row, min(wp.sinks, b0), b0,
+                                       at + 1, c, static_cast<uint16_t *>(p.o) + q_off,
+                                       p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(un.z_q) * p.Sq + un.q_row + r);
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+    }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_window(const LaunchMaps &m, const WindowParams &p, cudaStream_t stream)
+{
+    static unsigned long long set_dense = 0, set_varlen = 0;
+    const bool vl = p.k.cu_q != nullptr;
+    auto kern = vl ? window_kernel<D, BF16, true> : window_kernel<D, BF16, false>;
+    cudaError_t e = set_smem_once(kern, WindowLayout<D>::SMEM_BYTES, vl ? set_varlen : set_dense);
+    if (e != cudaSuccess)
+        return e;
+    const int ctas = p.k.units < p.k.num_sms ? p.k.units : p.k.num_sms;
+    kern<<<ctas, NUM_THREADS, WindowLayout<D>::SMEM_BYTES, stream>>>(m.q, m.k, m.v, p);
+    return cudaGetLastError();
+}
+
+}  // namespace sdp

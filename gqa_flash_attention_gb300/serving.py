@@ -3,7 +3,8 @@
 ``qk_norm_rope``: norms and position rotation of the query and key heads in one pass, with
 ``rope_inv_freq`` and ``rope_table`` for its frequencies. ``Cache4``: a paged cache held in 4 bits,
 written by ``cache4_append`` and read back by ``cache4_gather``; ``fwd_cache4``: the attention of each
-sequence's last tokens over it.
+sequence's last tokens over it. ``fwd_window`` and ``fwd_varlen_window``: prefill attention with a sliding
+window and first tokens that stay visible.
 
 As in the rest of the package, these functions check and marshal arguments for the C ABI of
 ``include/sdp.h`` (which states layouts, ownership and errors), PyTorch supplies memory and
@@ -21,7 +22,8 @@ import torch
 from . import SDP_OK, _check, _DTYPE_CODE, _on, _stream_handle, lib
 
 __all__ = ["rope_inv_freq", "rope_table", "RopeTable", "qk_norm_rope", "Cache4", "cache4_empty", "cache4_append",
-           "cache4_gather", "CACHE4_GROUP", "fwd_cache4", "cache4_workspace_bytes"]
+           "cache4_gather", "CACHE4_GROUP", "fwd_cache4", "cache4_workspace_bytes",
+           "fwd_window", "fwd_varlen_window"]
 
 CACHE4_GROUP = 64  # channels that share one scale and bias
 
@@ -46,6 +48,10 @@ def _lib() -> ctypes.CDLL:
         L.sdp_fwd_cache4_workspace_bytes.restype = ll
         L.sdp_fwd_cache4.argtypes = [vp, *pool, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, ctypes.c_ulonglong, vp]
         L.sdp_fwd_cache4.restype = i
+        L.sdp_fwd_window.argtypes = [vp] * 5 + [i] * 6 + [f, i, i, i, vp]
+        L.sdp_fwd_window.restype = i
+        L.sdp_fwd_varlen_window.argtypes = [vp] * 7 + [i] * 7 + [f, i, i, i, vp]
+        L.sdp_fwd_varlen_window.restype = i
         _declared = L
     return _declared
 
@@ -69,6 +75,21 @@ def _empty(shape, dtype, dev: int, stream) -> torch.Tensor:
         t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(now)
     return t
+
+
+def _outputs(q, out, lse, return_lse, lse_shape, dev: int, stream):
+    """The output buffers of an attention call: given ones checked, others allocated."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, dev, stream)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError("out must be a contiguous tensor shaped and typed like q")
+    if lse is None:
+        if return_lse:
+            lse = _empty(lse_shape, torch.float32, dev, stream)
+    elif (tuple(lse.shape) != tuple(lse_shape) or lse.dtype != torch.float32 or not lse.is_contiguous()
+          or lse.get_device() != dev):
+        raise ValueError(f"lse must be a contiguous float32 tensor {tuple(lse_shape)} on q's device")
+    return out, lse
 
 
 # ------------------------------------------------------------------ positions
@@ -382,15 +403,7 @@ def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_t
     if ns != nseq or Dc != D:
         raise ValueError(f"shape mismatch: q {tuple(shape)}, {ns} sequences of head dim {Dc} in the cache")
     lens = _int32("cache_lens", cache_lens, nseq, dev)
-    if out is None:
-        out = _empty(shape, q.dtype, dev, stream)
-    elif out.shape != shape or out.dtype != q.dtype or not out.is_contiguous() or out.get_device() != dev:
-        raise ValueError("out must be a contiguous tensor shaped and typed like q")
-    if lse is None:
-        if return_lse:
-            lse = _empty(shape[:-1], torch.float32, dev, stream)
-    elif lse.shape != shape[:-1] or lse.dtype != torch.float32 or not lse.is_contiguous() or lse.get_device() != dev:
-        raise ValueError("lse must be a contiguous float32 tensor of q's shape without the last dimension")
+    out, lse = _outputs(q, out, lse, return_lse, shape[:-1], dev, stream)
     if nseq == 0 or rows == 0:
         return out, lse
     if scale is None:
@@ -406,6 +419,87 @@ def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_t
             q.data_ptr(), *pool, lens, out.data_ptr(), 0 if lse is None else lse.data_ptr(), nseq, rows, Hq, Hkv, D,
             scale, dt, window, sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
             _stream_handle(stream, dev))
+    if rc != SDP_OK:
+        _check(rc)
+    return out, lse
+
+
+# ------------------------------------------------------------------ sliding windows
+
+
+def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+               scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               return_lse: bool = True, stream=None):
+    """Causal attention over the last `window` keys and the first `sinks`.
+
+    q: [B, Hq, Sq, D]; k, v: [B, Hkv, Skv, D], contiguous, as sdp_fwd. Row i is at position
+    p = Skv - Sq + i and sees keys j <= p with j > p - window or j < sinks. Returns (o like q, lse
+    fp32 [B, Hq, Sq] or None); a row that sees no key gives 0 and -inf. Enqueued on `stream`
+    (default: the current stream), not synchronised.
+    """
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be 4-D [B, H, S, D]")
+    dev = q.get_device()
+    dt = _DTYPE_CODE.get(q.dtype)
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v must be CUDA tensors on one device")
+    if dt is None or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype, float16 or bfloat16")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("q, k, v must be contiguous")
+    _no_grad(q, k, v)
+    B, Hq, Sq, D = q.shape
+    kshape = k.shape
+    if kshape[0] != B or kshape[3] != D or v.shape != kshape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    out, lse = _outputs(q, out, lse, return_lse, (B, Hq, Sq), dev, stream)
+    with _on(dev):
+        rc = _lib().sdp_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                   0 if lse is None else lse.data_ptr(), B, Hq, kshape[1], Sq, kshape[2], D,
+                                   1.0 / math.sqrt(D) if scale is None else scale, dt, window, sinks,
+                                   _stream_handle(stream, dev))
+    if rc != SDP_OK:
+        _check(rc)
+    return out, lse
+
+
+def fwd_varlen_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                      cu_seqlens_k: torch.Tensor, max_seqlen_q: int, window: int, sinks: int = 0,
+                      scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      return_lse: bool = True, stream=None):
+    """fwd_window over a variable-length batch packed back to back.
+
+    q: [total_q, Hq, D]; k, v: [total_k, Hkv, D], contiguous; cu_seqlens_q, cu_seqlens_k: int32
+    [nseq + 1] offsets on the device; max_seqlen_q: a host int >= every query length, as
+    sdp_fwd_varlen. A sequence's query rows are its last positions. Returns (o like q, lse fp32
+    [Hq, total_q] or None). Bad offsets show in poll_status().
+    """
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k, v must be 3-D [tokens, heads, D]")
+    dev = q.get_device()
+    dt = _DTYPE_CODE.get(q.dtype)
+    if dev < 0 or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k, v must be CUDA tensors on one device")
+    if dt is None or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k, v must share one dtype, float16 or bfloat16")
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()):
+        raise ValueError("q, k, v must be contiguous")
+    _no_grad(q, k, v)
+    total_q, Hq, D = q.shape
+    kshape = k.shape
+    if kshape[2] != D or v.shape != kshape:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    n = cu_seqlens_q.shape[0] if cu_seqlens_q.dim() == 1 else 0
+    if n < 2:
+        raise ValueError("sequence offsets must be 1-D [nseq + 1]")
+    cu_q, cu_k = _int32("cu_seqlens_q", cu_seqlens_q, n, dev), _int32("cu_seqlens_k", cu_seqlens_k, n, dev)
+    out, lse = _outputs(q, out, lse, return_lse, (Hq, total_q), dev, stream)
+    with _on(dev):
+        rc = _lib().sdp_fwd_varlen_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                          0 if lse is None else lse.data_ptr(), cu_q, cu_k, n - 1, Hq, kshape[1],
+                                          total_q, kshape[0], max_seqlen_q, D,
+                                          1.0 / math.sqrt(D) if scale is None else scale, dt, window, sinks,
+                                          _stream_handle(stream, dev))
     if rc != SDP_OK:
         _check(rc)
     return out, lse

@@ -301,7 +301,7 @@ int sdp_qk_norm_rope(const void *q, long long q_sb, long long q_ss, long long q_
  *
  * sdp_cache4_gather — reads sequences back as 16-bit rows (fp32 value, rounded once): row
  * cu[i] + t of k and v becomes token t of sequence i. Rows in no sequence are not written.
- * For a prefill over a cached prefix: gather, then attend over the packed rows.
+ * For a prefill over a cached prefix: gather, then sdp_fwd_varlen_window.
  *
  * Offsets that decrease or leave [0, tokens], lengths below the new rows or past
  * max_pages * page_size (SDP_ERR_BAD_SEQLENS) and pages outside the pool
@@ -344,6 +344,28 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
                    int num_pages, int page_size, const int *block_table, long long table_stride, int max_pages,
                    const int *cache_lens, void *o, float *lse, int nseq, int rows, int Hq, int Hkv, int D, float scale,
                    int dtype, int window, int sinks, void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/*
+ * sdp_fwd_window, sdp_fwd_varlen_window — sdp_fwd and sdp_fwd_varlen with a sliding
+ * window and first tokens that stay visible: row i of a sequence with sq query rows and
+ * skv keys is at position p = skv - sq + i (its rows are the last ones, so a chunk behind a
+ * cached prefix has its place; sdp_fwd_causal aligns at the top instead) and sees the keys
+ * j <= p with j > p - window or j < sinks. A row that sees none (p < 0) gets O = 0 and
+ * LSE = -inf. window >= 1 and sinks >= 0; a window of skv or more is plain causal attention.
+ * Tiles of 128 keys outside a query tile's window are not read.
+ *
+ * Layouts, ownership, errors and streams as sdp_fwd and sdp_fwd_varlen (offsets are checked by
+ * the kernel and reported by sdp_poll_status); fewer than 2^30 rows or keys. Keys and values
+ * that a row does not see may hold infinities or NaN: they do not reach it. In a batch of up to
+ * 512 sequences the work is the tiles that exist, beyond that the longest sequence's for each. A
+ * launch runs the same kernel when it is captured; nothing is allocated after the first call on a
+ * device. The wait limit and debug flags 1, 4 and 32 apply.
+ */
+int sdp_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq, int Hkv, int Sq,
+                   int Skv, int D, float scale, int dtype, int window, int sinks, void *stream);
+int sdp_fwd_varlen_window(const void *q, const void *k, const void *v, void *o, float *lse, const int *cu_seqlens_q,
+                          const int *cu_seqlens_k, int nseq, int Hq, int Hkv, int total_q, int total_k,
+                          int max_seqlen_q, int D, float scale, int dtype, int window, int sinks, void *stream);
 
 /*
  * sdp_poll_status — synchronise `stream`, then read and clear the current
