@@ -2,31 +2,36 @@
 // 16-bit rows (cache4.cuh has the layout).
 //
 // Writing a group of 64 channels x_c:  b = bf16(min x),  s = bf16(max(0, (max x - b) / 15)),
-// n_c = clamp(rint((x_c - b) / s), 0, 15), 0 where s = 0. The quotient is a true division: inputs
-// of few bits often lie exactly on a border between two codes, where a product with 1 / s falls
-// on either side.
+// n_c = clamp(rint((x_c - b) / s), 0, 15), 0 where s = 0. The quotient is correctly rounded: inputs
+// of few bits often lie exactly on a border between two codes, where a product with 1 / s alone
+// falls on either side. One correctly rounded reciprocal serves the group, and each quotient is
+// corrected by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): three operations an element where a division takes a dozen. The
+// extremes are found on the 16-bit pairs as loaded, minimum and negated maximum in one register.
 //
-// Both kernels are HBM-bound elementwise passes: a warp takes one token and runs over its 2 Hkv
-// rows (K heads, then V heads), D/8 lanes a row, each lane one 16-byte access on the 16-bit side
-// and one 4-byte word of eight codes on the other, so a row's codes are one 64- or 128-byte
-// access. The token's sequence and page are looked up once a warp.
+// Both kernels are HBM-bound elementwise passes: a warp takes a few consecutive tokens and runs over
+// their 2 Hkv rows each (K heads, then V heads), D/8 lanes a row, each lane one 16-byte access on
+// the 16-bit side and one 4-byte word of eight codes on the other, so a row's codes are one 64- or
+// 128-byte access. Each lane looks up the place of one of the warp's tokens (a chain of dependent
+// loads, which one token a warp left exposed: 131 us for 39253 tokens written and read back).
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 #include "cache4.cuh"
+#include "ptx.cuh"
 #include "sdp.h"
 #include "sixteen.cuh"
 
 namespace {
 
 using sdp::Cache4View;
-using sdp::find_sequence;
-using sdp::pack8;
+using sdp::mul2;
 using sdp::unpack8;
 
 constexpr int kWarps = 4;
 constexpr int kUnroll = 4;
+constexpr int kMaxPasses = 32;  // of a warp that takes several tokens
 constexpr unsigned FULL = 0xffffffffu;
 
 struct RowsParams {
@@ -36,52 +41,54 @@ struct RowsParams {
     const int *cu, *lens;              // gather: lens is null, rows of a sequence are its tokens from 0
     unsigned int *status;
     int nseq, tokens;
-    int rows_per_warp;
+    int tokens_per_warp;  // consecutive tokens a warp takes, up to 32
+    int per_warp;         // passes of a token that a warp runs through
 };
 
-// A minimum / maximum that keeps NaN (fminf would drop it).
-__device__ __forceinline__ float min_nan(float a, float b)
+// Where this lane's token (token0 + lane, one of `n`) lives, as its row of head 0 in the pool's
+// [pages * Hkv * page_size] rows; -1 where it is in no sequence, or (with a status code) for bad offsets and
+// pages outside the pool. Called by a whole warp: the first token's sequence is searched by all lanes
+// together, 32 candidates a step (two trips to memory for 1024 sequences); the others' are near it.
+__device__ __forceinline__ long long locate(const RowsParams &p, int token0, int n, int lane)
 {
-    float d;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
-
-// Where a token lives: false (and a status code) for bad offsets or a page outside the pool.
-__device__ __forceinline__ bool locate(const RowsParams &p, int token, int lane, long long *page, int *place)
-{
-    const int s = find_sequence(p.cu, p.nseq, token, lane);
-    if (s >= p.nseq)
-        return false;  // in no sequence: left as it is
-    const int first = __ldg(p.cu + s), end = __ldg(p.cu + s + 1);
-    bool ok = first >= 0 && end <= p.tokens;
+    int lo = 0;
+    for (int len = p.nseq; len > 1;) {  // the last sequence that begins at or before token0 lies in [lo, lo + len)
+        const int step = (len + 31) / 32;
+        const bool before = lane * step < len && __ldg(p.cu + lo + lane * step) <= token0;
+        const unsigned m = __ballot_sync(FULL, before);
+        const int used = m == 0u ? 0 : (31 - __clz(m)) * step;
+        lo += used;
+        len = min(step, len - used);
+    }
+    const int token = token0 + lane;
+    if (lane >= n)
+        return -1;
+    int next = __ldg(p.cu + lo + 1);
+    while (token >= next && lo + 1 < p.nseq)  // over empty sequences too
+        next = __ldg(p.cu + ++lo + 1);
+    if (token < __ldg(p.cu + lo))
+        return -1;
+    const int first = __ldg(p.cu + lo), end = next;
+    if (token >= end)
+        return -1;  // in no sequence: left as it is
+    bool ok = first >= 0 && end <= p.tokens && first <= token;
     int pos = ok ? token - first : 0;
     if (ok && p.lens != nullptr) {
-        const int before = __ldg(p.lens + s) - (end - first);  // tokens that were there already
+        const int before = __ldg(p.lens + lo) - (end - first);  // tokens that were there already
         ok = before >= 0;
         pos = ok && pos <= INT32_MAX - before ? pos + before : INT32_MAX;
     }
     const int slot = ok ? pos / p.c.page_size : 0;
     if (!ok || slot >= p.c.max_pages) {
-        if (lane == 0)
-            atomicCAS(p.status, 0u, sdp::kBadSeqlens);
-        return false;
+        atomicCAS(p.status, 0u, sdp::kBadSeqlens);
+        return -1;
     }
-    const int id = __ldg(p.c.table + s * p.c.table_stride + slot);
+    const int id = __ldg(p.c.table + lo * p.c.table_stride + slot);
     if (id < 0 || id >= p.c.num_pages) {
-        if (lane == 0)
-            atomicCAS(p.status, 0u, sdp::kBadPages);
-        return false;
+        atomicCAS(p.status, 0u, sdp::kBadPages);
+        return -1;
     }
-    *page = id;
-    *place = pos - slot * p.c.page_size;
-    return true;
+    return static_cast<long long>(id) * p.c.Hkv * p.c.page_size + (pos - slot * p.c.page_size);
 }
 
 // Block 0 looks all offsets over: a token of a sequence with bad ones may belong to none.
@@ -96,99 +103,168 @@ __device__ __forceinline__ void check_offsets(const RowsParams &p)
     }
 }
 
+// A warp's share: tokens [token0, + n) and of each the passes [pass0, pass1), RPP rows a pass (K's
+// heads, then V's). Passes are numbered through, token by token.
 template <int D>
-struct WarpItem {
+struct Share {
     static constexpr int LPR = D / 8, RPP = 32 / LPR;
-    int token, r0, r1;
-    bool valid;
-    __device__ __forceinline__ explicit WarpItem(const RowsParams &p)
+    int token0, pass0, per_token, count;
+    int passes_k;  // K's passes of a token (V's are as many)
+    __device__ __forceinline__ explicit Share(const RowsParams &p)
     {
-        const int rows = 2 * p.c.Hkv;
-        const int runs = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
+        passes_k = (p.c.Hkv + RPP - 1) / RPP;
+        const int runs = (2 * passes_k + p.per_warp - 1) / p.per_warp;
         const long long item = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-        valid = item < static_cast<long long>(p.tokens) * runs;
-        token = static_cast<int>(item / runs);
-        r0 = static_cast<int>(item - static_cast<long long>(token) * runs) * p.rows_per_warp;
-        r1 = min(rows, r0 + p.rows_per_warp);
+        const long long group = item / runs;
+        pass0 = static_cast<int>(item - group * runs) * p.per_warp;
+        per_token = min(2 * passes_k, pass0 + p.per_warp) - pass0;
+        const long long t0 = group * p.tokens_per_warp;
+        token0 = static_cast<int>(min(static_cast<long long>(p.tokens), t0));
+        count = min(p.tokens_per_warp, p.tokens - token0) * per_token;
+    }
+    __device__ __forceinline__ int tokens() const { return count / per_token; }
+};
+
+// A place in a share's passes: the token (index in the share), K or V, and this lane's head (-1 past the last).
+template <int D>
+struct Cursor {
+    int token, y;
+    __device__ __forceinline__ explicit Cursor(const Share<D> &sh) : token(0), y(sh.pass0) {}
+    __device__ __forceinline__ void next(const Share<D> &sh)
+    {
+        if (++y == sh.pass0 + sh.per_token) {
+            y = sh.pass0;
+            ++token;
+        }
+    }
+    __device__ __forceinline__ bool is_k(const Share<D> &sh) const { return y < sh.passes_k; }
+    __device__ __forceinline__ int head(const RowsParams &p, const Share<D> &sh, int sub) const
+    {
+        const int h = (y < sh.passes_k ? y : y - sh.passes_k) * Share<D>::RPP + sub;
+        return h < p.c.Hkv ? h : -1;
     }
 };
+
+// Minimum of two pairs of 16-bit floats that keeps NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    if constexpr (BF16)
+        asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    else
+        asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// t / s correctly rounded, from the correctly rounded reciprocal of s.
+__device__ __forceinline__ float quotient(float t, float s, float inv)
+{
+    const float q = __fmul_rn(t, inv);
+    return __fmaf_rn(__fmaf_rn(-q, s, t), inv, q);
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsParams p)
 {
-    using W = WarpItem<D>;
+    using S = Share<D>;
     const int lane = threadIdx.x & 31;
     check_offsets(p);
-    const W it(p);
-    if (!it.valid)
+    const S sh(p);
+    if (sh.count <= 0)
         return;
-    const int sub = lane / W::LPR, c0 = (lane % W::LPR) * 8;
-    auto src = [&](int r) {
-        return reinterpret_cast<const uint4 *>(r < p.c.Hkv ? p.k + it.token * p.k_st + r * p.k_sh + c0
-                                                           : p.v + it.token * p.v_st + (r - p.c.Hkv) * p.v_sh + c0);
-    };
+    const int sub = lane / S::LPR, c0 = (lane % S::LPR) * 8;
     uint4 v[kUnroll];
-#pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-        const int r = it.r0 + i * W::RPP + sub;
-        if (r < it.r1)
-            v[i] = __ldg(src(r));
-    }
-    long long page;
-    int place;
-    if (!locate(p, it.token, lane, &page, &place))
-        return;
-    for (int r0 = it.r0; r0 < it.r1; r0 += kUnroll * W::RPP) {
-        if (r0 != it.r0) {
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int r = r0 + i * W::RPP + sub;
-                if (r < it.r1)
-                    v[i] = __ldg(src(r));
-            }
-        }
+    Cursor<D> ahead(sh), at(sh);
+    int to_load = sh.count;
+    auto load = [&]() {
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            if (r0 + i * W::RPP >= it.r1)
+            const int h = to_load > 0 ? ahead.head(p, sh, sub) : -1;
+            const long long t = sh.token0 + ahead.token;
+            v[i] = h < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                         : __ldg(reinterpret_cast<const uint4 *>(
+                               (ahead.is_k(sh) ? p.k + t * p.k_st + h * p.k_sh : p.v + t * p.v_st + h * p.v_sh) + c0));
+            ahead.next(sh);
+            --to_load;
+        }
+    };
+    load();
+    const long long my_row = locate(p, sh.token0, sh.tokens(), lane);
+    for (int x0 = 0; x0 < sh.count; x0 += kUnroll) {
+        uint4 now[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+            now[i] = v[i];
+        if (to_load > 0)
+            load();
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            if (x0 + i >= sh.count)
                 break;  // the same for the whole warp
-            const int r = r0 + i * W::RPP + sub;
-            const bool live = r < it.r1;
-            float x[8];
-            unpack8<BF16>(live ? v[i] : make_uint4(0u, 0u, 0u, 0u), x);
-            float lo = x[0], hi = x[0];
+            const long long row0 = __shfl_sync(FULL, my_row, at.token);
+            const int h = at.head(p, sh, sub);
+            const bool is_k = at.is_k(sh);
+            at.next(sh);
+            const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+            // (minimum, - maximum) of the group, in the type of the rows: exact
+            constexpr uint32_t SIGNS = 0x80008000u;
+            const uint32_t lo = min2_nan<BF16>(min2_nan<BF16>(w[0], w[1]), min2_nan<BF16>(w[2], w[3]));
+            const uint32_t hi = min2_nan<BF16>(min2_nan<BF16>(w[0] ^ SIGNS, w[1] ^ SIGNS),
+                                               min2_nan<BF16>(w[2] ^ SIGNS, w[3] ^ SIGNS));
+            uint32_t both = min2_nan<BF16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 #pragma unroll
-            for (int e = 1; e < 8; ++e) {
-                lo = min_nan(lo, x[e]);
-                hi = max_nan(hi, x[e]);
-            }
+            for (int off = 4; off > 0; off >>= 1)  // eight lanes hold a group
+                both = min2_nan<BF16>(both, __shfl_xor_sync(FULL, both, off));
+            const float2 ends = sdp::unpack16<BF16>(both);
+            const uint32_t b16 = __bfloat16_as_ushort(__float2bfloat16_rn(ends.x));
+            const float b = __uint_as_float(b16 << 16);
+            const float span = __fsub_rn(-ends.y, b);
+            uint32_t codes = 0, s16;
+            if (span > 1e-28f && span < 1e30f) {
+                const float q15 = quotient(span, 15.f, 1.f / 15.f);
+                s16 = __bfloat16_as_ushort(__float2bfloat16_rn(q15));
+                const float s = __uint_as_float(s16 << 16), inv = __frcp_rn(s);
+                const uint64_t s2 = sdp::ptx::f2_pack(-s, -s), inv2 = sdp::ptx::f2_pack(inv, inv);
+                const uint64_t b2 = sdp::ptx::f2_pack(-b, -b), big = sdp::ptx::f2_pack(8388608.f, 8388608.f);
+                uint32_t bytes[4];
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1) {  // eight lanes hold a group
-                lo = min_nan(lo, __shfl_xor_sync(FULL, lo, off));
-                hi = max_nan(hi, __shfl_xor_sync(FULL, hi, off));
-            }
-            const __nv_bfloat16 b16 = __float2bfloat16_rn(lo);
-            const float b = __bfloat162float(b16);
-            const __nv_bfloat16 s16 = __float2bfloat16_rn(max_nan(__fdiv_rn(__fsub_rn(hi, b), 15.f), 0.f));
-            const float s = __bfloat162float(s16);
-            uint32_t codes = 0;
-            if (s != 0.f) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], b), s)), 0.f), 15.f);
-                    codes |= static_cast<uint32_t>(static_cast<int>(n)) << (4 * e);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = sdp::unpack16<BF16>(w[j]);
+                    const uint64_t t = sdp::ptx::f2_add(sdp::ptx::f2_pack(f.x, f.y), b2);
+                    uint64_t q = mul2(t, inv2);
+                    q = sdp::ptx::f2_fma(sdp::ptx::f2_fma(q, s2, t), inv2, q);  // t / s, correctly rounded
+                    float q0, q1;
+                    sdp::ptx::f2_unpack(q, q0, q1);
+                    // below 15.5 always (s >= (1 - 2^-9) span / 15); below 0 where b was rounded up. 2^23 + q
+                    // rounds to the code, ties to even
+                    const uint64_t r = sdp::ptx::f2_add(sdp::ptx::f2_pack(fmaxf(q0, 0.f), fmaxf(q1, 0.f)), big);
+                    float r0, r1;
+                    sdp::ptx::f2_unpack(r, r0, r1);
+                    bytes[j] = __float_as_uint(fmaf(r1 - 8388608.f, 16.f, r0));  // both codes in the low byte
+                }
+                codes = __byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040), __byte_perm(bytes[2], bytes[3], 0x0040),
+                                    0x5410);
+            } else {  // a constant group, a NaN, or a scale whose reciprocal or remainders leave fp32's range
+                const float q15 = __fdiv_rn(span, 15.f);
+                s16 = __bfloat16_as_ushort(__float2bfloat16_rn(q15 < 0.f ? 0.f : q15));  // NaN stays
+                const float s = __uint_as_float(s16 << 16);
+                if (s != 0.f) {
+                    float x[8];
+                    unpack8<BF16>(now[i], x);
+#pragma unroll 1
+                    for (int e = 0; e < 8; ++e) {
+                        const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], b), s)), 0.f), 15.f);
+                        codes |= static_cast<uint32_t>(static_cast<int>(n)) << (4 * e);
+                    }
                 }
             }
-            if (live) {
-                const bool is_k = r < p.c.Hkv;
-                const long long row = (page * p.c.Hkv + (is_k ? r : r - p.c.Hkv)) * p.c.page_size + place;
-                uint8_t *out = is_k ? p.c.k_codes : p.c.v_codes;
-                *reinterpret_cast<uint32_t *>(out + row * (D / 2) + c0 / 2) = codes;
-                if (c0 % sdp::kCacheGroup == 0) {
-                    uint32_t *sc = is_k ? p.c.k_scales : p.c.v_scales;
-                    sc[row * (D / sdp::kCacheGroup) + c0 / sdp::kCacheGroup] =
-                        static_cast<uint32_t>(__bfloat16_as_ushort(s16)) |
-                        (static_cast<uint32_t>(__bfloat16_as_ushort(b16)) << 16);
-                }
+            if (h >= 0 && row0 >= 0) {
+                const long long row = row0 + static_cast<long long>(h) * p.c.page_size;
+                *reinterpret_cast<uint32_t *>((is_k ? p.c.k_codes : p.c.v_codes) + row * (D / 2) + c0 / 2) = codes;
+                if (c0 % sdp::kCacheGroup == 0)
+                    (is_k ? p.c.k_scales : p.c.v_scales)[row * (D / sdp::kCacheGroup) + c0 / sdp::kCacheGroup] =
+                        s16 | (b16 << 16);
             }
         }
     }
@@ -197,44 +273,53 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kWarps) cache4_gather_kernel(const RowsParams p)
 {
-    using W = WarpItem<D>;
+    using S = Share<D>;
     const int lane = threadIdx.x & 31;
     check_offsets(p);
-    const W it(p);
-    if (!it.valid)
+    const S sh(p);
+    if (sh.count <= 0)
         return;
-    long long page;
-    int place;
-    if (!locate(p, it.token, lane, &page, &place))
-        return;
-    const int sub = lane / W::LPR, c0 = (lane % W::LPR) * 8;
-    for (int r0 = it.r0; r0 < it.r1; r0 += kUnroll * W::RPP) {
+    const long long my_row = locate(p, sh.token0, sh.tokens(), lane);
+    const int sub = lane / S::LPR, c0 = (lane % S::LPR) * 8;
+    Cursor<D> at(sh);
+    for (int x0 = 0; x0 < sh.count; x0 += kUnroll) {
         uint32_t codes[kUnroll], pair[kUnroll];
+        uint16_t *out[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int r = r0 + i * W::RPP + sub;
-            if (r < it.r1) {
-                const bool is_k = r < p.c.Hkv;
-                const long long row = (page * p.c.Hkv + (is_k ? r : r - p.c.Hkv)) * p.c.page_size + place;
+            const long long row0 = __shfl_sync(FULL, my_row, at.token & 31);
+            const int h = x0 + i < sh.count ? at.head(p, sh, sub) : -1;
+            const bool is_k = at.is_k(sh);
+            out[i] = nullptr;
+            if (h >= 0 && row0 >= 0) {
+                const long long row = row0 + static_cast<long long>(h) * p.c.page_size;
                 codes[i] = __ldg(reinterpret_cast<const uint32_t *>((is_k ? p.c.k_codes : p.c.v_codes) +
                                                                     row * (D / 2) + c0 / 2));
                 pair[i] = __ldg((is_k ? p.c.k_scales : p.c.v_scales) + row * (D / sdp::kCacheGroup) +
                                 c0 / sdp::kCacheGroup);
+                const long long t = sh.token0 + at.token;
+                out[i] = (is_k ? p.k + t * p.k_st + h * p.k_sh : p.v + t * p.v_st + h * p.v_sh) + c0;
             }
+            at.next(sh);
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-            const int r = r0 + i * W::RPP + sub;
-            if (r < it.r1) {
-                const float s = __uint_as_float(pair[i] << 16), b = __uint_as_float(pair[i] & 0xffff0000u);
-                float x[8];
+            if (out[i] == nullptr)
+                continue;
+            const float s = __uint_as_float(pair[i] << 16), b = __uint_as_float(pair[i] & 0xffff0000u);
+            const uint64_t s2 = sdp::ptx::f2_pack(s, s), b2 = sdp::ptx::f2_pack(b, b);
+            const uint64_t big = sdp::ptx::f2_pack(-8388608.f, -8388608.f);
+            uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)  // s * code is exact in fp32 (8 + 4 bits): one rounding, then the store's
-                    x[e] = fmaf(s, static_cast<float>((codes[i] >> (4 * e)) & 15u), b);
-                uint16_t *out = r < p.c.Hkv ? p.k + it.token * p.k_st + r * p.k_sh + c0
-                                            : p.v + it.token * p.v_st + (r - p.c.Hkv) * p.v_sh + c0;
-                *reinterpret_cast<uint4 *>(out) = pack8<BF16>(x);
+            for (int j = 0; j < 4; ++j) {
+                // a code as 2^23 + n less 2^23; s * n is exact in fp32 (8 + 4 bits): one rounding, then the store's
+                const uint64_t n = sdp::ptx::f2_pack(__uint_as_float(((codes[i] >> (8 * j)) & 15u) | 0x4b000000u),
+                                                     __uint_as_float(((codes[i] >> (8 * j + 4)) & 15u) | 0x4b000000u));
+                float lo, hi;
+                sdp::ptx::f2_unpack(sdp::ptx::f2_fma(s2, sdp::ptx::f2_add(n, big), b2), lo, hi);
+                o[j] = sdp::pack16<BF16>(lo, hi);
             }
+            *reinterpret_cast<uint4 *>(out[i]) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -287,8 +372,8 @@ int rows_params(RowsParams &p, const void *k_codes, const void *k_scales, const 
     return SDP_OK;
 }
 
-// Device, status word and the split of the rows over warps: one pass a warp while that leaves
-// SMs without a full set of warps, then as many rows as share a token's look-up.
+// Device, status word and the split of the passes over warps: one pass a warp while that leaves SMs
+// without a full set of warps, then a token's passes, then several tokens that share one look-up.
 int plan(RowsParams &p, int D, unsigned *blocks)
 {
     int dev = 0, sms = 0;
@@ -298,12 +383,16 @@ int plan(RowsParams &p, int D, unsigned *blocks)
     if ((rc = sdp::status_word(dev, &p.status)) != SDP_OK)
         return rc;
     const int rpp = 256 / D;
-    const long long rows = 2LL * p.c.Hkv, passes = (rows + rpp - 1) / rpp;
+    const long long passes = 2LL * ((p.c.Hkv + rpp - 1) / rpp);
     long long per = p.tokens * passes / (static_cast<long long>(sms) * 32);
-    per = per < 1 ? 1 : (per > passes ? passes : per);
-    p.rows_per_warp = static_cast<int>(per * rpp);
-    const long long runs = (rows + p.rows_per_warp - 1) / p.rows_per_warp;
-    const long long n = (p.tokens * runs + kWarps - 1) / kWarps;
+    per = per < 1 ? 1 : per;
+    p.per_warp = static_cast<int>(per < passes ? per : passes);
+    // enough passes a warp to pay for the look-up, while every SM keeps its warps
+    long long share = per / passes < kMaxPasses / passes ? per / passes : kMaxPasses / passes;
+    p.tokens_per_warp = static_cast<int>(share < 1 ? 1 : (share > 32 ? 32 : share));
+    const long long runs = (passes + p.per_warp - 1) / p.per_warp;
+    const long long groups = (static_cast<long long>(p.tokens) + p.tokens_per_warp - 1) / p.tokens_per_warp;
+    const long long n = (groups * runs + kWarps - 1) / kWarps;
     if (n > INT32_MAX)
         return SDP_ERR_OVERFLOW;
     *blocks = static_cast<unsigned>(n);

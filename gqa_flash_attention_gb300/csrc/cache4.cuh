@@ -30,27 +30,4 @@ struct Cache4View {
     int num_pages, page_size, max_pages, Hkv;
 };
 
-// Index s with cu[s] <= t < cu[s + 1] of non-decreasing offsets cu[0..n], found by all 32 lanes
-// together, 32 candidates a step (two trips to memory for up to 1024 sequences, where a binary
-// search makes ten); n when t lies outside. t is the same in every lane.
-__device__ __forceinline__ int find_sequence(const int *cu, int n, int t, int lane)
-{
-    int lo = 0, len = n;  // the answer lies in [lo, lo + len)
-    while (len > 0) {
-        const int step = (len + 31) / 32;
-        const int i = lo + lane * step;
-        // sequences that begin at or before t form a prefix of the candidates
-        const bool before = lane * step < len && __ldg(cu + i) <= t;
-        const unsigned m = __ballot_sync(0xffffffffu, before);
-        if (m == 0u)
-            return n;
-        const int used = (31 - __clz(m)) * step;
-        lo += used;
-        len = min(step, len - used);
-        if (step == 1)
-            break;
-    }
-    return lo < n && __ldg(cu + lo) <= t && t < __ldg(cu + lo + 1) ? lo : n;
-}
-
 }  // namespace sdp

@@ -18,22 +18,27 @@
 // far as u_i is, and its upper 32 bits, read as a signed number, are the angle in units of
 // 2^-31 half turns for sincospif. The product costs three integer multiplications.
 //
-// The work is HBM-bound: each element is read and written once. A warp takes one token and a
-// run of its heads, D/8 lanes a row with one 16-byte load each, kPassUnroll rows' loads in
-// flight; the token's R/2 cosines and sines are computed once for the run, spread over the
-// lanes, and read back from shared memory (with every lane computing its own eight pairs, four
-// lanes would compute each of them at D = 128).
+// The work is HBM-bound: each element is read and written once, and at full bandwidth an SM has
+// about 170 issue slots for a 512-byte pass of a warp. So what a row's channels share over a token's
+// heads is folded once: with A = w cos (w outside the rotation) and B = -+ w' sin for the partner's
+// weight w', an element is r * (A x + B x'), r the row's norm factor, in packed pairs of fp32; the
+// partner x' travels as it was loaded (four 32-bit shuffles a row). A warp takes one token and a run
+// of its passes (32 / (D / 8) rows of q or of k, one 16-byte load a lane), kPassUnroll passes' loads
+// in flight; the token's R/2 cosines and sines are computed once for the run, spread over the lanes,
+// and read back from shared memory. (With the weights applied and fp32 values shuffled row by row,
+// 39253 tokens of 34 heads at D = 256 took 348 us.)
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
+#include "ptx.cuh"
 #include "sdp.h"
 #include "sdp_internal.h"
 #include "sixteen.cuh"
 
 namespace {
 
-using sdp::pack8;
+using sdp::mul2;
 using sdp::unpack8;
 
 constexpr int kWarps = 4;
@@ -52,7 +57,8 @@ struct RopeParams {
     float mscale, eps;
     int S, Hq, Hkv, R;
     int tokens;         // B * S
-    int rows_per_warp;  // heads a warp runs through, in passes of 32 / (D / 8) rows
+    int passes_q, passes;  // of a token: q's, and q's and k's
+    int per_warp;          // passes a warp runs through
 };
 
 // w: eight weights at channel c0 of `base`, 16-bit or fp32.
@@ -75,36 +81,44 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     constexpr int RPP = 32 / LPR;  // rows a pass
     __shared__ float2 cs_all[kWarps][D / 2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int heads = p.Hq + p.Hkv;
-    const int runs = (heads + p.rows_per_warp - 1) / p.rows_per_warp;
+    const int runs = (p.passes + p.per_warp - 1) / p.per_warp;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;
     if (item >= static_cast<long long>(p.tokens) * runs)
         return;
     const int token = static_cast<int>(item / runs);
-    const int h0 = static_cast<int>(item - static_cast<long long>(token) * runs) * p.rows_per_warp;
-    const int h1 = min(heads, h0 + p.rows_per_warp);
+    const int pass0 = static_cast<int>(item - static_cast<long long>(token) * runs) * p.per_warp;
+    const int pass1 = min(p.passes, pass0 + p.per_warp);
     const int b = token / p.S, s = token - b * p.S;
     float2 *cs = cs_all[warp];
 
     const int sub = lane / LPR, c0 = (lane % LPR) * 8;
     const uint16_t *q = p.q + b * p.qs[0] + s * p.qs[1] + c0;
     const uint16_t *k = p.k + b * p.ks[0] + s * p.ks[1] + c0;
-    uint16_t *qo = p.q_out + b * p.qos[0] + s * p.qos[1] + c0;
-    uint16_t *ko = p.k_out + b * p.kos[0] + s * p.kos[1] + c0;
-    auto src = [&](int h) {
-        return reinterpret_cast<const uint4 *>(h < p.Hq ? q + h * p.qs[2] : k + (h - p.Hq) * p.ks[2]);
-    };
-    auto dst = [&](int h) {
-        return reinterpret_cast<uint4 *>(h < p.Hq ? qo + h * p.qos[2] : ko + (h - p.Hq) * p.kos[2]);
-    };
-    // the first rows' loads run while the angles are computed
+    // The run as a segment of q's heads and one of k's: first head, heads left from it.
+    const bool q_first = pass0 < p.passes_q;
+    const int end_q = min(pass1, p.passes_q);
+    const uint16_t *src;
+    long long step;
+    int left;  // rows from this lane's first on: live while > 0
     uint4 v[kPassUnroll];
+    auto load = [&]() {  // the next kPassUnroll passes' rows
 #pragma unroll
-    for (int i = 0; i < kPassUnroll; ++i) {
-        const int h = h0 + i * RPP + sub;
-        if (h < h1)
-            v[i] = *src(h);
-    }
+        for (int i = 0; i < kPassUnroll; ++i) {
+            v[i] = left > 0 ? *reinterpret_cast<const uint4 *>(src) : make_uint4(0u, 0u, 0u, 0u);
+            src += step;
+            left -= RPP;
+        }
+    };
+    auto open = [&](bool of_q) {
+        const int h0 = (of_q ? pass0 : max(0, pass0 - p.passes_q)) * RPP + sub;
+        const int h1 = of_q ? min(p.Hq, end_q * RPP) : min(p.Hkv, (pass1 - p.passes_q) * RPP);
+        step = (of_q ? p.qs[2] : p.ks[2]);
+        src = (of_q ? q : k) + h0 * step;
+        step *= RPP;
+        left = h1 - h0;
+        load();
+    };
+    open(q_first);  // the first rows' loads run while the angles are computed
 
     const int half = p.R / 2;
     if (half > 0) {
@@ -123,66 +137,120 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     // its channels and those R/2 away, which lane +- R/16 of the same row holds
     const bool turns_here = c0 < p.R;
     const bool upper = c0 >= half;
-    float cc[8], sn[8];
-    if (turns_here) {
+    const int partner_c0 = INTERLEAVED || !turns_here ? c0 : upper ? c0 - half : c0 + half;
+    const int partner = lane + (partner_c0 - c0) / 8;
+    uint64_t fa[4], fb[4];  // the factors A and B of the lane's channels, for q or for k
+    auto factors = [&](bool of_q) {
+        const void *wb = of_q ? p.wq : p.wk;
+        float w[8], wp[8], x[8], y[8];
+        if (wb != nullptr) {
+            load_weights<BF16, W32>(wb, c0, w);
+            load_weights<BF16, W32>(wb, partner_c0, wp);
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float2 t = INTERLEAVED ? cs[c0 / 2 + e / 2] : cs[(upper ? c0 - half : c0) + e];
-            cc[e] = t.x;
-            // the partner's sign: - sin for a pair's first channel, + sin for its second
-            sn[e] = (INTERLEAVED ? (e & 1) : upper) ? t.y : -t.y;
+            const float we = wb != nullptr ? w[e] : 1.f;
+            x[e] = we;
+            y[e] = 0.f;
+            if (turns_here) {
+                const float2 t = INTERLEAVED ? cs[c0 / 2 + e / 2] : cs[(upper ? c0 - half : c0) + e];
+                const float wo = wb != nullptr ? wp[INTERLEAVED ? e ^ 1 : e] : 1.f;
+                x[e] = we * t.x;
+                // the partner's sign: - sin for a pair's first channel, + sin for its second
+                y[e] = wo * ((INTERLEAVED ? (e & 1) : upper) ? t.y : -t.y);
+            }
         }
-    }
-    const int partner = turns_here ? (upper ? lane - half / 8 : lane + half / 8) : lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fa[i] = sdp::ptx::f2_pack(x[2 * i], x[2 * i + 1]);
+            fb[i] = sdp::ptx::f2_pack(y[2 * i], y[2 * i + 1]);
+        }
+    };
 
-    for (int h = h0; h < h1; h += kPassUnroll * RPP) {
-        if (h != h0) {
+    for (int seg = q_first ? 0 : 1; seg < 2; ++seg) {
+        const bool of_q = seg == 0;
+        const int passes = of_q ? end_q - pass0 : pass1 - max(pass0, p.passes_q);
+        if (passes <= 0)
+            break;
+        if (of_q != q_first)
+            open(of_q);
+        factors(of_q);
+        const bool normed = (of_q ? p.wq : p.wk) != nullptr;
+        const int h0 = (of_q ? pass0 : max(0, pass0 - p.passes_q)) * RPP + sub;
+        int live = (of_q ? min(p.Hq, end_q * RPP) : min(p.Hkv, (pass1 - p.passes_q) * RPP)) - h0;
+        uint16_t *dst = of_q ? p.q_out + b * p.qos[0] + s * p.qos[1] + h0 * p.qos[2] + c0
+                             : p.k_out + b * p.kos[0] + s * p.kos[1] + h0 * p.kos[2] + c0;
+        const long long dst_step = (of_q ? p.qos[2] : p.kos[2]) * RPP;
+        for (int pass = 0; pass < passes; pass += kPassUnroll) {
+            uint4 now[kPassUnroll];
+#pragma unroll
+            for (int i = 0; i < kPassUnroll; ++i)
+                now[i] = v[i];
+            if (pass + kPassUnroll < passes)
+                load();
 #pragma unroll
             for (int i = 0; i < kPassUnroll; ++i) {
-                const int hr = h + i * RPP + sub;
-                if (hr < h1)
-                    v[i] = *src(hr);
-            }
-        }
+                if (pass + i >= passes)
+                    break;  // the same for the whole warp
+                const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+                uint64_t x[4], y[4];
 #pragma unroll
-        for (int i = 0; i < kPassUnroll; ++i) {
-            if (h + i * RPP >= h1)
-                break;  // the same for the whole warp
-            const int hr = h + i * RPP + sub;
-            const bool live = hr < h1;
-            float x[8];
-            unpack8<BF16>(live ? v[i] : make_uint4(0u, 0u, 0u, 0u), x);
-            const void *wb = hr < p.Hq ? p.wq : p.wk;
-            if (p.wq != nullptr || p.wk != nullptr) {
-                float ss = 0.f;
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = sdp::unpack16<BF16>(w[j]);
+                    x[j] = sdp::ptx::f2_pack(f.x, f.y);
+                    y[j] = mul2(x[j], fa[j]);
+                }
+                if (half > 0) {
+                    uint32_t o[4];
+                    if constexpr (!INTERLEAVED) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    ss = fmaf(x[e], x[e], ss);
+                        for (int j = 0; j < 4; ++j)
+                            o[j] = __shfl_sync(FULL, w[j], partner);
+                    }
+                    if (turns_here) {  // outside the rotation B is no factor: 0 times an infinity is NaN
 #pragma unroll
-                for (int off = LPR / 2; off > 0; off >>= 1)
-                    ss += __shfl_xor_sync(FULL, ss, off);
-                if (wb != nullptr) {
+                        for (int j = 0; j < 4; ++j) {
+                            float2 f;
+                            if constexpr (INTERLEAVED) {
+                                float lo, hi;
+                                sdp::ptx::f2_unpack(x[j], lo, hi);
+                                f = make_float2(hi, lo);
+                            } else {
+                                f = sdp::unpack16<BF16>(o[j]);
+                            }
+                            y[j] = sdp::ptx::f2_fma(sdp::ptx::f2_pack(f.x, f.y), fb[j], y[j]);
+                        }
+                    }
+                }
+                if (normed) {
+                    uint64_t sq = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int j = 1; j < 4; ++j)
+                        sq = sdp::ptx::f2_fma(x[j], x[j], sq);
+                    float s0, s1;
+                    sdp::ptx::f2_unpack(sq, s0, s1);
+                    float ss = s0 + s1;
+#pragma unroll
+                    for (int off = LPR / 2; off > 0; off >>= 1)
+                        ss += __shfl_xor_sync(FULL, ss, off);
                     const float r = rsqrtf(ss * (1.f / D) + p.eps);
-                    float w[8];
-                    load_weights<BF16, W32>(wb, c0, w);
+                    const uint64_t rr = sdp::ptx::f2_pack(r, r);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] *= r * w[e];
+                    for (int j = 0; j < 4; ++j)
+                        y[j] = mul2(y[j], rr);
                 }
-            }
-            if (half > 0) {
-                float y[8];
+                uint32_t o[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    y[e] = INTERLEAVED ? x[e ^ 1] : __shfl_sync(FULL, x[e], partner);
-                if (turns_here) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        x[e] = fmaf(x[e], cc[e], y[e] * sn[e]);
+                for (int j = 0; j < 4; ++j) {
+                    float lo, hi;
+                    sdp::ptx::f2_unpack(y[j], lo, hi);
+                    o[j] = sdp::pack16<BF16>(lo, hi);
                 }
+                if (live > 0)
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+                dst += dst_step;
+                live -= RPP;
             }
-            if (live)
-                *dst(hr) = pack8<BF16>(x);
         }
     }
 }
@@ -273,14 +341,17 @@ extern "C" int sdp_qk_norm_rope(const void *q, long long q_sb, long long q_ss, l
     p.Hkv = Hkv;
     p.R = rot_dim;
     p.tokens = static_cast<int>(tokens);
-    // Rows a warp: one pass while that leaves SMs without a full set of warps, then as many as
-    // share a token's angles.
+    // Passes a warp: one while that leaves SMs without a full set of warps, then as many as share a
+    // token's angles and factors.
     const int rpp = 256 / D;
-    const long long passes = (heads + rpp - 1) / rpp;
+    const long long passes_q = (Hq + static_cast<long long>(rpp) - 1) / rpp;
+    const long long passes = passes_q + (Hkv + static_cast<long long>(rpp) - 1) / rpp;
     long long per = tokens * passes / (static_cast<long long>(sms) * 32);
     per = per < 1 ? 1 : (per > passes ? passes : per);
-    p.rows_per_warp = static_cast<int>(per * rpp);
-    const long long runs = (heads + p.rows_per_warp - 1) / p.rows_per_warp;
+    p.passes_q = static_cast<int>(passes_q);
+    p.passes = static_cast<int>(passes);
+    p.per_warp = static_cast<int>(per);
+    const long long runs = (passes + per - 1) / per;
     const long long blocks = (tokens * runs + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX)
         return SDP_ERR_OVERFLOW;

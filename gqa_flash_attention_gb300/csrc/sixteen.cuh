@@ -51,4 +51,12 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8])
                       pack16<BF16>(x[6], x[7]));
 }
 
+// a * b on packed pairs of fp32, each rounded as a scalar product.
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 }  // namespace sdp
