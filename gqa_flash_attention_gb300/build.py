@@ -1,5 +1,6 @@
 """Builds libsdp.so in-tree: one nvcc process per translation unit, in
-parallel, for sm_103a only, then a shared-library link.
+parallel, for sm_103a only, then a shared-library link; and beside it the
+serving operators' Python binding (_serving.so, C++ against this torch).
 
     python -m gqa_flash_attention_gb300.build [--force]
 """
@@ -16,6 +17,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libsdp.so")
+BINDING_SRC = os.path.join(PKG, "binding", "binding.cpp")
+BINDING = os.path.join(PKG, "_serving.so")
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,21 +47,59 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> str:
+    """The binding's object file; linked once libsdp.so is there."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    obj = os.path.join(BUILD, "binding.o")
+    includes = [INCLUDE, sysconfig.get_paths()["include"], *cpp_extension.include_paths(), _cuda_include()]
+    cmd = [os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in includes), "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {BINDING_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _cuda_include() -> str:
+    import shutil
+    nvcc = shutil.which(NVCC)
+    return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include") if nvcc else ""
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{PKG}", "-l:libsdp.so", "-Wl,-rpath,$ORIGIN",
+           f"-L{lib}", f"-Wl,-rpath,{lib}", "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking {BINDING} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False) -> str:
-    """Compile every CUDA source for sm_103a and link gqa_flash_attention_gb300/libsdp.so."""
-    if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(p) for p in _deps())
-        if os.path.getmtime(LIB) >= newest:
+    """Compile every CUDA source for sm_103a, link gqa_flash_attention_gb300/libsdp.so, and build the binding."""
+    if not force and os.path.exists(LIB) and os.path.exists(BINDING):
+        newest = max(os.path.getmtime(p) for p in [*_deps(), BINDING_SRC])
+        if min(os.path.getmtime(LIB), os.path.getmtime(BINDING)) >= newest:
             return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([NVCC, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 
