@@ -7,29 +7,40 @@
 // The G query heads of a KV head and the n rows are the columns of one problem per (sequence, KV
 // head): 8 * NT columns a CTA, so that the codes are unpacked once for all of them.
 //
-// Bound: HBM, 4.5 bits a channel once per KV head. The tensor work is small but the codes have to
-// pass through registers, so the kernel is built to keep the instructions per code few:
+// Bound: HBM, 4.5 bits a channel once per KV head. The tensor work is small, but the codes have to
+// pass through registers, so the kernel is built to keep the instructions per code few. Both
+// products run in fp16 whatever the type of q, because a code needs no arithmetic to be an fp16
+// number: two codes of a 32-bit word (channels c and c + 4: any pairing will do, the queries and
+// the output are laid out to match) are the subnormals n * 2^-24 after one "and", or n * 2^-20
+// where they lie four bits up, so eight codes take one shift and four "and"s. (bf16 has only seven
+// bits below its exponent: 128 + n took a shift a pair, a larger bias term and, for V, a
+// subtraction.)
 //
 //   K: value = s n + b per (token, 64 channels), so the score of a group is
 //        s * sum_c q_c n_c + b * sum_c q_c.
-//      Codes enter the MMA as they are: two of a 32-bit word (channels c and c + 4: any pairing
-//      will do, the queries are laid out to match) become a register by one shift and one and/or.
-//      bf16: 0x4300 | n is 128 + n exactly; the 128 is taken out with b (b - 128 s). fp16: n in
-//      the low bits is the subnormal n * 2^-24 exactly; s takes the 2^24.
-//   V: with the group's s folded into the weights, sum_t (p_t s_t) (n_tc - 8) + sum_t p_t (b_t + 8 s_t).
-//      n - 8 in bf16 is 128 + n less 136, exactly: O is a sum of many small terms of both signs, and
-//      with the 128 left in (and taken out at the end, as for a score) it lost up to 7e-3 of O over
-//      32768 keys. p_t s_t as two bf16 (high part and remainder, 2^-17 relative: fp16's range would
-//      not hold p s, and one bf16 would cost more than the output's rounding): in two MMAs, or where
-//      the live columns fill only half of the eight (up to four, TWICE) in one, with the high parts
-//      in columns 0-3 and the remainders of the same queries in columns 4-7.
-//   These MMAs bound the kernel: mma.sync takes 32 cycles a scheduler for one m16n8k16 here.
-//   S = K Q^T with 16 tokens by 8 columns (m16n8k16), O = V^T P with 16 channels by 8 columns:
-//   few columns fill the n side. p turns from S's layout (token rows) to P's (column rows) by
-//   movmatrix on the two halves of its 32 bits.
+//      A row of q comes as fp16 times a power of two that brings its largest channel into
+//      [2^14, 2^15), odd channels over 16: every bf16 or fp16 channel down to 2^-25 of the largest
+//      keeps all its bits, and the score's factor takes the power back. The bias terms come from
+//      one more MMA, in bf16, whose A operand is the (s, b) words as they lie in memory and whose B
+//      operand holds the group sums of q in three bf16 parts.
+//   V: with the group's s folded into the weights, sum_t (p_t s_t) n_tc + sum_t p_t b_t; the second
+//      sum stays in fp32. p s in fp16 is taken against a power of two S that bounds the scales seen
+//      so far (O is rescaled when one exceeds it, as for the running maximum): at the most 2^15,
+//      full precision down to 2^-20 S, and below that off by 2^-31 S at the most. One fp16 (2^-12 on
+//      average) for bf16 outputs, as fine as the weights of a prefill; for fp16 outputs, whose own
+//      rounding is no coarser, a second one holds what the first left out.
 //
-//   The bias terms of a score come from one more MMA, whose A operand is the (s, b) words as they lie
-//   in memory and whose B operand holds the group sums of q (times -128 for s in bf16) in bf16 parts.
+//   S = K Q^T with 16 tokens by 8 columns (m16n8k16), O = V^T P with 16 channels by 8 columns:
+//   few columns fill the n side. p s turns from S's layout (token rows) to P's (column rows) by one
+//   movmatrix.
+//
+// What bounds it now: with 64 ragged sequences of up to 4096 keys (D = 128, 4 columns) 80 % of the
+// time the integer units, the issue slots (60 % each) and the latency between dependent
+// instructions, at four warps a scheduler: O, the ring and a tile's fragments leave registers for
+// no more. DRAM is at 36 % and the tensor pipe at 14 %. (The products on tcgen05 with e4m3 codes, the
+// unpacked codes passing through tensor and shared memory between warps of different roles, took
+// 89 us there and 76 us for 8 x 16384 at D = 256, against 61.8 and 57.4: a tile's chain of hand-overs is longer
+// than its share of the copy rate, and neither two CTAs an SM nor deeper rings hid it.)
 //
 // Work split: all sequences' tiles of 32 tokens are numbered sequence by sequence, KV head by KV
 // head (each problem with OVERHEAD positions more for its start), and cut into equal runs, one a
@@ -82,7 +93,9 @@ constexpr int TILE = 32;     // tokens a warp step
 constexpr int OVERHEAD = 1;  // tiles that a problem's start and end cost as much as
 constexpr int MERGE_THREADS = 256;
 constexpr unsigned FULL = 0xffffffffu;
-constexpr float RESCALE = 8.f;
+constexpr float RESCALE = 8.f;               // weights stay below 2^8 of the reference
+constexpr float RANGE = 64.f;                // p = 1 with the largest scale is stored as 64 at most, so 2^8 of it fits fp16
+constexpr float CODE_UNIT = 16777216.f / RANGE;  // of an O accumulator: codes are n * 2^-24
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kSlotNeverFilled = 3;  // the status word's site of a load that did not land
 
@@ -122,7 +135,8 @@ __device__ __forceinline__ int busy_runs(const Cache4AttnParams &p, long long to
 // First position of run i.
 __device__ __forceinline__ long long run_start(long long total, int i, int n) { return total * i / n; }
 
-// Floats of one part in the workspace: O [columns][D], then m and l of each column, in all a
+// Floats of one part in the workspace: O [columns][D] (over its own l, so that no part is larger than the
+// values it joins), then m and l of each column, in all a
 // multiple of 4 (O is stored 16 bytes at a time) whatever the number of columns.
 template <int D>
 __host__ __device__ constexpr long long part_floats(int cols)
@@ -179,22 +193,29 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a)
     return d;
 }
 
-// Codes i of the two 16-bit halves of w as a pair of 16-bit floats (128 + n in bf16; the fp16
-// subnormal n * 2^-24 with magic 0).
-template <uint32_t MAGIC>
+// Codes i and i + 4 of a word as two fp16 numbers: the subnormals n * 2^-24 for even i, and n * 2^-20, with no
+// shift of their own, for odd i.
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, int i)
 {
-    return ((w >> (4 * i)) & 0x000f000fu) | MAGIC;
+    return (i < 2 ? w : w >> 8) & ((i & 1) ? 0x00f000f0u : 0x000f000fu);
 }
 
-// The same pair as bf16 n - 8.
-__device__ __forceinline__ uint32_t centred_pair(uint32_t w, int i)
+// Pairs of fp16: a * b, a * b + c.
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b)
 {
-    const uint32_t u = code_pair<0x43004300u>(w, i);
-    const uint32_t c = 0x43084308u;  // 136
-    __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), *reinterpret_cast<const __nv_bfloat162 *>(&c));
-    return *reinterpret_cast<uint32_t *>(&d);
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// The larger of each 16-bit half.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
 __device__ __forceinline__ float scale_of(uint32_t pair) { return __uint_as_float(pair << 16); }
 __device__ __forceinline__ float bias_of(uint32_t pair) { return __uint_as_float(pair & 0xffff0000u); }
@@ -264,21 +285,28 @@ __device__ __forceinline__ bool wait_slot(uint32_t bar, uint32_t parity, unsigne
 
 // One tile's scores to weights to O (see the top of the file). MASKED: some column does not see
 // some key of the tile, or the tile ends past the sequence.
-template <int D, bool BF16, int NT, bool TWICE>
+template <int D, bool BF16, int NT>
 struct Tile {
+    static constexpr int PARTS = BF16 ? 1 : 2;  // fp16 parts of a weight
+
     using P = c4::Plan<D, NT>;
     static constexpr int GQ = P::GQ;
-    float o[D / 16][NT][4], m[NT][2], l[NT][2], corr[NT][GQ];
+    float o[D / 16][NT][4], m[NT][2], l[NT][2], corr[NT][2][GQ];
+    float f[NT][2];         // of the columns: from a score's units to base 2
+    uint32_t s_bits;        // V's scales so far are at most this bf16, a power of two (or 0)
+    float x_mul;            // RANGE / it
 
     __device__ __forceinline__ void clear()
     {
+        s_bits = 0;
+        x_mul = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
             for (int gq = 0; gq < GQ; ++gq)
-                corr[nt][gq] = 0.f;
+                corr[nt][0][gq] = corr[nt][1][gq] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i)
                 o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
@@ -287,7 +315,7 @@ struct Tile {
 
     // s = scores in base 2 of the K tile at kc: rows ta, ta + 8 of each 16-token chunk, columns
     // 2 quad, 2 quad + 1.
-    __device__ __forceinline__ void scores(float (&s)[2][NT][4], const uint8_t *kc, const uint2 *qf, int lane, float c)
+    __device__ __forceinline__ void scores(float (&s)[2][NT][4], const uint8_t *kc, const uint2 *qf, int lane)
     {
         using namespace c4;
         const int row8 = lane >> 2, quad = lane & 3;
@@ -331,26 +359,17 @@ struct Tile {
 #pragma unroll
                 for (int mc = 0; mc < 2; ++mc) {
                     const uint32_t x = j < 2 ? wa[mc].x : wa[mc].y, y = j < 2 ? wb[mc].x : wb[mc].y;
-                    constexpr uint32_t MAGIC = BF16 ? 0x43004300u : 0u;
                     const int h = 2 * (j & 1);
-                    const uint32_t a0 = code_pair<MAGIC>(x, h), a1 = code_pair<MAGIC>(y, h);
-                    const uint32_t a2 = code_pair<MAGIC>(x, h + 1), a3 = code_pair<MAGIC>(y, h + 1);
+                    const uint32_t a0 = code_pair(x, h), a1 = code_pair(y, h);
+                    const uint32_t a2 = code_pair(x, h + 1), a3 = code_pair(y, h + 1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (BF16)
-                            mma_bf16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
-                        else
-                            mma_f16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16(acc[mc][nt], a0, a1, a2, a3, b[nt].x, b[nt].y);
                 }
             }
 #pragma unroll
             for (int mc = 0; mc < 2; ++mc) {
-                float sa = scale_of(ksc[(mc * 16 + ta) * GQ + gq]), sb = scale_of(ksc[(mc * 16 + ta + 8) * GQ + gq]);
-                if constexpr (!BF16) {
-                    sa *= 16777216.f;  // 2^24
-                    sb *= 16777216.f;
-                }
+                const float sa = scale_of(ksc[(mc * 16 + ta) * GQ + gq]), sb = scale_of(ksc[(mc * 16 + ta + 8) * GQ + gq]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     s[mc][nt][0] = fmaf(sa, acc[mc][nt][0], s[mc][nt][0]);
@@ -366,7 +385,7 @@ struct Tile {
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    s[mc][nt][i] *= c;
+                    s[mc][nt][i] *= f[nt][i & 1];
     }
 
     // Keys that a column does not see drop out: key tok0 + ... against positions first + r / G.
@@ -379,7 +398,7 @@ struct Tile {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int col = nt * 8 + 2 * quad + i;
-                const int at = first + min(p.n - 1, (r_base + (TWICE ? col & 3 : col)) / p.G);
+                const int at = first + min(p.n - 1, (r_base + col) / p.G);
                 const int from = p.window > 0 ? at - p.window : -1;  // keys past it are in the window
 #pragma unroll
                 for (int mc = 0; mc < 2; ++mc)
@@ -392,12 +411,10 @@ struct Tile {
             }
     }
 
-    // The running maximum moves when some score is more than RESCALE above it; then s becomes the
-    // weights in P's layout (rows quad + {0, 4, 8, 12} of each chunk, column row8).
-    __device__ __forceinline__ void weights(float (&s)[2][NT][4], int lane)
+    // The running maximum moves when some score is more than RESCALE above it; then s becomes the weights.
+    __device__ __forceinline__ void weights(float (&s)[2][NT][4])
     {
         using namespace c4;
-        const int row8 = lane >> 2;
         bool over = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -427,12 +444,11 @@ struct Tile {
                     o[i][nt][2] *= a[0];
                     o[i][nt][3] *= a[1];
                 }
-                // corr belongs to column row8, whose factor lanes with quad = row8 / 2 hold
-                const float x0 = __shfl_sync(FULL, a[0], row8 >> 1), x1 = __shfl_sync(FULL, a[1], row8 >> 1);
-                const float f = (row8 & 1) ? x1 : x0;
 #pragma unroll
-                for (int gq = 0; gq < GQ; ++gq)
-                    corr[nt][gq] *= f;
+                for (int gq = 0; gq < GQ; ++gq) {
+                    corr[nt][0][gq] *= a[0];
+                    corr[nt][1][gq] *= a[1];
+                }
             }
         }
 #pragma unroll
@@ -445,16 +461,10 @@ struct Tile {
                 const float p2 = ptx::ex2(s[mc][nt][2] - m0), p3 = ptx::ex2(s[mc][nt][3] - m1);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
-                const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
-                const uint32_t u2 = __float_as_uint(p2), u3 = __float_as_uint(p3);
-                const uint32_t l0 = movmatrix(__byte_perm(u0, u1, 0x5410));
-                const uint32_t h0 = movmatrix(__byte_perm(u0, u1, 0x7632));
-                const uint32_t l1 = movmatrix(__byte_perm(u2, u3, 0x5410));
-                const uint32_t h1 = movmatrix(__byte_perm(u2, u3, 0x7632));
-                s[mc][nt][0] = __uint_as_float(__byte_perm(l0, h0, 0x5410));
-                s[mc][nt][1] = __uint_as_float(__byte_perm(l0, h0, 0x7632));
-                s[mc][nt][2] = __uint_as_float(__byte_perm(l1, h1, 0x5410));
-                s[mc][nt][3] = __uint_as_float(__byte_perm(l1, h1, 0x7632));
+                s[mc][nt][0] = p0;
+                s[mc][nt][1] = p1;
+                s[mc][nt][2] = p2;
+                s[mc][nt][3] = p3;
             }
         }
     }
@@ -465,40 +475,114 @@ struct Tile {
     __device__ __forceinline__ void output(const float (&w)[2][NT][4], const uint8_t *vc, int lane)
     {
         using namespace c4;
-        const int row8 = lane >> 2, quad = lane & 3;
-        const uint32_t *vsc = reinterpret_cast<const uint32_t *>(vc + P::CODE);
+        const int row8 = lane >> 2, quad = lane & 3, ta = (row8 >> 1) + ((row8 & 1) << 2);
+        // ---- scales of the tokens ta, ta + 8 of each chunk, and their bound
+        uint32_t sb[2][2][GQ];
+        uint32_t top = 0;
+#pragma unroll
+        for (int mc = 0; mc < 2; ++mc)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint32_t *at = reinterpret_cast<const uint32_t *>(vc + P::CODE) + (mc * 16 + ta + 8 * x) * GQ;
+                if constexpr (GQ == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(at);
+                    sb[mc][x][0] = v.x, sb[mc][x][1] = v.y, sb[mc][x][2] = v.z, sb[mc][x][3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(at);
+                    sb[mc][x][0] = v.x, sb[mc][x][1] = v.y;
+                }
+                bool seen = !MASKED;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    seen |= w[mc][nt][2 * x] != 0.f || w[mc][nt][2 * x + 1] != 0.f;
+#pragma unroll
+                for (int gq = 0; gq < GQ; ++gq)
+                    top = max_halves(top, seen ? sb[mc][x][gq] : 0u);
+            }
+        if (__any_sync(FULL, (top & 0xffffu) > s_bits)) {  // (a scale below zero, too: its bits are above)
+            uint32_t mx = 0;
+#pragma unroll
+            for (int mc = 0; mc < 2; ++mc)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    bool seen = !MASKED;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        seen |= w[mc][nt][2 * x] != 0.f || w[mc][nt][2 * x + 1] != 0.f;
+#pragma unroll
+                    for (int gq = 0; gq < GQ; ++gq) {
+                        const uint32_t b = sb[mc][x][gq] & 0x7fffu;
+                        mx = max(mx, seen && b < 0x7f80u ? b : 0u);  // one that is not finite bounds nothing
+                    }
+                }
+            mx = __reduce_max_sync(FULL, mx);
+            if (mx > s_bits) {
+                // the power of two above it, kept where RANGE over it is a normal number
+                const uint32_t next = max(8u, min(254u, (mx >> 7) + 1)) << 7;
+                const float bound = __uint_as_float(next << 16), ratio = __uint_as_float(s_bits << 16) / bound;
+                s_bits = next;
+                x_mul = RANGE / bound;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            o[i][nt][x] *= ratio;
+            }
+        }
 #pragma unroll
         for (int mc = 0; mc < 2; ++mc) {
+            // the weights as two fp16, and where they are not 0
+            uint32_t hi[NT][2], lo[NT][2], live[NT][2];
+            if constexpr (PARTS == 2) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float p0 = w[mc][nt][2 * x], p1 = w[mc][nt][2 * x + 1];
+                        hi[nt][x] = pack16<false>(p0, p1);
+                        const float2 h = unpack16<false>(hi[nt][x]);
+                        lo[nt][x] = pack16<false>(p0 - h.x, p1 - h.y);
+                        if constexpr (MASKED)
+                            live[nt][x] = (p0 != 0.f ? 0xffffu : 0u) | (p1 != 0.f ? 0xffff0000u : 0u);
+                    }
+            }
 #pragma unroll
             for (int gq = 0; gq < GQ; ++gq) {
                 uint32_t v[4];
-                float sc[4], bi[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = mc * 16 + quad + 4 * i;
-                    v[i] = *reinterpret_cast<const uint32_t *>(vc + t * (D / 2) + gq * 32 + row8 * 4);
-                    const uint32_t pr = vsc[t * GQ + gq];
-                    sc[i] = scale_of(pr);
-                    bi[i] = fmaf(8.f, sc[i], bias_of(pr));
-                }
-                uint32_t hi[NT][2], lo[NT][2];
+                for (int i = 0; i < 4; ++i)
+                    v[i] = *reinterpret_cast<const uint32_t *>(vc + (mc * 16 + quad + 4 * i) * (D / 2) + gq * 32 + row8 * 4);
+                uint32_t pw[PARTS][NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float x[4];
+                for (int x = 0; x < 2; ++x) {
+                    const float sc = scale_of(sb[mc][x][gq]) * x_mul, bi = bias_of(sb[mc][x][gq]);
+                    const uint32_t s2 = PARTS == 2 ? pack16<false>(sc, sc) : 0u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float pi = w[mc][nt][i];
-                        const bool out = MASKED && pi == 0.f;
-                        x[i] = out ? 0.f : pi * sc[i];
-                        corr[nt][gq] = out ? corr[nt][gq] : fmaf(pi, bi[i], corr[nt][gq]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float y[2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        hi[nt][i] = pack16<true>(x[2 * i], x[2 * i + 1]);
-                        lo[nt][i] = pack16<true>(x[2 * i] - __uint_as_float(hi[nt][i] << 16),
-                                                 x[2 * i + 1] - __uint_as_float(hi[nt][i] & 0xffff0000u));
-                        if (TWICE && row8 >= 4)
-                            hi[nt][i] = lo[nt][i];
+                        for (int i = 0; i < 2; ++i) {
+                            const float pi = w[mc][nt][2 * x + i];
+                            const bool out = MASKED && pi == 0.f;
+                            if constexpr (PARTS == 1)
+                                y[i] = out ? 0.f : pi * sc;
+                            corr[nt][i][gq] = out ? corr[nt][i][gq] : fmaf(pi, bi, corr[nt][i][gq]);
+                        }
+                        if constexpr (PARTS == 1) {
+                            pw[0][nt][x] = movmatrix(pack16<false>(y[0], y[1]));
+                        } else {
+                            // w * s rounded, and what that left out
+                            uint32_t a = hmul2(hi[nt][x], s2);
+                            uint32_t b = hfma2(lo[nt][x], s2, hfma2(hi[nt][x], s2, a ^ 0x80008000u));
+                            if constexpr (MASKED) {
+                                a &= live[nt][x];
+                                b &= live[nt][x];
+                            }
+                            pw[0][nt][x] = movmatrix(a);
+                            pw[PARTS - 1][nt][x] = movmatrix(b);
+                        }
                     }
                 }
                 // halves of the words: codes 0-3 of two tokens, codes 4-7 of two tokens
@@ -508,21 +592,20 @@ struct Tile {
                 for (int mt = 0; mt < 4; ++mt) {
                     const uint32_t w01 = mt < 2 ? x01 : y01, w23 = mt < 2 ? x23 : y23;
                     const int h = 2 * (mt & 1);
-                    const uint32_t a0 = centred_pair(w01, h), a1 = centred_pair(w01, h + 1);
-                    const uint32_t a2 = centred_pair(w23, h), a3 = centred_pair(w23, h + 1);
+                    const uint32_t a0 = code_pair(w01, h), a1 = code_pair(w01, h + 1);
+                    const uint32_t a2 = code_pair(w23, h), a3 = code_pair(w23, h + 1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                        if constexpr (!TWICE)
-                            mma_bf16(o[gq * 4 + mt][nt], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
-                    }
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < PARTS; ++i)
+                            mma_f16(o[gq * 4 + mt][nt], a0, a1, a2, a3, pw[i][nt][0], pw[i][nt][1]);
                 }
             }
         }
     }
 };
 
-template <int D, bool BF16, int NT, bool TWICE>
+template <int D, bool BF16, int NT>
 __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kernel(const Cache4AttnParams p)
 {
     using namespace c4;
@@ -677,8 +760,7 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
 
     const int run = warp * gridDim.x + blockIdx.x;
     const int R = p.n * p.G;
-    Tile<D, BF16, NT, TWICE> t;
-    static_assert(!TWICE || NT == 1, "eight columns");
+    Tile<D, BF16, NT> t;
     for (; !w.done(); w.find(p)) {
         const int g = w.u / p.chunks, r_base = (w.u - g * p.chunks) * P::COLS;
         auto row_of = [&](int r) {  // the (sequence, row, head) row of column r in q, o and lse
@@ -688,34 +770,59 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         __syncwarp();
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int r = TWICE ? row8 & 3 : r_base + nt * 8 + row8;
+            const int r = r_base + nt * 8 + row8;
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (r < R ? row_of(r) : 0) * D) + quad * 2;
+            uint4 x[GQ][2];
+            float mx = 0.f;
+            bool odd = false;  // an infinity or a NaN
+#pragma unroll
+            for (int gq = 0; gq < GQ; ++gq)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    x[gq][j] = r < R ? __ldg(src + gq * 8 + j) : make_uint4(0u, 0u, 0u, 0u);
+                    float v[8];
+                    unpack8<BF16>(x[gq][j], v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        mx = fmaxf(mx, fabsf(v[i]));
+                        odd |= !(fabsf(v[i]) <= 3.4028235e38f);
+                    }
+                }
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, 2));
+            odd = (__ballot_sync(FULL, odd) >> (lane & ~3)) & 15u;
+            // The power of two that brings the row's largest into [2^14, 2^15): in fp16 every channel down to 2^-25
+            // of it keeps its 11 bits, a sixteenth of it, too.
+            const int ex = max(-126, min(126, 141 - static_cast<int>(__float_as_uint(mx) >> 23)));
+            const float factor = mx == 0.f || odd ? 1.f : __uint_as_float(static_cast<uint32_t>(ex + 127) << 23);
+            const float back = odd ? __uint_as_float(0x7fc00000u) : p.c * 16777216.f / factor;  // 2^24 of the codes
+            t.f[nt][0] = __shfl_sync(FULL, back, 8 * quad);
+            t.f[nt][1] = __shfl_sync(FULL, back, 8 * quad + 4);
             float sum[GQ];
 #pragma unroll
             for (int gq = 0; gq < GQ; ++gq) {
-                uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (r < R) {
-                    x[0] = __ldg(src + gq * 8);
-                    x[1] = __ldg(src + gq * 8 + 1);
-                }
                 float a = 0.f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    // channels (c, c + 4) pair up, as the codes of a word do
-                    qf[((gq * 4 + 2 * j) * NT + nt) * 32 + lane] =
-                        make_uint2(__byte_perm(x[j].x, x[j].z, 0x5410), __byte_perm(x[j].x, x[j].z, 0x7632));
-                    qf[((gq * 4 + 2 * j + 1) * NT + nt) * 32 + lane] =
-                        make_uint2(__byte_perm(x[j].y, x[j].w, 0x5410), __byte_perm(x[j].y, x[j].w, 0x7632));
-                    float f[8];
-                    unpack8<BF16>(x[j], f);
+                    float v[8];
+                    unpack8<BF16>(x[gq][j], v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        a += f[i];
+                    for (int i = 0; i < 8; ++i) {
+                        v[i] = odd ? 0.f : v[i] * factor;
+                        a += v[i];
+                    }
+                    // channels (c, c + 4) pair up, as the codes of a word do; odd ones meet codes times 16
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qf[((gq * 4 + 2 * j + i) * NT + nt) * 32 + lane] =
+                            make_uint2(pack16<false>(v[2 * i], v[2 * i + 4]),
+                                       pack16<false>(v[2 * i + 1] * 0.0625f, v[2 * i + 5] * 0.0625f));
                 }
                 a += __shfl_xor_sync(FULL, a, 1);
-                sum[gq] = a + __shfl_xor_sync(FULL, a, 2);
+                a += __shfl_xor_sync(FULL, a, 2);
+                sum[gq] = a * 5.9604644775390625e-8f;  // 2^-24
             }
-            // the bias step's B operand: k pair j holds (-128, 1) * part j / GQ of group j % GQ's sum
+            // the bias step's B operand: k pair j holds (0, part j / GQ of group j % GQ's sum)
 #pragma unroll
             for (int st = 0; st < P::BIAS_STEPS; ++st) {
                 uint32_t b[2];
@@ -730,7 +837,7 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
                     const float p0 = __bfloat162float(__float2bfloat16_rn(a));
                     const float p1 = __bfloat162float(__float2bfloat16_rn(a - p0));
                     const float part = which == 0 ? p0 : which == 1 ? p1 : which == 2 ? (a - p0) - p1 : 0.f;
-                    b[x] = pack16<true>(BF16 ? -128.f * part : 0.f, part);
+                    b[x] = pack16<true>(0.f, part);
                 }
                 qf[((P::KSTEPS + st) * NT + nt) * 32 + lane] = make_uint2(b[0], b[1]);
             }
@@ -748,11 +855,11 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
             float s[2][NT][4];
             if (!landed())
                 return;
-            t.scores(s, ring_p + slot * P::SLOT, qf, lane, p.c);
+            t.scores(s, ring_p + slot * P::SLOT, qf, lane);
             refill();
             if (!whole)
                 t.mask(s, p, tok0, first, r_base, lane);
-            t.weights(s, lane);
+            t.weights(s);
             if (!landed())
                 return;
             if (whole)
@@ -765,6 +872,7 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         // ---- the segment's result: a lane holds channels 8 row8 .. + 7 of each group, of columns
         // 2 quad and 2 quad + 1
         const bool direct = w.e0 == 0 && w.e1 == w.sp.count;
+        const float bound = __uint_as_float(t.s_bits << 16);
         // a part that continues a problem is this run's first segment, one that begins it its last
         float *part = p.workspace + (static_cast<long long>(run) * 2 + (w.e0 == 0 ? 1 : 0)) * part_floats<D>(p.part_cols);
 #pragma unroll
@@ -776,24 +884,20 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
                 for (int off = 4; off < 32; off <<= 1)
                     sum += __shfl_xor_sync(FULL, sum, off);
                 const int col = nt * 8 + 2 * quad + i, r = r_base + col;
-                const float inv = !direct ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key: 0 and -inf
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a row that sees no key: 0 and -inf
 #pragma unroll
                 for (int gq = 0; gq < GQ; ++gq) {
-                    float c = t.corr[nt][gq];
-                    c += __shfl_xor_sync(FULL, c, 1);
-                    c += __shfl_xor_sync(FULL, c, 2);
-                    c = __shfl_sync(FULL, c, 8 * quad + 4 * i);  // lanes with row8 = 2 quad + i hold this column's
+                    float c = t.corr[nt][i][gq];
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        c += __shfl_xor_sync(FULL, c, off);
                     float y[8];
 #pragma unroll
                     for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                        {
-                            float a = t.o[gq * 4 + mt][nt][2 * x + i];
-                            if constexpr (TWICE)  // columns + 4: the remainders
-                                a += __shfl_xor_sync(FULL, a, 2);
-                            y[2 * mt + x] = (a + c) * inv;
-                        }
+                        for (int x = 0; x < 2; ++x)  // odd channels' codes came times 16
+                            y[2 * mt + x] =
+                                fmaf(t.o[gq * 4 + mt][nt][2 * x + i] * (inv * (x == 0 ? CODE_UNIT : CODE_UNIT / 16.f)), bound, c * inv);
                     if (r >= R)
                         continue;
                     const int c0 = gq * kCacheGroup + row8 * 8;
@@ -830,28 +934,12 @@ __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const C
     constexpr int THREADS = MERGE_THREADS, WARPS = THREADS / 32, LANES = D / 4, GROUPS = THREADS / LANES;
     __shared__ long long both[2][WARPS];
     __shared__ float4 y_all[GROUPS][LANES];
-    __shared__ float l_all[GROUPS];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int per_seq = p.Hkv * p.chunks;
     const int col = blockIdx.x % p.part_cols, problem = blockIdx.x / p.part_cols;
     const int s = problem / per_seq, u = problem - s * per_seq;
     const int g = u / p.chunks, r = (u - g * p.chunks) * 8 * NT + col;
-    if (r >= p.n * p.G)
-        return;
     const Span sp = span_of(p, s);
-    const long long row = (static_cast<long long>(s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
-    if (sp.count == 0) {
-        if (sp.bad) {
-            if (tid == 0)
-                atomicCAS(p.status, 0u, kBadSeqlens);
-            return;
-        }
-        if (tid < D / 8)
-            reinterpret_cast<uint4 *>(p.o + row * D)[tid] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0 && p.lse != nullptr)
-            p.lse[row] = -INFINITY;
-        return;
-    }
     // positions before this sequence, and in all
     long long before = 0, total = 0;
     {
@@ -879,6 +967,24 @@ __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const C
     }
     before *= per_seq;
     total *= per_seq;
+    // What is above needs only the lengths and runs beside the attention's end. Every thread waits for that
+    // end: what follows on the stream waits for this kernel alone.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (r >= p.n * p.G)
+        return;
+    const long long row = (static_cast<long long>(s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
+    if (sp.count == 0) {
+        if (sp.bad) {
+            if (tid == 0)
+                atomicCAS(p.status, 0u, kBadSeqlens);
+            return;
+        }
+        if (tid < D / 8)
+            reinterpret_cast<uint4 *>(p.o + row * D)[tid] = make_uint4(0u, 0u, 0u, 0u);
+        if (tid == 0 && p.lse != nullptr)
+            p.lse[row] = -INFINITY;
+        return;
+    }
     // the problem's tiles, behind its OVERHEAD
     const long long u0 = before + u * problem_length(sp) + OVERHEAD, u1 = u0 + sp.count;
     const int busy = busy_runs(p, total);
@@ -891,29 +997,36 @@ __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const C
     auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * part_floats<D>(pc); };
     // every group finds the maximum for itself (its threads read the same words)
     const int grp = tid / LANES, c4x = tid % LANES;
-    float mx = -INFINITY;
-    for (int x = lane; x < parts; x += 32)
-        mx = fmaxf(mx, part(x)[pc * D + col]);
+    auto m_of = [&](int x) { return part(x)[pc * D + col]; };
+    auto l_of = [&](int x) { return part(x)[pc * (D + 1) + col]; };
+    const float m0 = lane < parts ? m_of(lane) : -INFINITY, l0 = lane < parts ? l_of(lane) : 0.f;
+    float mx = m0;
+    for (int x = lane + 32; x < parts; x += 32)
+        mx = fmaxf(mx, m_of(x));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+    // 1: the part holds 0, or NaN
+    auto weight = [&](float mw, float lw) { return (mw == -INFINITY ? 1.f : ptx::ex2(mw - mx)) * lw; };
+    float sum = weight(m0, l0);
+    for (int x = lane + 32; x < parts; x += 32)
+        sum += weight(m_of(x), l_of(x));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        sum += __shfl_xor_sync(FULL, sum, off);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
 #pragma unroll 4
     for (int x = grp; x < parts; x += GROUPS) {
         const float *src = part(x);
         const float4 t = reinterpret_cast<const float4 *>(src + col * D)[c4x];
-        const float mw = src[pc * D + col], lw = src[pc * (D + 1) + col];
-        const float f = mw == -INFINITY ? 1.f : ptx::ex2(mw - mx);  // 1: the part holds 0, or NaN
-        sum = fmaf(f, lw, sum);
+        const float f = weight(m_of(x), l_of(x)) * inv;
         y.x = fmaf(f, t.x, y.x);
         y.y = fmaf(f, t.y, y.y);
         y.z = fmaf(f, t.z, y.z);
         y.w = fmaf(f, t.w, y.w);
     }
     y_all[grp][c4x] = y;
-    if (c4x == 0)
-        l_all[grp] = sum;
     __syncthreads();
     if (grp != 0)
         return;
@@ -924,21 +1037,19 @@ __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const C
         y.y += t.y;
         y.z += t.z;
         y.w += t.w;
-        sum += l_all[i];
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     reinterpret_cast<uint2 *>(p.o + row * D)[c4x] =
-        make_uint2(pack16<BF16>(y.x * inv, y.y * inv), pack16<BF16>(y.z * inv, y.w * inv));
+        make_uint2(pack16<BF16>(y.x, y.y), pack16<BF16>(y.z, y.w));
     if (c4x == 0 && p.lse != nullptr)
         p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
-template <int D, bool BF16, int NT, bool TWICE>
+template <int D, bool BF16, int NT>
 cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
 {
     using P = c4::Plan<D, NT>;
     static unsigned long long done = 0;
-    auto kern = cache4_attn_kernel<D, BF16, NT, TWICE>;
+    auto kern = cache4_attn_kernel<D, BF16, NT>;
     cudaError_t e = set_smem_once(kern, P::BYTES, done);
     if (e != cudaSuccess)
         return e;
@@ -946,8 +1057,17 @@ cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
     kern<<<sms, P::THREADS, P::BYTES, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    cache4_merge_kernel<D, BF16, NT><<<p.nseq * p.Hkv * p.chunks * p.part_cols, c4::MERGE_THREADS, 0, st>>>(p);
-    return cudaGetLastError();
+    // the blocks of the join start where the attention's CTAs end, not when the last one has
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t config{};
+    config.gridDim = dim3(p.nseq * p.Hkv * p.chunks * p.part_cols);
+    config.blockDim = dim3(c4::MERGE_THREADS);
+    config.stream = st;
+    config.attrs = &early;
+    config.numAttrs = 1;
+    return cudaLaunchKernelEx(&config, cache4_merge_kernel<D, BF16, NT>, p);
 }
 
 // One per (head dim, dtype): 8 columns a warp up to that many, else 16.

@@ -6,10 +6,8 @@ namespace sdp {
 cudaError_t cache4_attn_d128_fp16(const Cache4AttnParams &p, int sms, cudaStream_t st)
 {
     const int columns = p.n * p.G;
-    if (columns <= 4)
-        return launch_cache4_attn<128, false, 1, true>(p, sms, st);
-    return columns <= 8 ? launch_cache4_attn<128, false, 1, false>(p, sms, st)
-                        : launch_cache4_attn<128, false, 2, false>(p, sms, st);
+    return columns <= 8 ? launch_cache4_attn<128, false, 1>(p, sms, st)
+                        : launch_cache4_attn<128, false, 2>(p, sms, st);
 }
 
 }  // namespace sdp

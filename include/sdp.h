@@ -333,8 +333,8 @@ int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_c
  *        the GPU (two graphs replayed at once need two); its contents do not matter
  *        before and are unspecified after.
  * Scores, weights and sums in fp32; the products take the 4-bit codes as they are and the
- * queries and weights in 16 bits (the weights as two bf16 parts). The same call gives the
- * same bits. A bad length leaves that sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a
+ * queries and weights in fp16 against powers of two that fit each row of q and the scales seen
+ * (one fp16 a weight for bf16 outputs, two for fp16). The same call gives the same bits. A bad length leaves that sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a
  * page outside the pool leaves them unspecified (SDP_ERR_BAD_PAGES), a wait that runs out
  * all rows (SDP_ERR_DEVICE_TIMEOUT). Two kernels are enqueued on `stream`. The workspace
  * size depends on the current device; a negative value is a status code.

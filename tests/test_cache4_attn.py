@@ -2,13 +2,17 @@
 against the definition in 64 bits on the very codes and scales.
 
 Tolerance, for a column with queries q and keys and values of scales sk, sv and values v: a score
-is the sum over groups of s * (sum q (128 + n)) + (b - 128 s) * sum q in bf16, and the same
-without the 128 in fp16, accumulated in fp32 by the tensor core (each step may drop a bit of the
-running sum's last place, 2^-23 of it; D / 16 steps a group and two more): with N = 143 or 16 the
-largest factor of q, its error is at most e = scale * sum_c |q_c| * max sk * N * 2^-19 + 2^-22 * |score|
-(scale, ex2 argument). Weights are then off by a factor 1 + 2 e at most, the stored value by
-    finfo.eps / 2 * |o|  (half a step)  +  2 e * max |v|  +  2^-17 * max |sv| * 143  (weights as two
-    bf16, sums of 128 + n)  +  2^-25 (fp16 subnormals),
+is the sum over groups of s * sum q n + b * sum q with n in 0..15, its products exact (11 bits by
+four, the row of q times a power of two; channels below 2^-25 of the largest are off by 2^-36 of it
+at most), accumulated in fp32 by the tensor core (each step may drop a bit of the running sum's last
+place, 2^-23 of it; D / 16 steps a group and two more): its error is at most
+e = scale * sum_c |q_c| * max sk * 16 * 2^-19 + 2^-22 * |score| (scale, ex2 argument). Weights are
+then off by a factor 1 + 2 e at most, the stored value by
+    finfo.eps / 2 * |o|  (half a step)  +  2 e * max |v|
+    + 15 max |sv| * (2^-11 for bf16: weights times scales in one fp16, half a step; 2^-21 for fp16: in
+      two)  +  15 max |sv| * 2^-14  (O's steps: at most 5120 / 16 here, 2^-23 each; with 2^-21 less
+      than 2^-14)  +  n keys * 15 * 2 max |sv| * 2^-31  (weights times scales among fp16's subnormals,
+      2^-25 of 64 for 2 max |sv|)  +  2^-25 (fp16 subnormals of the output),
 the log-sum-exp by e + 2^-20 * (1 + |lse|).
 """
 import math
@@ -110,7 +114,7 @@ def check(q, o, lse, lens, ks, vs, dtype, window=0, sinks=0, scale=None):
     rows, D = q.shape[1], q.shape[3]
     scale = 1 / math.sqrt(D) if scale is None else scale
     o, lse, q = o.double().cpu(), None if lse is None else lse.double().cpu(), q.cpu()
-    N = 143 if dtype == torch.bfloat16 else 16
+    W = 15 * (2.0 ** -11 + 2.0 ** -14 if dtype == torch.bfloat16 else 2.0 ** -14)
     for s, n in enumerate(lens):
         pos = torch.arange(n - rows, n)
         ro, rl = reference(q[s], ks[s][0], vs[s][0], pos, scale, window, sinks)
@@ -121,9 +125,9 @@ def check(q, o, lse, lens, ks, vs, dtype, window=0, sinks=0, scale=None):
         if n == 0:
             continue
         top = rl.masked_fill(none, 0).abs()
-        e = abs(scale) * q[s].double().abs().sum(-1) * ks[s][1].max() * N * 2.0 ** -19 + 2.0 ** -22 * (top + 20)
+        e = abs(scale) * q[s].double().abs().sum(-1) * ks[s][1].max() * 16 * 2.0 ** -19 + 2.0 ** -22 * (top + 20)
         tol = (torch.finfo(dtype).eps / 2 * ro.abs() + 2 * e[..., None] * vs[s][0].abs().max()
-               + 2.0 ** -17 * vs[s][1].max() * 143 + 2.0 ** -25)
+               + vs[s][1].max() * (W + n * 15 * 2.0 ** -30) + 2.0 ** -25)
         bad = ((o[s] - ro).abs() > tol) | torch.isnan(o[s])
         assert not bad.any(), (s, n, int(bad.sum()), (o[s] - ro).abs()[bad].max(), tol[bad].max())
         if lse is not None:
@@ -206,6 +210,43 @@ def test_scales_and_loud_keys(scale, dt):
     o, lse = sdp.fwd_cache4(q, cache, torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda(), scale=scale)
     assert sdp.poll_status() == sdp.SDP_OK
     check(q, o, lse, lens, ks, vs, dtype, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_scales_of_every_size(dt):
+    """Scales of V that grow, shrink, are 0, are below it (no quantiser gives one) and, in bf16, near the ends of
+    the range; rows of q of very different sizes."""
+    g = torch.Generator().manual_seed(21)
+    dtype, lens = DTYPES[dt], [700, 700, 90, 64]
+    cache, table, ks, vs = fill(lens, 1, 128, 16, dtype, g)
+    for s, n in enumerate(lens):
+        t = torch.arange(n)
+        sc = torch.rand(n, 2, generator=g) + 0.1
+        if s == 0:
+            sc = sc * 2.0 ** (t[:, None] / 50)
+        elif s == 1:
+            sc = sc * 2.0 ** (-t[:, None] / 20)
+        elif s == 2:
+            sc[t % 3 == 0] *= -4
+        else:
+            sc = torch.zeros_like(sc)
+        if dt == "bf16" and s < 2:
+            sc = sc * 2.0 ** (110 if s == 0 else -110)
+        at, off = table[s, t // 16].long().cuda(), (t % 16).cuda()
+        scales = cache.v_scales[at, 0, off].cpu()  # [n, 2 groups, (scale, bias)]
+        scales[..., 0] = sc.bfloat16()
+        cache.v_scales[at, 0, off] = scales.cuda()
+        codes = cache.v_codes[at, 0, off].cpu()
+        vs[s] = (values(codes, scales)[:, None], scales[..., 0].double().abs()[:, None])
+    q = torch.randn(4, 3, 4, 128, generator=g)
+    q[:, 1] *= 1e-4
+    q[:, 2, 1:3] *= torch.tensor([3e-8, 40.0])[:, None]
+    q = q.to(dtype).cuda()
+    o, lse = sdp.fwd_cache4(q, cache, torch.tensor(lens, dtype=torch.int32).cuda(), table.cuda())
+    assert sdp.poll_status() == sdp.SDP_OK
+    keep = [0, 1, 2, 3] if dt == "bf16" else [1, 2, 3]  # 15 * 2^14 and its sums are near fp16's end
+    check(q[keep], o[keep], lse[keep], [lens[i] for i in keep], [ks[i] for i in keep], [vs[i] for i in keep], dtype)
 
 
 @pytest.mark.gpu
