@@ -9,11 +9,15 @@
 // System/6000 processor", 1990): three operations an element where a division takes a dozen. The
 // extremes are found on the 16-bit pairs as loaded, minimum and negated maximum in one register.
 //
-// Both kernels are HBM-bound elementwise passes: a warp takes a few consecutive tokens and runs over
-// their 2 Hkv rows each (K heads, then V heads), D/8 lanes a row, each lane one 16-byte access on
-// the 16-bit side and one 4-byte word of eight codes on the other, so a row's codes are one 64- or
-// 128-byte access. Each lane looks up the place of one of the warp's tokens (a chain of dependent
-// loads, which one token a warp left exposed: 131 us for 39253 tokens written and read back).
+// Both kernels are elementwise passes over HBM, bounded in practice by their instructions (at 62529 tokens
+// of 2 heads of 256 channels, cold: 46 us written, 36 us read back, where the bytes alone take 23 us each; a
+// writer's group costs a reduction, a division and a reciprocal before its elements begin). A warp takes a few
+// consecutive tokens and runs over their 2 Hkv rows each (K heads, then V heads), D/16 lanes a row. A lane
+// holds two chunks of eight channels of one group, each one 16-byte access on the 16-bit side and one 4-byte
+// word of codes on the other, so that four lanes share what a group costs. (With one chunk a lane, eight
+// lanes a group, the two took 65 and 46 us; with four, 75 and 40: half the warps with twice the registers
+// leave the loads' latency open.) Each lane looks up the place of one of the warp's tokens (a chain of
+// dependent loads, which one token a warp left exposed).
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -30,8 +34,11 @@ using sdp::mul2;
 using sdp::unpack8;
 
 constexpr int kWarps = 4;
-constexpr int kUnroll = 4;
-constexpr int kMaxPasses = 32;  // of a warp that takes several tokens
+constexpr int kUnroll = 2;           // passes whose loads a warp issues at once
+constexpr int kChunks = 2;           // of eight channels a lane, all of one group
+constexpr int kLanes = 8 / kChunks;  // of a group
+constexpr int kStep = 8 * kLanes;    // channels from one of a lane's chunks to the next
+constexpr int kMaxPasses = 32;      // of a warp that takes several tokens
 constexpr unsigned FULL = 0xffffffffu;
 
 struct RowsParams {
@@ -107,7 +114,7 @@ __device__ __forceinline__ void check_offsets(const RowsParams &p)
 // heads, then V's). Passes are numbered through, token by token.
 template <int D>
 struct Share {
-    static constexpr int LPR = D / 8, RPP = 32 / LPR;
+    static constexpr int LPR = D / 64 * kLanes, RPP = 32 / LPR;
     int token0, pass0, per_token, count;
     int passes_k;  // K's passes of a token (V's are as many)
     __device__ __forceinline__ explicit Share(const RowsParams &p)
@@ -145,6 +152,13 @@ struct Cursor {
     }
 };
 
+// First of a lane's channels in its row: a group's lanes take its chunks of eight channels in turn, so that each
+// access of the lanes together is in one piece.
+__device__ __forceinline__ int first_channel(int lane_of_row)
+{
+    return lane_of_row / kLanes * sdp::kCacheGroup + lane_of_row % kLanes * 8;
+}
+
 // Minimum of two pairs of 16-bit floats that keeps NaN.
 template <bool BF16>
 __device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b)
@@ -173,8 +187,8 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
     const S sh(p);
     if (sh.count <= 0)
         return;
-    const int sub = lane / S::LPR, c0 = (lane % S::LPR) * 8;
-    uint4 v[kUnroll];
+    const int sub = lane / S::LPR, c0 = first_channel(lane % S::LPR);
+    uint4 v[kUnroll][kChunks];
     Cursor<D> ahead(sh), at(sh);
     int to_load = sh.count;
     auto load = [&]() {
@@ -182,9 +196,11 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
         for (int i = 0; i < kUnroll; ++i) {
             const int h = to_load > 0 ? ahead.head(p, sh, sub) : -1;
             const long long t = sh.token0 + ahead.token;
-            v[i] = h < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                         : __ldg(reinterpret_cast<const uint4 *>(
-                               (ahead.is_k(sh) ? p.k + t * p.k_st + h * p.k_sh : p.v + t * p.v_st + h * p.v_sh) + c0));
+            const uint16_t *src =
+                (ahead.is_k(sh) ? p.k + t * p.k_st + h * p.k_sh : p.v + t * p.v_st + h * p.v_sh) + c0;
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+                v[i][x] = h < 0 ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4 *>(src + x * kStep));
             ahead.next(sh);
             --to_load;
         }
@@ -192,10 +208,12 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
     load();
     const long long my_row = locate(p, sh.token0, sh.tokens(), lane);
     for (int x0 = 0; x0 < sh.count; x0 += kUnroll) {
-        uint4 now[kUnroll];
+        uint4 now[kUnroll][kChunks];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i)
-            now[i] = v[i];
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+                now[i][x] = v[i][x];
         if (to_load > 0)
             load();
 #pragma unroll
@@ -206,30 +224,36 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
             const int h = at.head(p, sh, sub);
             const bool is_k = at.is_k(sh);
             at.next(sh);
-            const uint32_t w[4] = {now[i].x, now[i].y, now[i].z, now[i].w};
+            uint32_t w[4 * kChunks];
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+                w[4 * x] = now[i][x].x, w[4 * x + 1] = now[i][x].y, w[4 * x + 2] = now[i][x].z, w[4 * x + 3] = now[i][x].w;
             // (minimum, - maximum) of the group, in the type of the rows: exact
             constexpr uint32_t SIGNS = 0x80008000u;
-            const uint32_t lo = min2_nan<BF16>(min2_nan<BF16>(w[0], w[1]), min2_nan<BF16>(w[2], w[3]));
-            const uint32_t hi = min2_nan<BF16>(min2_nan<BF16>(w[0] ^ SIGNS, w[1] ^ SIGNS),
-                                               min2_nan<BF16>(w[2] ^ SIGNS, w[3] ^ SIGNS));
+            uint32_t lo = w[0], hi = w[0] ^ SIGNS;
+#pragma unroll
+            for (int j = 1; j < 4 * kChunks; ++j) {
+                lo = min2_nan<BF16>(lo, w[j]);
+                hi = min2_nan<BF16>(hi, w[j] ^ SIGNS);
+            }
             uint32_t both = min2_nan<BF16>(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 #pragma unroll
-            for (int off = 4; off > 0; off >>= 1)  // eight lanes hold a group
+            for (int off = kLanes / 2; off > 0; off >>= 1)
                 both = min2_nan<BF16>(both, __shfl_xor_sync(FULL, both, off));
             const float2 ends = sdp::unpack16<BF16>(both);
             const uint32_t b16 = __bfloat16_as_ushort(__float2bfloat16_rn(ends.x));
             const float b = __uint_as_float(b16 << 16);
             const float span = __fsub_rn(-ends.y, b);
-            uint32_t codes = 0, s16;
+            uint32_t codes[kChunks] = {}, s16;
             if (span > 1e-28f && span < 1e30f) {
                 const float q15 = quotient(span, 15.f, 1.f / 15.f);
                 s16 = __bfloat16_as_ushort(__float2bfloat16_rn(q15));
                 const float s = __uint_as_float(s16 << 16), inv = __frcp_rn(s);
                 const uint64_t s2 = sdp::ptx::f2_pack(-s, -s), inv2 = sdp::ptx::f2_pack(inv, inv);
                 const uint64_t b2 = sdp::ptx::f2_pack(-b, -b), big = sdp::ptx::f2_pack(8388608.f, 8388608.f);
-                uint32_t bytes[4];
+                uint32_t bytes[4 * kChunks];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
+                for (int j = 0; j < 4 * kChunks; ++j) {
                     const float2 f = sdp::unpack16<BF16>(w[j]);
                     const uint64_t t = sdp::ptx::f2_add(sdp::ptx::f2_pack(f.x, f.y), b2);
                     uint64_t q = mul2(t, inv2);
@@ -243,25 +267,33 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_append_kernel(const RowsPa
                     sdp::ptx::f2_unpack(r, r0, r1);
                     bytes[j] = __float_as_uint(fmaf(r1 - 8388608.f, 16.f, r0));  // both codes in the low byte
                 }
-                codes = __byte_perm(__byte_perm(bytes[0], bytes[1], 0x0040), __byte_perm(bytes[2], bytes[3], 0x0040),
-                                    0x5410);
+#pragma unroll
+                for (int x = 0; x < kChunks; ++x)
+                    codes[x] = __byte_perm(__byte_perm(bytes[4 * x], bytes[4 * x + 1], 0x0040),
+                                           __byte_perm(bytes[4 * x + 2], bytes[4 * x + 3], 0x0040), 0x5410);
             } else {  // a constant group, a NaN, or a scale whose reciprocal or remainders leave fp32's range
                 const float q15 = __fdiv_rn(span, 15.f);
                 s16 = __bfloat16_as_ushort(__float2bfloat16_rn(q15 < 0.f ? 0.f : q15));  // NaN stays
                 const float s = __uint_as_float(s16 << 16);
                 if (s != 0.f) {
-                    float x[8];
-                    unpack8<BF16>(now[i], x);
+#pragma unroll
+                    for (int x = 0; x < kChunks; ++x) {
+                        float f[8];
+                        unpack8<BF16>(now[i][x], f);
 #pragma unroll 1
-                    for (int e = 0; e < 8; ++e) {
-                        const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], b), s)), 0.f), 15.f);
-                        codes |= static_cast<uint32_t>(static_cast<int>(n)) << (4 * e);
+                        for (int e = 0; e < 8; ++e) {
+                            const float n = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(f[e], b), s)), 0.f), 15.f);
+                            codes[x] |= static_cast<uint32_t>(static_cast<int>(n)) << (4 * e);
+                        }
                     }
                 }
             }
             if (h >= 0 && row0 >= 0) {
                 const long long row = row0 + static_cast<long long>(h) * p.c.page_size;
-                *reinterpret_cast<uint32_t *>((is_k ? p.c.k_codes : p.c.v_codes) + row * (D / 2) + c0 / 2) = codes;
+                uint8_t *dst = (is_k ? p.c.k_codes : p.c.v_codes) + row * (D / 2) + c0 / 2;
+#pragma unroll
+                for (int x = 0; x < kChunks; ++x)
+                    *reinterpret_cast<uint32_t *>(dst + x * kStep / 2) = codes[x];
                 if (c0 % sdp::kCacheGroup == 0)
                     (is_k ? p.c.k_scales : p.c.v_scales)[row * (D / sdp::kCacheGroup) + c0 / sdp::kCacheGroup] =
                         s16 | (b16 << 16);
@@ -280,10 +312,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_gather_kernel(const RowsPa
     if (sh.count <= 0)
         return;
     const long long my_row = locate(p, sh.token0, sh.tokens(), lane);
-    const int sub = lane / S::LPR, c0 = (lane % S::LPR) * 8;
+    const int sub = lane / S::LPR, c0 = first_channel(lane % S::LPR);
     Cursor<D> at(sh);
     for (int x0 = 0; x0 < sh.count; x0 += kUnroll) {
-        uint32_t codes[kUnroll], pair[kUnroll];
+        uint32_t codes[kUnroll][kChunks], pair[kUnroll];
         uint16_t *out[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
@@ -293,8 +325,10 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_gather_kernel(const RowsPa
             out[i] = nullptr;
             if (h >= 0 && row0 >= 0) {
                 const long long row = row0 + static_cast<long long>(h) * p.c.page_size;
-                codes[i] = __ldg(reinterpret_cast<const uint32_t *>((is_k ? p.c.k_codes : p.c.v_codes) +
-                                                                    row * (D / 2) + c0 / 2));
+                const uint8_t *src = (is_k ? p.c.k_codes : p.c.v_codes) + row * (D / 2) + c0 / 2;
+#pragma unroll
+                for (int x = 0; x < kChunks; ++x)
+                    codes[i][x] = __ldg(reinterpret_cast<const uint32_t *>(src + x * kStep / 2));
                 pair[i] = __ldg((is_k ? p.c.k_scales : p.c.v_scales) + row * (D / sdp::kCacheGroup) +
                                 c0 / sdp::kCacheGroup);
                 const long long t = sh.token0 + at.token;
@@ -309,17 +343,22 @@ __global__ void __launch_bounds__(32 * kWarps) cache4_gather_kernel(const RowsPa
             const float s = __uint_as_float(pair[i] << 16), b = __uint_as_float(pair[i] & 0xffff0000u);
             const uint64_t s2 = sdp::ptx::f2_pack(s, s), b2 = sdp::ptx::f2_pack(b, b);
             const uint64_t big = sdp::ptx::f2_pack(-8388608.f, -8388608.f);
-            uint32_t o[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                // a code as 2^23 + n less 2^23; s * n is exact in fp32 (8 + 4 bits): one rounding, then the store's
-                const uint64_t n = sdp::ptx::f2_pack(__uint_as_float(((codes[i] >> (8 * j)) & 15u) | 0x4b000000u),
-                                                     __uint_as_float(((codes[i] >> (8 * j + 4)) & 15u) | 0x4b000000u));
-                float lo, hi;
-                sdp::ptx::f2_unpack(sdp::ptx::f2_fma(s2, sdp::ptx::f2_add(n, big), b2), lo, hi);
-                o[j] = sdp::pack16<BF16>(lo, hi);
+            for (int x = 0; x < kChunks; ++x) {
+                // a byte a code, then a code as 2^23 + n less 2^23; s * n is exact in fp32 (8 + 4 bits): one rounding,
+                // then the store's
+                const uint32_t even = codes[i][x] & 0x0f0f0f0fu, odd = (codes[i][x] >> 4) & 0x0f0f0f0fu;
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t n = sdp::ptx::f2_pack(__uint_as_float(__byte_perm(even, 0x4b000000u, 0x7550 | j)),
+                                                         __uint_as_float(__byte_perm(odd, 0x4b000000u, 0x7550 | j)));
+                    float lo, hi;
+                    sdp::ptx::f2_unpack(sdp::ptx::f2_fma(s2, sdp::ptx::f2_add(n, big), b2), lo, hi);
+                    o[j] = sdp::pack16<BF16>(lo, hi);
+                }
+                *reinterpret_cast<uint4 *>(out[i] + x * kStep) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            *reinterpret_cast<uint4 *>(out[i]) = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -382,7 +421,7 @@ int plan(RowsParams &p, int D, unsigned *blocks)
         return rc;
     if ((rc = sdp::status_word(dev, &p.status)) != SDP_OK)
         return rc;
-    const int rpp = 256 / D;
+    const int rpp = 32 / (D / 64 * kLanes);
     const long long passes = 2LL * ((p.c.Hkv + rpp - 1) / rpp);
     long long per = p.tokens * passes / (static_cast<long long>(sms) * 32);
     per = per < 1 ? 1 : per;
