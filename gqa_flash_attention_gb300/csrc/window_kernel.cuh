@@ -15,7 +15,17 @@
 //    loads and first scores running during the current unit's end (barrier phases and ring
 //    positions count across units). Units cost alike and neighbours share their K/V, so CTA c
 //    takes units c, c + C, c + 2C, ... with no counter to claim from, the same in a captured
-//    graph.
+//    graph. A warpgroup of its own writes a unit's rows while the softmax warps are with the next
+//    unit, and a warp of its own looks the units up ahead: with both done by the softmax warps, 7.8 us
+//    passed at each unit's end at D = 256 (1.1 us a tile), and 12 packed prompts (W = 1024, D = 256)
+//    took 903 us instead of 789, 16384 rows (W = 4096, D = 128) 697 instead of 634. A launch of one unit
+//    a CTA at most has no next unit to go on with, and the hand-overs cost it 1.8 us of 8.3: it
+//    runs without them (OVERLAP). O leaves tensor memory 32 columns at a time, stored as it comes: taken
+//    out whole first, which frees it earlier, the first was slower (812 us), its unrolled code larger.
+//  - What bounds it: at D = 128 the softmax (1390 cycles a tile, 1024 of them the exponentials at their
+//    rate); at D = 256 the products (2048 cycles a tile at the tensor cores' rate, 2130 measured) and
+//    what is left at a unit's end, the last product, O's way out and the next unit's first product
+//    one after the other.
 //  - Only the tiles that cut a window or the diagonal (two or three a unit, plus the sinks') are
 //    masked, from four 32-bit words of visible keys a row; the others run without a test.
 //  - A row may see nothing in a tile, or at all (more rows than keys): its maximum stays -inf, its
@@ -45,13 +55,17 @@ struct WindowLayout {
     // Query tiles in shared memory: two at D=128 (the next unit's Q loads while this unit runs),
     // one at D=256 (two would leave too few ring slots).
     static constexpr int QB = D == 128 ? 2 : 1;
-    static constexpr int NSLOTS = (L::SMEM_LIMIT - BAR_AREA - 1024 - QB * L::Q_BYTES) / L::CHUNK_BYTES;
+    static constexpr int NSLOTS = (L::SMEM_LIMIT - BAR_AREA - 2 * L::BM * 4 - 4 * 48 - 1024 - QB * L::Q_BYTES) / L::CHUNK_BYTES;
     // q_full[QB], slot_full[NS], slot_empty[NS], s_full[NB], p_full[NB], o_done[ring], final[2],
-    // q_free[QB], o_free
-    static constexpr int NBARS = QB + 2 * NSLOTS + 2 * L::NSBUF + O_DONE_RING + 2 + QB + 1;
+    // q_free[QB], o_free, sum_full[2], sum_free[2], unit_full[UNITS], unit_free[UNITS]
+    static constexpr int UNITS = 4;  // units looked up ahead
+    static constexpr int NBARS = QB + 2 * NSLOTS + 2 * L::NSBUF + O_DONE_RING + 2 + QB + 1 + 4 + 2 * UNITS;
     static constexpr int BAR_OFF = QB * L::Q_BYTES + NSLOTS * L::CHUNK_BYTES;
     static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, then the abort flag
-    static constexpr int SMEM_BYTES = BAR_OFF + BAR_AREA + 1024;
+    static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;  // two units' row factors, for the rows' ends
+    static constexpr int UNIT_OFF = SUM_OFF + 2 * L::BM * 4;
+    static constexpr int UNIT_AREA = UNITS * 48;
+    static constexpr int SMEM_BYTES = UNIT_OFF + UNIT_AREA + 1024;
     static_assert(HOLDER_OFF + 8 <= BAR_OFF + BAR_AREA, "barrier area");
     static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
     // Ring parity across units of any lengths (global load positions): the S issuer waits for
@@ -142,8 +156,17 @@ static __device__ __noinline__ void recompute_row(const uint16_t *q, const uint1
         *lse = (m + ptx::lg2(l)) * LN2;
 }
 
-template <int D, bool BF16, bool VARLEN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+// Warpgroups: softmax, then the loading and issuing warps, then (OVERLAP) those that write the rows. Registers a
+// thread of each with OVERLAP: the block launches with WINDOW_LAUNCH_REGS each, and the softmax takes what the
+// second group gives back.
+constexpr int WINDOW_LAUNCH_REGS = 168, WINDOW_SOFTMAX_REGS = 232, WINDOW_ISSUE_REGS = 104;
+static_assert(WINDOW_SOFTMAX_REGS + WINDOW_ISSUE_REGS <= 2 * WINDOW_LAUNCH_REGS, "registers of the launch");
+constexpr int window_threads(bool overlap) { return overlap ? 384 : 256; }
+
+// OVERLAP: a warpgroup of its own writes a unit's rows while the softmax goes on with the next unit; without it the
+// softmax warps do.
+template <int D, bool BF16, bool VARLEN, bool OVERLAP>
+__global__ void __launch_bounds__(window_threads(OVERLAP), 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const WindowParams wp)
 {
@@ -174,6 +197,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t final0 = o_done0 + 8u * O_DONE_RING;
     const uint32_t q_free0 = final0 + 16u;  // + 8 b: the S MMAs that read query tile b last are done
     const uint32_t o_free = q_free0 + 8u * QB;
+    const uint32_t sum_full0 = o_free + 8u;  // + 8 (unit & 1): its row factors are there
+    const uint32_t sum_free0 = sum_full0 + 16u;
+    const uint32_t unit_full0 = sum_free0 + 16u, unit_free0 = unit_full0 + 8u * WL::UNITS;  // + 8 (i % UNITS)
+    float *const row_factor = reinterpret_cast<float *>(smem + WL::SUM_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + WL::HOLDER_OFF);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
@@ -182,20 +209,48 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
     // A unit's geometry: Q/O and K/V planes, its first row within its sequence (q0) and in the row
     // coordinate (q_row), the first K/V row, the sequence's rows, the position of its row 0, and its
-    // tiles: ns of the sinks, then those from t_lo, n in all. n = 0: no key (zero: its rows get O = 0
-    // and LSE = -inf), a slot past the last tile, or (bad) invalid offsets.
-    struct Unit {
-        int z_q, z_kv, q0, q_row, kv_row0, sq, pos0, t_lo, ns, n;
-        bool zero, bad;
+    // tiles: ns of the sinks, then those from t_lo, n in all. n = 0: no key (its rows get O = 0 and
+    // LSE = -inf); n < 0: nothing to do, in the ring: nor in any unit after it.
+    struct __align__(16) Unit {
+        int z_q, z_kv, q0, q_row, kv_row0, sq, pos0, t_lo, ns, n, unused[2];
         __device__ __forceinline__ int tile(int j) const { return j < ns ? j : t_lo + j - ns; }
     };
-    auto unit_of = [&](int u) {
+    auto unit_of = [&](int u) {  // by a whole warp
         Unit r{};
+        r.n = -1;
         const int hi = u % p.G;
         u /= p.G;
         if constexpr (VARLEN) {
-            if (p.n_tiles > 0 && (u = varlen_compact_unit(p, u)) < 0)
-                return r;  // a slot past the last query tile
+            if (p.n_tiles > 0) {
+                // tile t of the list of those that exist, in sequence order: the sequence, from the sums of
+                // their tiles, 32 sequences a step (CTA 0 looks all of them over for bad offsets)
+                const int t = u % p.n_tiles, g = u / p.n_tiles;
+                const VarlenScan v{p.cu_q, p.cu_k, p.nseq, p.n_qtiles, p.Sq, p.Skv};
+                int found = -1;
+                for (int base = 0, acc = 0; base < p.nseq && (found < 0 || blockIdx.x == 0); base += 32) {
+                    bool bad;
+                    const int tiles = varlen_tiles(v, base + lane, bad);
+                    if (bad && blockIdx.x == 0)
+                        atomicCAS(p.status, 0u, static_cast<unsigned>(SITE_SEQLENS));
+                    int incl = tiles;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int x = __shfl_up_sync(0xffffffffu, incl, d);
+                        if (lane >= d)
+                            incl += x;
+                    }
+                    incl += acc;
+                    const unsigned hit = __ballot_sync(0xffffffffu, incl - tiles <= t && t < incl);
+                    if (hit != 0u) {
+                        const int src = __ffs(hit) - 1;
+                        found = ((base + src) * p.Hkv + g) * p.n_qtiles + t - __shfl_sync(0xffffffffu, incl - tiles, src);
+                    }
+                    acc = __shfl_sync(0xffffffffu, incl, 31);
+                }
+                if (found < 0)
+                    return r;  // a slot past the last query tile
+                u = found;
+            }
         }
         const int qt = u % p.n_qtiles, bg = u / p.n_qtiles;
         const int b = bg / p.Hkv, g = bg - b * p.Hkv;
@@ -204,7 +259,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         r.q0 = qt * L::BM;
         const SeqGeom sg = seq_geom(p, b);
         if (!sg.ok) {
-            r.bad = true;
+            if (lane == 0) {
+                const uint32_t cta = blockIdx.x < 0xFFFFFFu ? blockIdx.x : 0xFFFFFFu;
+                atomicCAS(p.status, 0u, SITE_SEQLENS | (cta << 8));
+            }
             return r;
         }
         r.sq = sg.sq;
@@ -216,10 +274,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // positions of the tile's first and last row
         const int p_lo = r.pos0 + (wp.pack_sq > 0 ? 0 : r.q0);
         const int p_hi = r.pos0 + (wp.pack_sq > 0 ? wp.pack_sq - 1 : min(r.q0 + L::BM, sg.sq) - 1);
-        if (p_hi < 0) {
-            r.zero = true;
+        r.n = 0;
+        if (p_hi < 0)
             return r;
-        }
         r.t_lo = max(0, p_lo - wp.window + 1) / L::BN;
         r.ns = min((min(wp.sinks, p_hi + 1) + L::BN - 1) / L::BN, r.t_lo);
         r.n = r.ns + p_hi / L::BN + 1 - r.t_lo;
@@ -243,7 +300,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             ptx::mbar_init(o_done0 + 8u * i, 1);
         ptx::mbar_init(final0, 1);
         ptx::mbar_init(final0 + 8u, 1);
-        ptx::mbar_init(o_free, 4);  // one arrival per softmax warp
+        ptx::mbar_init(o_free, 4);  // one arrival a warp of the rows' ends
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(sum_full0 + 8u * b, 128);
+            ptx::mbar_init(sum_free0 + 8u * b, 4);
+        }
+        for (int i = 0; i < WL::UNITS; ++i) {
+            ptx::mbar_init(unit_full0 + 8u * i, 1);
+            ptx::mbar_init(unit_free0 + 8u * i, 11);  // the warps that read it
+        }
         *abort_flag = 0;
         ptx::fence_barrier_init();
     }
@@ -256,213 +321,359 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    // OVERLAP: warp 7 looks up the units blockIdx.x, + gridDim.x, ... ahead of the others (in a batch of odd lengths
+    // that takes a search and a few dependent loads) and hands those with rows on through a ring. Else a CTA has
+    // one unit, which every warp looks up. k counts those with tiles.
+    int u = static_cast<int>(blockIdx.x);
+    auto next_unit = [&]() {
+        Unit r;
+        r.n = -1;
+        while (u < p.units && r.n < 0) {
+            r = unit_of(u);
+            u += static_cast<int>(gridDim.x);
+        }
+        return r;
+    };
+    Unit ahead;
+    if (!OVERLAP || warp == 7)
+        ahead = next_unit();  // while tensor memory is allocated
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const WaitCtx cx{abort_flag, p.status, p.timeout_ns};
-    const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
+    // Bounded waits as in the forward kernels, but inline: a call in a branch with registers of its own
+    // (setmaxnreg) does not assemble.
     auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
-        return __all_sync(0xffffffffu, wait_bounded(bar, parity, cx, site));
+        bool done = ptx::mbar_try_wait(bar, parity);
+        if (!__all_sync(0xffffffffu, done)) {
+            const uint64_t t0 = ptx::globaltimer_ns();
+            for (uint32_t it = 1; !__all_sync(0xffffffffu, done = ptx::mbar_try_wait(bar, parity)); ++it) {
+                if ((it & 15u) != 0)
+                    continue;
+                const bool late = ptx::globaltimer_ns() - t0 > p.timeout_ns;
+                if (__any_sync(0xffffffffu, late || *abort_flag)) {
+                    if (late && !done) {
+                        *abort_flag = 1;
+                        const uint32_t cta = blockIdx.x < 0xFFFFFFu ? blockIdx.x : 0xFFFFFFu;
+                        atomicCAS(p.status, 0u, site | (cta << 8));
+                    }
+                    return false;
+                }
+            }
+        }
+        return true;
+    };
+    auto drain = [&](uint32_t bar, uint32_t parity) {  // of what this warp issued itself
+        const uint64_t t0 = ptx::globaltimer_ns();
+        while (!ptx::mbar_try_wait(bar, parity) && ptx::globaltimer_ns() - t0 <= p.timeout_ns) {
+        }
     };
 
-    // Every role walks the units first, first + step, ...; k counts those with tiles.
-    if (warp == 4) {
-        // ------------------------------------------------------ TMA producer
-        if (!(p.debug_flags & DEBUG_NO_LOADS)) {  // whole warp; one elected lane issues
-            int slot = 0, k = 0;
-            uint32_t ph = 0, armed_mask = 0, armed_par = 0, q_armed = 0, q_par = 0;
-            bool ok = true;
-            for (int u = first; ok && u < p.units; u += step) {
-                const Unit un = unit_of(u);
+    Unit *const ring = reinterpret_cast<Unit *>(smem + WL::UNIT_OFF);
+    auto take = [&](int i, Unit &un) -> bool {  // unit i; false at the end or when a wait ran out
+        if constexpr (!OVERLAP) {
+            un = ahead;
+            return i == 0 && un.n >= 0;
+        }
+        const int at = i % WL::UNITS;
+        if (!wait_all(unit_full0 + 8u * at, (i / WL::UNITS) & 1, SITE_Q_FULL))
+            return false;
+        un = ring[at];
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(unit_free0 + 8u * at);
+        return un.n >= 0;
+    };
+    auto o_tile_of = [&](const Unit &un) {
+        return static_cast<uint16_t *>(p.o) + un.z_q * wp.q_plane + static_cast<long long>(un.q_row) * wp.q_row;
+    };
+    auto lse_of = [&](const Unit &un, int row) {
+        return p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(un.z_q) * p.Sq + un.q_row + row;
+    };
+    auto no_key = [&](const Unit &un, int row) {  // the row of a unit without tiles
+        if (un.q0 + row >= un.sq)
+            return;
+        for (int i = 0; i < D / 8; ++i)
+            reinterpret_cast<uint4 *>(o_tile_of(un) + row * wp.q_row)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (p.lse != nullptr)
+            *lse_of(un, row) = -INFINITY;
+    };
+    // A unit's rows, 32 of them by each of four warps (w4): O, complete with tile `last`, times inv_l (negative: the
+    // row saw no key) to global memory, and O's tensor memory to the next unit's first PV.
+    auto write_rows = [&](const Unit &un, int w4, int last, float inv_l) -> bool {
+        const int row = w4 * 32 + lane;
+        const uint32_t t_o = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + L::TM_O;
+        uint16_t *const o_tile = o_tile_of(un);
+        const bool row_ok = un.q0 + row < un.sq, none = inv_l < 0.f;
+        if (!wait_all(o_done0 + 8u * (last % O_DONE_RING), (last / O_DONE_RING) & 1, SITE_O_DONE))
+            return false;
+        ptx::tc_fence_after();
+        float probe = 0.f;  // NaN once an element of the row is not finite
+#pragma unroll 1
+        for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            ptx::tmem_ld32(t_o + 32 * cc, o);
+            ptx::tmem_wait_ld();
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float a = __uint_as_float(o[2 * i]), b = __uint_as_float(o[2 * i + 1]);
+                probe = fmaf(a, 0.f, fmaf(b, 0.f, probe));
+                pk[i] = none ? 0u : pack2<BF16>(a * inv_l, b * inv_l);
+            }
+            // four lanes' rows by four 16-byte units, transposed in two exchanges: lane l then holds
+            // unit l & 3 of the rows l, l ^ 1, l ^ 2 and l ^ 3, and the four write 64 bytes of a row at once
+            const bool odd = lane & 1, high = lane & 2;
+            uint32_t own[2][4], next[2][4], out[4][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t u0 = pk[8 * h + x], u1 = pk[8 * h + 4 + x];
+                    own[h][x] = odd ? u1 : u0;
+                    next[h][x] = __shfl_xor_sync(0xffffffffu, odd ? u0 : u1, 1);
+                }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                out[0][x] = high ? own[1][x] : own[0][x];
+                out[1][x] = high ? next[1][x] : next[0][x];
+                out[2][x] = __shfl_xor_sync(0xffffffffu, high ? own[0][x] : own[1][x], 2);
+                out[3][x] = __shfl_xor_sync(0xffffffffu, high ? next[0][x] : next[1][x], 2);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (un.q0 + (row ^ i) < un.sq)
+                    reinterpret_cast<uint4 *>(o_tile + (row ^ i) * wp.q_row)[4 * cc + (lane & 3)] =
+                        make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0)
+            ptx::mbar_arrive(o_free);
+        unsigned again = __ballot_sync(0xffffffffu, row_ok && !none && probe != 0.f);
+        while (again != 0u) {
+            const int src = __ffs(again) - 1;
+            again &= again - 1u;
+            const int r = w4 * 32 + src;
+            const int at = un.pos0 + (wp.pack_sq > 0 ? (un.q0 + r) % wp.pack_sq : un.q0 + r);
+            const int b0 = max(0, at - wp.window + 1);
+            const long long q_off = un.z_q * wp.q_plane + static_cast<long long>(un.q_row + r) * wp.q_row;
+            const long long kv_off = un.z_kv * wp.kv_plane + static_cast<long long>(un.kv_row0) * wp.kv_row;
+            __syncwarp();  // the row's first stores before those that replace them
+            recompute_row<D, BF16>(static_cast<const uint16_t *>(wp.q) + q_off,
+                                   static_cast<const uint16_t *>(wp.kk) + kv_off,
+                                   static_cast<const uint16_t *>(wp.v) + kv_off, wp.kv_row, min(wp.sinks, b0), b0,
+                                   at + 1, p.c, static_cast<uint16_t *>(p.o) + q_off,
+                                   lse_of(un, r));
+        }
+        return true;
+    };
+    if (warp >= 4 && warp < 8) {
+        if constexpr (OVERLAP)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(WINDOW_ISSUE_REGS));
+        if (warp == 4) {
+            // ------------------------------------------------------ TMA producer
+            if (!(p.debug_flags & DEBUG_NO_LOADS)) {  // whole warp; one elected lane issues
+                int slot = 0, k = 0;
+                uint32_t ph = 0, armed_mask = 0, armed_par = 0, q_armed = 0, q_par = 0;
+                bool ok = true;
+                Unit un;
+                for (int i = 0; ok && take(i, un); ++i) {
+                    const int n = un.n;
+                    if (n == 0)
+                        continue;
+                    const int b = k % QB;
+                    if (k >= QB && !(ok = wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL)))
+                        break;
+                    ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, L::Q_BYTES);
+#pragma unroll
+                    for (int c = 0; c < D / L::BOX_COLS; ++c)
+                        ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, &tm_q, q_full0 + 8u * b, c * L::BOX_COLS,
+                                           un.q_row, un.z_q);
+                    q_armed |= 1u << b;
+                    q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
+                    auto load_tile = [&](const CUtensorMap *map, int j) -> bool {
+#pragma unroll
+                        for (int ch = 0; ch < CPT; ++ch) {
+                            const uint32_t full = slot_full0 + 8u * slot;
+                            if (!wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY))
+                                return false;
+                            ptx::mbar_arrive_expect_tx_w(full, L::CHUNK_BYTES);
+                            const uint32_t dst = s_ring + slot * L::CHUNK_BYTES;
+                            const int y = un.kv_row0 + un.tile(j) * L::BN;
+                            ptx::tma_load_3d_w(dst, map, full, ch * 128, y, un.z_kv);
+                            ptx::tma_load_3d_w(dst + L::BOX_BYTES, map, full, ch * 128 + L::BOX_COLS, y, un.z_kv);
+                            armed_mask |= 1u << slot;
+                            armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
+                            if (++slot == NS) {
+                                slot = 0;
+                                ph ^= 1u;
+                            }
+                        }
+                        return true;
+                    };
+                    ok = load_tile(&tm_k, 0);
+                    for (int j = 0; ok && j < n; ++j) {
+                        if (j + 1 < n)
+                            ok = load_tile(&tm_k, j + 1);
+                        if (ok)
+                            ok = load_tile(&tm_v, j);
+                    }
+                    ++k;
+                }
+                // Every copy this thread issued lands before the CTA may exit.
+                for (int b = 0; b < QB; ++b)
+                    if (q_armed & (1u << b))
+                        drain(q_full0 + 8u * b, (q_par >> b) & 1u);
+                for (int s = 0; s < NS; ++s)
+                    if (armed_mask & (1u << s))
+                        drain(slot_full0 + 8u * s, (armed_par >> s) & 1u);
+            }
+        } else if (warp == 5) {
+            // ------------------------------------------- S = Q K^T issuer
+            const uint64_t dk = ptx::smem_desc_sw128(s_ring, 16, 1024);
+            bool issued = false, ok = true;
+            int g0 = 0, pos0 = 0, k = 0;  // tiles and ring chunks of the earlier units
+            Unit un;
+            for (int i = 0; ok && take(i, un); ++i) {
                 const int n = un.n;
                 if (n == 0)
                     continue;
                 const int b = k % QB;
-                if (k >= QB && !(ok = wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL)))
+                const uint64_t dq = ptx::smem_desc_sw128(s_q0 + b * L::Q_BYTES, 16, 1024);
+                if (!(ok = wait_all(q_full0 + 8u * b, (k / QB) & 1, SITE_Q_FULL)))
                     break;
-                ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, L::Q_BYTES);
-#pragma unroll
-                for (int c = 0; c < D / L::BOX_COLS; ++c)
-                    ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, &tm_q, q_full0 + 8u * b, c * L::BOX_COLS,
-                                       un.q_row, un.z_q);
-                q_armed |= 1u << b;
-                q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
-                auto load_tile = [&](const CUtensorMap *map, int j) -> bool {
+                for (int t = 0; ok && t < n; ++t) {
+                    const int gt = g0 + t;
+                    const int p0 = pos0 + pos_k<CPT>(t);
+                    if (gt >= NB) {  // buffer gt % NB held P of tile gt - NB: its PV must have read it
+                        const int pv = gt - NB;
+                        if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
+                            break;
+                    }
 #pragma unroll
                     for (int ch = 0; ch < CPT; ++ch) {
-                        const uint32_t full = slot_full0 + 8u * slot;
-                        if (!wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY))
-                            return false;
-                        ptx::mbar_arrive_expect_tx_w(full, L::CHUNK_BYTES);
-                        const uint32_t dst = s_ring + slot * L::CHUNK_BYTES;
-                        const int y = un.kv_row0 + un.tile(j) * L::BN;
-                        ptx::tma_load_3d_w(dst, map, full, ch * 128, y, un.z_kv);
-                        ptx::tma_load_3d_w(dst + L::BOX_BYTES, map, full, ch * 128 + L::BOX_COLS, y, un.z_kv);
-                        armed_mask |= 1u << slot;
-                        armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
-                        if (++slot == NS) {
-                            slot = 0;
-                            ph ^= 1u;
-                        }
+                        const int pos = p0 + ch;
+                        if (!(ok = wait_all(slot_full0 + 8u * (pos % NS), (pos / NS) & 1, SITE_SLOT_FULL)))
+                            break;
                     }
-                    return true;
-                };
-                ok = load_tile(&tm_k, 0);
-                for (int j = 0; ok && j < n; ++j) {
-                    if (j + 1 < n)
-                        ok = load_tile(&tm_k, j + 1);
-                    if (ok)
-                        ok = load_tile(&tm_v, j);
+                    if (!ok)
+                        break;
+                    ptx::tc_fence_after();
+                    const uint32_t d_tmem = tmem + L::TM_S + (gt % NB) * L::BN;
+#pragma unroll
+                    for (int ch = 0; ch < CPT; ++ch) {
+                        const int slot = (p0 + ch) % NS;
+                        const uint64_t kslot = dk + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                        const uint64_t qch = dq + static_cast<uint64_t>((2 * ch * L::BOX_BYTES) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) {
+                            const uint32_t off = ((kk >> 2) * L::BOX_BYTES + (kk & 3) * 32) >> 4;
+                            ptx::mma_ss_w(d_tmem, qch + off, kslot + off, IDESC_S, (ch | kk) != 0);
+                        }
+                        issued = true;
+                        ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                    }
+                    ptx::mma_commit_w(s_full0 + 8u * (gt % NB));
                 }
+                if (!ok)
+                    break;
+                ptx::mma_commit_w(q_free0 + 8u * b);  // query tile b may take unit k + QB's Q
+                g0 += n;
+                pos0 += 2 * CPT * n;
                 ++k;
             }
-            // Every copy this thread issued lands before the CTA may exit.
-            for (int b = 0; b < QB; ++b)
-                if (q_armed & (1u << b))
-                    wait_drain(q_full0 + 8u * b, (q_par >> b) & 1u, p.timeout_ns);
-            for (int s = 0; s < NS; ++s)
-                if (armed_mask & (1u << s))
-                    wait_drain(slot_full0 + 8u * s, (armed_par >> s) & 1u, p.timeout_ns);
-        }
-    } else if (warp == 5) {
-        // ------------------------------------------- S = Q K^T issuer
-        const uint64_t dk = ptx::smem_desc_sw128(s_ring, 16, 1024);
-        bool issued = false, ok = true;
-        int g0 = 0, pos0 = 0, k = 0;  // tiles and ring chunks of the earlier units
-        for (int u = first; ok && u < p.units; u += step) {
-            const int n = unit_of(u).n;
-            if (n == 0)
-                continue;
-            const int b = k % QB;
-            const uint64_t dq = ptx::smem_desc_sw128(s_q0 + b * L::Q_BYTES, 16, 1024);
-            if (!(ok = wait_all(q_full0 + 8u * b, (k / QB) & 1, SITE_Q_FULL)))
-                break;
-            for (int t = 0; ok && t < n; ++t) {
-                const int gt = g0 + t;
-                const int p0 = pos0 + pos_k<CPT>(t);
-                if (gt >= NB) {  // buffer gt % NB held P of tile gt - NB: its PV must have read it
-                    const int pv = gt - NB;
-                    if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
-                        break;
-                }
-#pragma unroll
-                for (int ch = 0; ch < CPT; ++ch) {
-                    const int pos = p0 + ch;
-                    if (!(ok = wait_all(slot_full0 + 8u * (pos % NS), (pos / NS) & 1, SITE_SLOT_FULL)))
-                        break;
-                }
-                if (!ok)
-                    break;
-                ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem + L::TM_S + (gt % NB) * L::BN;
-#pragma unroll
-                for (int ch = 0; ch < CPT; ++ch) {
-                    const int slot = (p0 + ch) % NS;
-                    const uint64_t kslot = dk + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
-                    const uint64_t qch = dq + static_cast<uint64_t>((2 * ch * L::BOX_BYTES) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = ((kk >> 2) * L::BOX_BYTES + (kk & 3) * 32) >> 4;
-                        ptx::mma_ss_w(d_tmem, qch + off, kslot + off, IDESC_S, (ch | kk) != 0);
-                    }
-                    issued = true;
-                    ptx::mma_commit_w(slot_empty0 + 8u * slot);
-                }
-                ptx::mma_commit_w(s_full0 + 8u * (gt % NB));
+            if (issued) {  // all of this thread's MMAs complete before TMEM is freed
+                ptx::mma_commit_w(final0);
+                drain(final0, 0);
             }
-            if (!ok)
-                break;
-            ptx::mma_commit_w(q_free0 + 8u * b);  // query tile b may take unit k + QB's Q
-            g0 += n;
-            pos0 += 2 * CPT * n;
-            ++k;
-        }
-        if (issued) {  // all of this thread's MMAs complete before TMEM is freed
-            ptx::mma_commit_w(final0);
-            wait_drain(final0, 0, p.timeout_ns);
-        }
-    } else if (warp == 6) {
-        // ------------------------------------------ O += P V issuer
-        const uint64_t dv = ptx::smem_desc_sw128(s_ring, L::BOX_BYTES, 1024);
-        bool issued = false, ok = true;
-        int g0 = 0, pos0 = 0, k = 0;
-        for (int u = first; ok && u < p.units; u += step) {
-            const int n = unit_of(u).n;
-            if (n == 0)
-                continue;
-            for (int j = 0; ok && j < n; ++j) {
-                const int gj = g0 + j;
-                const int buf = gj % NB;
-                const int p0 = pos0 + pos_v<CPT>(j, n);
-                if constexpr (CPT == 1) {  // V_j's slot first, off the P_j -> PV_j path
-                    if (!(ok = wait_all(slot_full0 + 8u * (p0 % NS), (p0 / NS) & 1, SITE_SLOT_FULL)))
-                        break;
-                }
-                if (!(ok = wait_all(p_full0 + 8u * buf, (gj / NB) & 1, SITE_P_FULL)))
-                    break;
-                // a unit's first PV overwrites O: the previous unit's epilogue must have read it
-                if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
-                    break;
-                ptx::tc_fence_after();
-                const uint32_t a_tmem = tmem + L::TM_S + buf * L::BN;
-#pragma unroll
-                for (int ch = 0; ch < CPT; ++ch) {
-                    const int pos = p0 + ch;
-                    const int slot = pos % NS;
-                    if constexpr (CPT != 1) {
-                        if (!(ok = wait_all(slot_full0 + 8u * slot, (pos / NS) & 1, SITE_SLOT_FULL)))
+        } else if (warp == 6) {
+            // ------------------------------------------ O += P V issuer
+            const uint64_t dv = ptx::smem_desc_sw128(s_ring, L::BOX_BYTES, 1024);
+            bool issued = false, ok = true;
+            int g0 = 0, pos0 = 0, k = 0;
+            Unit un;
+            for (int i = 0; ok && take(i, un); ++i) {
+                const int n = un.n;
+                if (n == 0)
+                    continue;
+                for (int j = 0; ok && j < n; ++j) {
+                    const int gj = g0 + j;
+                    const int buf = gj % NB;
+                    const int p0 = pos0 + pos_v<CPT>(j, n);
+                    if constexpr (CPT == 1) {  // V_j's slot first, off the P_j -> PV_j path
+                        if (!(ok = wait_all(slot_full0 + 8u * (p0 % NS), (p0 / NS) & 1, SITE_SLOT_FULL)))
                             break;
-                        ptx::tc_fence_after();
                     }
-                    const uint64_t vslot = dv + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                    if (!(ok = wait_all(p_full0 + 8u * buf, (gj / NB) & 1, SITE_P_FULL)))
+                        break;
+                    // a unit's first PV overwrites O: the previous unit's epilogue must have read it
+                    if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
+                        break;
+                    ptx::tc_fence_after();
+                    const uint32_t a_tmem = tmem + L::TM_S + buf * L::BN;
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
-                                      (j > 0) || (kk > 0));
-                    issued = true;
-                    ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                    for (int ch = 0; ch < CPT; ++ch) {
+                        const int pos = p0 + ch;
+                        const int slot = pos % NS;
+                        if constexpr (CPT != 1) {
+                            if (!(ok = wait_all(slot_full0 + 8u * slot, (pos / NS) & 1, SITE_SLOT_FULL)))
+                                break;
+                            ptx::tc_fence_after();
+                        }
+                        const uint64_t vslot = dv + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
+                                          (j > 0) || (kk > 0));
+                        issued = true;
+                        ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                    }
+                    if (!ok)
+                        break;
+                    ptx::mma_commit_w(o_done0 + 8u * (gj % O_DONE_RING));
                 }
-                if (!ok)
-                    break;
-                ptx::mma_commit_w(o_done0 + 8u * (gj % O_DONE_RING));
+                g0 += n;
+                pos0 += 2 * CPT * n;
+                ++k;
             }
-            g0 += n;
-            pos0 += 2 * CPT * n;
-            ++k;
-        }
-        if (issued) {
-            ptx::mma_commit_w(final0 + 8u);
-            wait_drain(final0 + 8u, 0, p.timeout_ns);
+            if (issued) {
+                ptx::mma_commit_w(final0 + 8u);
+                drain(final0 + 8u, 0);
+            }
+        } else if constexpr (OVERLAP) {
+            // ------------------------------------------ the units, ahead of the others
+            for (int i = 0;; ++i) {
+                if (i > 0)
+                    ahead = next_unit();
+                const int at = i % WL::UNITS;
+                if (i >= WL::UNITS && !wait_all(unit_free0 + 8u * at, (i / WL::UNITS - 1) & 1, SITE_Q_FULL))
+                    break;
+                if (lane == 0) {
+                    ring[at] = ahead;
+                    ptx::mbar_arrive(unit_full0 + 8u * at);
+                }
+                if (ahead.n < 0)
+                    break;
+            }
         }
     } else if (warp < 4) {
-        // --------------------------------------- softmax / correction / epilogue
+        // --------------------------------------- softmax / correction
+        if constexpr (OVERLAP)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WINDOW_SOFTMAX_REGS));
         const int row = threadIdx.x;  // query row within the tile = TMEM lane
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t t_s = tmem + lane_off + L::TM_S;
         const uint32_t t_o = tmem + lane_off + L::TM_O;
         const float c = p.c;
         bool ok = true;
-        int g0 = 0;
-        for (int u = first; ok && u < p.units; u += step) {
-            const Unit un = unit_of(u);
+        int g0 = 0, k = 0;
+        Unit un;
+        for (int i = 0; ok && take(i, un); ++i) {
             const int n = un.n;
-            uint16_t *const o_row = static_cast<uint16_t *>(p.o) + un.z_q * wp.q_plane +
-                                    static_cast<long long>(un.q_row + row) * wp.q_row;
-            const bool row_ok = un.q0 + row < un.sq;
-            float *const lse_row =
-                p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(un.z_q) * p.Sq + un.q_row + row;
             if (n == 0) {
-                if (un.bad && row == 0) {
-                    const uint32_t cta = blockIdx.x < 0xFFFFFFu ? blockIdx.x : 0xFFFFFFu;
-                    atomicCAS(p.status, 0u, SITE_SEQLENS | (cta << 8));
-                }
-                if (un.zero && row_ok) {
-                    for (int i = 0; i < D / 8; ++i)
-                        reinterpret_cast<uint4 *>(o_row)[i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (lse_row != nullptr)
-                        *lse_row = -INFINITY;
-                }
+                if constexpr (!OVERLAP)
+                    no_key(un, row);
                 continue;
             }
             // this row's position; keys [0, pos] and (> pos - window or < sinks) are visible
@@ -583,61 +794,45 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (!ok)
                 break;
 
-            // ---------------------------------------------------------- epilogue
-            // O rows straight from registers to global memory, then O's tensor memory is released
-            // to the next unit's first PV.
-            {
-                const int pv = g0 + n - 1;
-                if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
+            // the row's end: its log-sum-exp, and its factor for O
+            const float inv_l = l == 0.f ? -1.f : 1.f / l;  // -1: the row saw no key
+            if (p.lse != nullptr && un.q0 + row < un.sq)
+                *lse_of(un, row) = l == 0.f ? -INFINITY : (m_used + ptx::lg2(l)) * LN2;
+            if constexpr (OVERLAP) {
+                const int b = k & 1;
+                if (k >= 2 && !(ok = wait_all(sum_free0 + 8u * b, ((k >> 1) - 1) & 1, SITE_O_DONE)))
                     break;
+                row_factor[b * L::BM + row] = inv_l;
+                ptx::mbar_arrive(sum_full0 + 8u * b);
+            } else if (!(ok = write_rows(un, warp, g0 + n - 1, inv_l))) {
+                break;
             }
-            ptx::tc_fence_after();
-            const bool none = l == 0.f;  // the row saw no key
-            const float inv_l = none ? 0.f : 1.f / l;
-            float probe = 0.f;  // NaN once an element of the row is not finite
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                ptx::tmem_ld32(t_o + 32 * cc, o);
-                ptx::tmem_wait_ld();
-                uint32_t pk[16];
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = __uint_as_float(o[2 * i]), b = __uint_as_float(o[2 * i + 1]);
-                    probe = fmaf(a, 0.f, fmaf(b, 0.f, probe));
-                    pk[i] = none ? 0u : pack2<BF16>(a * inv_l, b * inv_l);
-                }
-                if (row_ok) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        reinterpret_cast<uint4 *>(o_row)[4 * cc + x] =
-                            make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
-                }
+            g0 += n;
+            ++k;
+        }
+    } else {
+        // --------------------------------------- rows' ends: O times its factor, to global memory
+        const int w4 = warp & 3, row = w4 * 32 + lane;
+        bool ok = true;
+        int g0 = 0, k = 0;
+        Unit un;
+        for (int i = 0; ok && take(i, un); ++i) {
+            const int n = un.n;
+            if (n == 0) {
+                no_key(un, row);
+                continue;
             }
-            ptx::tc_fence_before();
+            const int b = k & 1;
+            if (!(ok = wait_all(sum_full0 + 8u * b, (k >> 1) & 1, SITE_O_DONE)))
+                break;
+            const float inv_l = row_factor[b * L::BM + row];
             __syncwarp();
             if (lane == 0)
-                ptx::mbar_arrive(o_free);
-            if (lse_row != nullptr && row_ok)
-                *lse_row = none ? -INFINITY : (m_used + ptx::lg2(l)) * LN2;
+                ptx::mbar_arrive(sum_free0 + 8u * b);
+            if (!(ok = write_rows(un, w4, g0 + n - 1, inv_l)))
+                break;
             g0 += n;
-
-            unsigned again = __ballot_sync(0xffffffffu, row_ok && !none && probe != 0.f);
-            while (again != 0u) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1u;
-                const int r = warp * 32 + src;
-                const int at = __shfl_sync(0xffffffffu, pos, src);
-                const int b0 = max(0, at - wp.window + 1);
-                const long long q_off = un.z_q * wp.q_plane + static_cast<long long>(un.q_row + r) * wp.q_row;
-                const long long kv_off = un.z_kv * wp.kv_plane + static_cast<long long>(un.kv_row0) * wp.kv_row;
-                __syncwarp();  // the row's first stores before those that replace them
-                recompute_row<D, BF16>(static_cast<const uint16_t *>(wp.q) + q_off,
-                                       static_cast<const uint16_t *>(wp.kk) + kv_off,
-                                       static_cast<const uint16_t *>(wp.v) + kv_off, wp.kv_row, min(wp.sinks, b0), b0,
-                                       at + 1, c, static_cast<uint16_t *>(p.o) + q_off,
-                                       p.lse == nullptr ? nullptr : p.lse + static_cast<size_t>(un.z_q) * p.Sq + un.q_row + r);
-            }
+            ++k;
         }
     }
 
@@ -653,14 +848,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 template <int D, bool BF16>
 cudaError_t launch_window(const LaunchMaps &m, const WindowParams &p, cudaStream_t stream)
 {
-    static unsigned long long set_dense = 0, set_varlen = 0;
     const bool vl = p.k.cu_q != nullptr;
-    auto kern = vl ? window_kernel<D, BF16, true> : window_kernel<D, BF16, false>;
-    cudaError_t e = set_smem_once(kern, WindowLayout<D>::SMEM_BYTES, vl ? set_varlen : set_dense);
+    const int ctas = p.k.units < p.k.num_sms ? p.k.units : p.k.num_sms;
+    // With a unit a CTA at most there is no next one to go on with, and the hand-over costs its latency.
+    const bool overlap = p.k.units > p.k.num_sms;
+    static unsigned long long set[2][2] = {};
+    auto kern = vl ? (overlap ? window_kernel<D, BF16, true, true> : window_kernel<D, BF16, true, false>)
+                   : (overlap ? window_kernel<D, BF16, false, true> : window_kernel<D, BF16, false, false>);
+    cudaError_t e = set_smem_once(kern, WindowLayout<D>::SMEM_BYTES, set[vl][overlap]);
     if (e != cudaSuccess)
         return e;
-    const int ctas = p.k.units < p.k.num_sms ? p.k.units : p.k.num_sms;
-    kern<<<ctas, NUM_THREADS, WindowLayout<D>::SMEM_BYTES, stream>>>(m.q, m.k, m.v, p);
+    kern<<<ctas, window_threads(overlap), WindowLayout<D>::SMEM_BYTES, stream>>>(m.q, m.k, m.v, p);
     return cudaGetLastError();
 }
 

@@ -296,6 +296,58 @@ def test_nan_and_infinity_stay_outside_the_window(D, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,dt", [(128, "bf16"), (256, "fp16")])
+@pytest.mark.parametrize("Sq,Skv", [(150, 100), (300, 300), (129, 700), (300, 5)])
+def test_a_large_batch_has_the_bits_of_its_parts(Sq, Skv, D, dt):
+    """Several units a CTA, whose rows a warpgroup of its own writes, against one unit a CTA at most; rows
+    without a key, and values that are not finite in and out of sight."""
+    g = torch.Generator(device="cuda").manual_seed(Sq + Skv)
+    dtype, W, sinks = DTYPES[dt], 40, 3
+    B, Hq, Hkv = 20, 8, 2
+    q = torch.randn(B, Hq, Sq, D, device="cuda", generator=g).to(dtype)
+    k, v = (torch.randn(B, Hkv, Skv, D, device="cuda", generator=g).to(dtype) for _ in range(2))
+    v[1, 0, Skv // 2, 3], v[2, 1, 0, 7], k[3, 1, Skv - 1, 0] = math.inf, math.nan, math.nan
+    q[4, 5, Sq // 2, 1] = math.nan
+    o, lse = sdp.fwd_window(q, k, v, W, sinks=sinks)
+    for b in range(B):
+        ob, lb = sdp.fwd_window(q[b:b + 1], k[b:b + 1], v[b:b + 1], W, sinks=sinks)
+        assert torch.equal(ob[0].view(torch.int16), o[b].view(torch.int16)) or torch.equal(
+            torch.nan_to_num(ob[0], nan=9), torch.nan_to_num(o[b], nan=9))
+        assert torch.equal(torch.nan_to_num(lb[0], nan=9), torch.nan_to_num(lse[b], nan=9))
+    # the same rows as a packed batch
+    pack = [x.transpose(1, 2).reshape(-1, x.shape[1], D).contiguous() for x in (q, k, v)]
+    cu_q, cu_k = (torch.arange(B + 1, dtype=torch.int32, device="cuda") * n for n in (Sq, Skv))
+    ov, lv = sdp.fwd_varlen_window(*pack, cu_q, cu_k, Sq, W, sinks=sinks)
+    ov, lv = ov.view(B, Sq, Hq, D).transpose(1, 2), lv.view(Hq, B, Sq).transpose(0, 1)
+    assert torch.equal(torch.isnan(ov), torch.isnan(o)) and torch.equal(torch.isnan(lv), torch.isnan(lse))
+    # (a tile at the end of a sequence also holds the next one's first keys: where those are not finite the rows
+    # before them are computed again, in other steps, so bits are compared behind the last such sequence)
+    assert torch.equal(torch.nan_to_num(ov[4:], nan=9), torch.nan_to_num(o[4:], nan=9))
+    assert torch.equal(torch.nan_to_num(lv[4:], nan=9), torch.nan_to_num(lse[4:], nan=9))
+    assert sdp.poll_status() == sdp.SDP_OK
+    rows = torch.isnan(o).any(-1)
+    assert not rows[[0] + list(range(5, B))].any()
+    assert int(rows[4].sum()) == (1 if Skv - Sq + Sq // 2 >= 0 else 0)  # a row without a key is 0, whatever its query
+    if Skv < Sq:
+        assert (o[:, :, :Sq - Skv][[0] + list(range(5, B))] == 0).all()
+
+
+@pytest.mark.gpu
+def test_waits_that_run_out_end_a_large_batch():
+    q, k, v = (torch.randn(8, 32, 300, 128, device="cuda").half() for _ in range(3))
+    want, lwant = sdp.fwd_window(q, k, v, 70)
+    old_ms, old = sdp.set_wait_timeout_ms(20), sdp.set_debug_flags(1)
+    try:
+        sdp.fwd_window(q, k, v, 70)
+        assert sdp.poll_status() == sdp.SDP_ERR_DEVICE_TIMEOUT
+    finally:
+        sdp.set_wait_timeout_ms(old_ms)
+        sdp.set_debug_flags(old)
+    o, lse = sdp.fwd_window(q, k, v, 70)
+    assert sdp.poll_status() == sdp.SDP_OK and torch.equal(o, want) and torch.equal(lse, lwant)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("flags", [0, 32], ids=["compact", "full_grid"])
 def test_bad_offsets_are_reported_and_skipped(flags):
     g = torch.Generator(device="cuda").manual_seed(7)
