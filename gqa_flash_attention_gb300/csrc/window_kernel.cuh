@@ -342,15 +342,16 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     // Bounded waits as in the forward kernels, but inline: a call in a branch with registers of its own
-    // (setmaxnreg) does not assemble.
-    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site) -> bool {
+    // (setmaxnreg) does not assemble. The limit holds a tile: who waits for `tiles` of them waits that much longer
+    // (and stops with the others when the tile's own wait has run out).
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site, int tiles = 1) -> bool {
         bool done = ptx::mbar_try_wait(bar, parity);
         if (!__all_sync(0xffffffffu, done)) {
             const uint64_t t0 = ptx::globaltimer_ns();
             for (uint32_t it = 1; !__all_sync(0xffffffffu, done = ptx::mbar_try_wait(bar, parity)); ++it) {
                 if ((it & 15u) != 0)
                     continue;
-                const bool late = ptx::globaltimer_ns() - t0 > p.timeout_ns;
+                const bool late = static_cast<float>(ptx::globaltimer_ns() - t0) > static_cast<float>(p.timeout_ns) * tiles;
                 if (__any_sync(0xffffffffu, late || *abort_flag)) {
                     if (late && !done) {
                         *abort_flag = 1;
@@ -643,12 +644,14 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
             }
         } else if constexpr (OVERLAP) {
             // ------------------------------------------ the units, ahead of the others
+            int longest = 1;  // of the units so far: its end may be what a place in the ring waits for
             for (int i = 0;; ++i) {
                 if (i > 0)
                     ahead = next_unit();
                 const int at = i % WL::UNITS;
-                if (i >= WL::UNITS && !wait_all(unit_free0 + 8u * at, (i / WL::UNITS - 1) & 1, SITE_Q_FULL))
+                if (i >= WL::UNITS && !wait_all(unit_free0 + 8u * at, (i / WL::UNITS - 1) & 1, SITE_Q_FULL, longest))
                     break;
+                longest = max(longest, ahead.n);
                 if (lane == 0) {
                     ring[at] = ahead;
                     ptx::mbar_arrive(unit_full0 + 8u * at);
@@ -823,7 +826,7 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                 continue;
             }
             const int b = k & 1;
-            if (!(ok = wait_all(sum_full0 + 8u * b, (k >> 1) & 1, SITE_O_DONE)))
+            if (!(ok = wait_all(sum_full0 + 8u * b, (k >> 1) & 1, SITE_O_DONE, n)))
                 break;
             const float inv_l = row_factor[b * L::BM + row];
             __syncwarp();

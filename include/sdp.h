@@ -388,6 +388,7 @@ unsigned int sdp_last_status_detail(void);
 /*
  * sdp_set_wait_timeout_ms — upper bound, in milliseconds, on any single wait
  * inside the kernel (default 2000). Applies to launches made after the call.
+ * (A warp of the sliding-window kernel that waits for several tiles of another has the limit for each.)
  * Returns the previous value. 0 restores the default.
  */
 unsigned int sdp_set_wait_timeout_ms(unsigned int ms);
