@@ -12,7 +12,7 @@ constexpr int kMaxRows = 32;
 struct Shape {
     bool wide;  // 16 columns a warp, else 8
     int chunks, sms, part_cols;
-    long long workspace_bytes;
+    long long parts_bytes, workspace_bytes;
 };
 
 int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, Shape *sh)
@@ -41,8 +41,9 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, Shape *sh)
     // two parts a warp: the problem it continues and the one it begins
     const int warps = D == 128 ? (sh->wide ? sdp::c4::Plan<128, 2>::WARPS : sdp::c4::Plan<128, 1>::WARPS)
                                : (sh->wide ? sdp::c4::Plan<256, 2>::WARPS : sdp::c4::Plan<256, 1>::WARPS);
-    sh->workspace_bytes = 2LL * sms * warps * 4 *
-                          (D == 128 ? sdp::c4::part_floats<128>(sh->part_cols) : sdp::c4::part_floats<256>(sh->part_cols));
+    sh->parts_bytes = 2LL * sms * warps * 4 *
+                      (D == 128 ? sdp::c4::part_floats<128>(sh->part_cols) : sdp::c4::part_floats<256>(sh->part_cols));
+    sh->workspace_bytes = sh->parts_bytes + static_cast<long long>(nseq) * Hkv * chunks * static_cast<long long>(sizeof(int2));
     return SDP_OK;
 }
 
@@ -101,6 +102,7 @@ extern "C" int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_
     p.table = block_table;
     p.lens = cache_lens;
     p.workspace = static_cast<float *>(workspace);
+    p.joins = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + sh.parts_bytes);
     p.timeout_ns = sdp::wait_timeout_ns();
     p.table_stride = table_stride;
     p.num_pages = num_pages;

@@ -34,13 +34,14 @@
 //   few columns fill the n side. p s turns from S's layout (token rows) to P's (column rows) by one
 //   movmatrix.
 //
-// What bounds it now: with 64 ragged sequences of up to 4096 keys (D = 128, 4 columns) 80 % of the
-// time the integer units, the issue slots (60 % each) and the latency between dependent
-// instructions, at four warps a scheduler: O, the ring and a tile's fragments leave registers for
-// no more. DRAM is at 36 % and the tensor pipe at 14 %. (The products on tcgen05 with e4m3 codes, the
-// unpacked codes passing through tensor and shared memory between warps of different roles, took
-// 89 us there and 76 us for 8 x 16384 at D = 256, against 61.8 and 57.4: a tile's chain of hand-overs is longer
-// than its share of the copy rate, and neither two CTAs an SM nor deeper rings hid it.)
+// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 57.7 us with the join): the
+// latency between dependent instructions at four warps a scheduler, with half of the integer units' and
+// 58 % of the issue slots' rate in use; O, the ring and a tile's fragments leave registers for no more
+// warps. DRAM is at 40 % and the tensor pipe at 17 %. With 16 columns at D = 256 (two warps a scheduler) the
+// slots are 31 % busy: 56 us for 8 x 16384. (The products on tcgen05 with e4m3 codes, the unpacked codes
+// passing through tensor and shared memory between warps of different roles, took 89 and 76 us: a tile's
+// chain of hand-overs is longer than its share of the copy rate, and neither two CTAs an SM nor deeper
+// rings hid it.)
 //
 // Work split: all sequences' tiles of 32 tokens are numbered sequence by sequence, KV head by KV
 // head (each problem with OVERHEAD positions more for its start), and cut into equal runs, one a
@@ -74,6 +75,7 @@ struct Cache4AttnParams {
     const uint32_t *k_scales, *v_scales;
     const int *table, *lens;
     float *workspace;
+    int2 *joins;             // behind the parts: of each problem its first run and its parts (0: written directly)
     unsigned int *status;
     unsigned long long timeout_ns;
     long long table_stride;
@@ -626,6 +628,16 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         ptx::fence_barrier_init();
     }
     // ---- where this warp's run starts: prefix sums of the sequences' positions, a few sequences a thread
+    const int run = warp * gridDim.x + blockIdx.x;  // consecutive runs lie on different SMs, so that few runs use many
+    // positions in all, from the warps' sums (which stay where they are)
+    auto positions = [&]() {
+        const long long *warp_sum = reinterpret_cast<const long long *>(smem + P::PREFIX) + THREADS;
+        long long total = 0;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i)
+            total += warp_sum[i];
+        return total;
+    };
     Walk ahead;  // the copies' place in the run
     {
         long long *prefix = reinterpret_cast<long long *>(smem + P::PREFIX), *warp_sum = prefix + THREADS;
@@ -649,13 +661,8 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         if (lane == 31)
             warp_sum[warp] = incl;
         __syncthreads();
-        long long total = 0;
-#pragma unroll
-        for (int w = 0; w < WARPS; ++w)
-            total += warp_sum[w];
+        const long long total = positions();
         const int busy = busy_runs(p, total);
-        // consecutive runs lie on different SMs, so that few runs use many
-        const int run = warp * gridDim.x + blockIdx.x;
         if (run >= busy)
             return;
         const long long x = run_start(total, run, busy);
@@ -758,7 +765,6 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         step_slot();
     };
 
-    const int run = warp * gridDim.x + blockIdx.x;
     const int R = p.n * p.G;
     Tile<D, BF16, NT> t;
     for (; !w.done(); w.find(p)) {
@@ -872,6 +878,16 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
         // ---- the segment's result: a lane holds channels 8 row8 .. + 7 of each group, of columns
         // 2 quad and 2 quad + 1
         const bool direct = w.e0 == 0 && w.e1 == w.sp.count;
+        if (w.e0 == 0 && lane == 0) {  // for the join
+            int parts = 0;
+            if (!direct) {  // the run ends in the problem, whose last tile some run after it holds
+                const long long total = positions();
+                const int busy = busy_runs(p, total);
+                const long long last = run_start(total, run + 1, busy) + (w.sp.count - w.e1) - 1;
+                parts = static_cast<int>(((last + 1) * busy - 1) / total) - run + 1;
+            }
+            p.joins[w.s * p.Hkv * p.chunks + w.u] = make_int2(run, parts);
+        }
         const float bound = __uint_as_float(t.s_bits << 16);
         // a part that continues a problem is this run's first segment, one that begins it its last
         float *part = p.workspace + (static_cast<long long>(run) * 2 + (w.e0 == 0 ? 1 : 0)) * part_floats<D>(p.part_cols);
@@ -923,82 +939,52 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
 }
 
 // Joins the parts of every problem that more than one run shares, in the order of the runs, and
-// writes the rows of empty sequences. One block a column of a problem: D / 4 threads hold its
-// channels, four each, and the block's THREADS / (D / 4) groups of them take every so-many-th part,
-// so that the parts of a long problem (57 at four sequences of 32768 keys) are read at once and not
-// one after the other.
-template <int D, bool BF16, int NT>
+// writes the rows of empty sequences. A block takes one column of a problem, its eight warps every eighth
+// part each, so that the parts of a long problem (76 at eight sequences of 16384 keys) are read at once and not one
+// after the other; or (ONE, with many problems, of a few parts each) a column a warp. The attention leaves each
+// problem's first run and parts: with every block finding them from the lengths, 2048 blocks took 11 us and 8192 took 42.
+template <int D, bool BF16, int NT, bool ONE>
 __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const Cache4AttnParams p)
 {
     using namespace c4;
-    constexpr int THREADS = MERGE_THREADS, WARPS = THREADS / 32, LANES = D / 4, GROUPS = THREADS / LANES;
-    __shared__ long long both[2][WARPS];
-    __shared__ float4 y_all[GROUPS][LANES];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int per_seq = p.Hkv * p.chunks;
-    const int col = blockIdx.x % p.part_cols, problem = blockIdx.x / p.part_cols;
+    constexpr int WARPS = MERGE_THREADS / 32, V = D / 128;  // V float4 a lane
+    __shared__ float4 y_all[ONE ? 1 : WARPS][32 * V];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_seq = p.Hkv * p.chunks, pc = p.part_cols;
+    const int blocks = ONE ? (pc + WARPS - 1) / WARPS : pc;  // of a problem
+    const int problem = blockIdx.x / blocks, at = blockIdx.x - problem * blocks;
+    const int col = ONE ? at * WARPS + warp : at;
     const int s = problem / per_seq, u = problem - s * per_seq;
     const int g = u / p.chunks, r = (u - g * p.chunks) * 8 * NT + col;
     const Span sp = span_of(p, s);
-    // positions before this sequence, and in all
-    long long before = 0, total = 0;
-    {
-        for (int i = tid; i < p.nseq; i += THREADS) {
-            const long long n = problem_length(span_of(p, i));
-            total += n;
-            before += i < s ? n : 0;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            before += __shfl_xor_sync(FULL, before, off);
-            total += __shfl_xor_sync(FULL, total, off);
-        }
-        if (lane == 0) {
-            both[0][warp] = before;
-            both[1][warp] = total;
-        }
-        __syncthreads();
-        before = total = 0;
-#pragma unroll
-        for (int i = 0; i < WARPS; ++i) {
-            before += both[0][i];
-            total += both[1][i];
-        }
-    }
-    before *= per_seq;
-    total *= per_seq;
-    // What is above needs only the lengths and runs beside the attention's end. Every thread waits for that
-    // end: what follows on the stream waits for this kernel alone.
+    // What is above runs beside the attention's end. Every thread waits for that end: what follows on the
+    // stream waits for this kernel alone.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (r >= p.n * p.G)
+    if (col >= pc || r >= p.n * p.G)
         return;
     const long long row = (static_cast<long long>(s) * p.n + r / p.G) * p.Hq + g * p.G + r % p.G;
     if (sp.count == 0) {
         if (sp.bad) {
-            if (tid == 0)
+            if (lane == 0)
                 atomicCAS(p.status, 0u, kBadSeqlens);
             return;
         }
-        if (tid < D / 8)
-            reinterpret_cast<uint4 *>(p.o + row * D)[tid] = make_uint4(0u, 0u, 0u, 0u);
-        if (tid == 0 && p.lse != nullptr)
+        if ((ONE || warp == 0) && lane < D / 8)
+            reinterpret_cast<uint4 *>(p.o + row * D)[lane] = make_uint4(0u, 0u, 0u, 0u);
+        if ((ONE || warp == 0) && lane == 0 && p.lse != nullptr)
             p.lse[row] = -INFINITY;
         return;
     }
-    // the problem's tiles, behind its OVERHEAD
-    const long long u0 = before + u * problem_length(sp) + OVERHEAD, u1 = u0 + sp.count;
-    const int busy = busy_runs(p, total);
-    // the run that holds position x: the largest i with run_start(i) <= x
-    const int i0 = static_cast<int>(((u0 + 1) * busy - 1) / total), i1 = static_cast<int>((u1 * busy - 1) / total);
-    if (i0 == i1)
-        return;  // written by the run's warp itself
-    const int parts = i1 - i0 + 1, pc = p.part_cols;
+    const int2 join = p.joins[problem];
+    const int i0 = join.x, parts = join.y;
+    // nothing to join; or the word was never written (a wait ran out, and the status says so)
+    if (parts < 2 || i0 < 0 || parts > p.runs - i0)
+        return;
     // part x (run i0 + x): the first begins the problem (slot 1), the others continue it (slot 0)
     auto part = [&](int x) { return p.workspace + (2LL * (i0 + x) + (x == 0 ? 1 : 0)) * part_floats<D>(pc); };
-    // every group finds the maximum for itself (its threads read the same words)
-    const int grp = tid / LANES, c4x = tid % LANES;
     auto m_of = [&](int x) { return part(x)[pc * D + col]; };
     auto l_of = [&](int x) { return part(x)[pc * (D + 1) + col]; };
+    // every warp finds the maximum and the sum for itself
     const float m0 = lane < parts ? m_of(lane) : -INFINITY, l0 = lane < parts ? l_of(lane) : 0.f;
     float mx = m0;
     for (int x = lane + 32; x < parts; x += 32)
@@ -1015,32 +1001,46 @@ __global__ void __launch_bounds__(c4::MERGE_THREADS) cache4_merge_kernel(const C
     for (int off = 16; off > 0; off >>= 1)
         sum += __shfl_xor_sync(FULL, sum, off);
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = grp; x < parts; x += GROUPS) {
-        const float *src = part(x);
-        const float4 t = reinterpret_cast<const float4 *>(src + col * D)[c4x];
-        const float f = weight(m_of(x), l_of(x)) * inv;
-        y.x = fmaf(f, t.x, y.x);
-        y.y = fmaf(f, t.y, y.y);
-        y.z = fmaf(f, t.z, y.z);
-        y.w = fmaf(f, t.w, y.w);
-    }
-    y_all[grp][c4x] = y;
-    __syncthreads();
-    if (grp != 0)
-        return;
+    float4 y[V];
 #pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-        const float4 t = y_all[i][c4x];
-        y.x += t.x;
-        y.y += t.y;
-        y.z += t.z;
-        y.w += t.w;
+    for (int i = 0; i < V; ++i)
+        y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = ONE ? 0 : warp; x < parts; x += ONE ? 1 : WARPS) {
+        const float4 *src = reinterpret_cast<const float4 *>(part(x) + col * D);
+        const float f = weight(m_of(x), l_of(x)) * inv;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float4 t = src[i * 32 + lane];
+            y[i].x = fmaf(f, t.x, y[i].x);
+            y[i].y = fmaf(f, t.y, y[i].y);
+            y[i].z = fmaf(f, t.z, y[i].z);
+            y[i].w = fmaf(f, t.w, y[i].w);
+        }
     }
-    reinterpret_cast<uint2 *>(p.o + row * D)[c4x] =
-        make_uint2(pack16<BF16>(y.x, y.y), pack16<BF16>(y.z, y.w));
-    if (c4x == 0 && p.lse != nullptr)
+    if constexpr (!ONE) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            y_all[warp][i * 32 + lane] = y[i];
+        __syncthreads();
+        if (warp != 0)
+            return;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float4 t = y_all[w][i * 32 + lane];
+                y[i].x += t.x;
+                y[i].y += t.y;
+                y[i].z += t.z;
+                y[i].w += t.w;
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        reinterpret_cast<uint2 *>(p.o + row * D)[i * 32 + lane] =
+            make_uint2(pack16<BF16>(y[i].x, y[i].y), pack16<BF16>(y[i].z, y[i].w));
+    if (lane == 0 && p.lse != nullptr)
         p.lse[row] = sum == 0.f ? -INFINITY : (mx + log2f(sum)) * kLn2;
 }
 
@@ -1062,12 +1062,17 @@ cudaError_t launch_cache4_attn(Cache4AttnParams p, int sms, cudaStream_t st)
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t config{};
-    config.gridDim = dim3(p.nseq * p.Hkv * p.chunks * p.part_cols);
+    // a column a warp once that still gives every SM two blocks
+    const int problems = p.nseq * p.Hkv * p.chunks;
+    const bool one = problems >= 2 * sms;
+    constexpr int WARPS = c4::MERGE_THREADS / 32;
+    config.gridDim = dim3(problems * (one ? (p.part_cols + WARPS - 1) / WARPS : p.part_cols));
     config.blockDim = dim3(c4::MERGE_THREADS);
     config.stream = st;
     config.attrs = &early;
     config.numAttrs = 1;
-    return cudaLaunchKernelEx(&config, cache4_merge_kernel<D, BF16, NT>, p);
+    return one ? cudaLaunchKernelEx(&config, cache4_merge_kernel<D, BF16, NT, true>, p)
+               : cudaLaunchKernelEx(&config, cache4_merge_kernel<D, BF16, NT, false>, p);
 }
 
 // One per (head dim, dtype): 8 columns a warp up to that many, else 16.

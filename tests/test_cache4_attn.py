@@ -199,6 +199,31 @@ def test_many_sequences(nseq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D,dt,rows", [(256, "fp16", 1), (128, "bf16", 2)])
+def test_many_problems_of_many_columns(D, dt, rows):
+    """Joins of a column a warp, more columns than a block has warps, one long sequence among short and empty
+    ones; a bad length in their midst leaves its own rows alone."""
+    g = torch.Generator().manual_seed(D)
+    dtype, Hq, Hkv = DTYPES[dt], 40, 2
+    lens = torch.randint(0, 90, (170,), generator=g).tolist()
+    lens[33], lens[100:103] = 2100, [0, 0, 1]
+    cache, table, ks, vs = fill(lens, Hkv, D, 16, dtype, g)
+    q = torch.randn(len(lens), rows, Hq, D, generator=g).to(dtype).cuda()
+    dl = torch.tensor(lens, dtype=torch.int32)
+    ws = torch.full((sdp.cache4_workspace_bytes(len(lens), rows, Hq, Hkv, D, dtype),), 255, dtype=torch.uint8, device="cuda")
+    o, lse = sdp.fwd_cache4(q, cache, dl.cuda(), table.cuda(), workspace=ws)
+    assert sdp.poll_status() == sdp.SDP_OK
+    check(q, o, lse, lens, ks, vs, dtype)
+    dl[50] = -3
+    o2 = torch.full_like(o, 9)
+    _, lse2 = sdp.fwd_cache4(q, cache, dl.cuda(), table.cuda(), out=o2, workspace=ws)
+    assert sdp.poll_status() == sdp.SDP_ERR_BAD_SEQLENS
+    assert (o2[50] == 9).all()
+    keep = [i for i in range(len(lens)) if i != 50]
+    check(q[keep], o2[keep], lse2[keep], [lens[i] for i in keep], [ks[i] for i in keep], [vs[i] for i in keep], dtype)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.3])
 @pytest.mark.parametrize("dt", ["fp16", "bf16"])
 def test_scales_and_loud_keys(scale, dt):
