@@ -10,8 +10,6 @@
 
 namespace {
 
-// Sequences a variable-length batch may have for the compact list of its tiles (as sdp_fwd_varlen).
-constexpr int kCompactMaxSeqs = 512;
 constexpr int kDebugNoPack = 4;
 constexpr int kDebugFullVarlenGrid = 32;
 
@@ -156,7 +154,7 @@ extern "C" int sdp_fwd_varlen_window(const void *q, const void *k, const void *v
     p.k.nseq = nseq;
     const long long slots = std::min(static_cast<long long>(nseq) * n_qtiles,
                                      (static_cast<long long>(total_q) + 127LL * nseq) / 128);
-    const bool compact = nseq <= kCompactMaxSeqs && !(p.k.debug_flags & kDebugFullVarlenGrid);
+    const bool compact = !(p.k.debug_flags & kDebugFullVarlenGrid);
     p.k.n_tiles = compact ? static_cast<int>(slots) : 0;
     p.k.units = static_cast<int>(compact ? slots * Hq : units * n_qtiles);
     p.q_plane = D;

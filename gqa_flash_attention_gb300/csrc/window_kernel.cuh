@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
         int z_q, z_kv, q0, q_row, kv_row0, sq, pos0, t_lo, ns, n, unused[2];
         __device__ __forceinline__ int tile(int j) const { return j < ns ? j : t_lo + j - ns; }
     };
+    int from = 0, before = 0;  // a sequence, and the tiles of those before it
     auto unit_of = [&](int u) {  // by a whole warp
         Unit r{};
         r.n = -1;
@@ -222,16 +223,17 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
         u /= p.G;
         if constexpr (VARLEN) {
             if (p.n_tiles > 0) {
-                // tile t of the list of those that exist, in sequence order: the sequence, from the sums of
-                // their tiles, 32 sequences a step (CTA 0 looks all of them over for bad offsets)
+                // Tile t of the list of those that exist, in sequence order: its sequence, from the sums of their
+                // tiles, 32 sequences a step. A CTA's units move on through the list, so the search goes on from
+                // the last one's place.
                 const int t = u % p.n_tiles, g = u / p.n_tiles;
                 const VarlenScan v{p.cu_q, p.cu_k, p.nseq, p.n_qtiles, p.Sq, p.Skv};
+                if (t < before)
+                    from = before = 0;
                 int found = -1;
-                for (int base = 0, acc = 0; base < p.nseq && (found < 0 || blockIdx.x == 0); base += 32) {
+                for (; from < p.nseq; from += 32) {
                     bool bad;
-                    const int tiles = varlen_tiles(v, base + lane, bad);
-                    if (bad && blockIdx.x == 0)
-                        atomicCAS(p.status, 0u, static_cast<unsigned>(SITE_SEQLENS));
+                    const int tiles = varlen_tiles(v, from + lane, bad);
                     int incl = tiles;
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1) {
@@ -239,13 +241,14 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                         if (lane >= d)
                             incl += x;
                     }
-                    incl += acc;
+                    incl += before;
                     const unsigned hit = __ballot_sync(0xffffffffu, incl - tiles <= t && t < incl);
                     if (hit != 0u) {
                         const int src = __ffs(hit) - 1;
-                        found = ((base + src) * p.Hkv + g) * p.n_qtiles + t - __shfl_sync(0xffffffffu, incl - tiles, src);
+                        found = ((from + src) * p.Hkv + g) * p.n_qtiles + t - __shfl_sync(0xffffffffu, incl - tiles, src);
+                        break;
                     }
-                    acc = __shfl_sync(0xffffffffu, incl, 31);
+                    before = __shfl_sync(0xffffffffu, incl, 31);
                 }
                 if (found < 0)
                     return r;  // a slot past the last query tile
@@ -324,6 +327,15 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
     // OVERLAP: warp 7 looks up the units blockIdx.x, + gridDim.x, ... ahead of the others (in a batch of odd lengths
     // that takes a search and a few dependent loads) and hands those with rows on through a ring. Else a CTA has
     // one unit, which every warp looks up. k counts those with tiles.
+    if (VARLEN && p.n_tiles > 0 && blockIdx.x == 0 && warp == 7) {  // all offsets: a bad sequence has no unit
+        const VarlenScan v{p.cu_q, p.cu_k, p.nseq, p.n_qtiles, p.Sq, p.Skv};
+        for (int i = lane; i < p.nseq; i += 32) {
+            bool bad;
+            varlen_tiles(v, i, bad);
+            if (bad)
+                atomicCAS(p.status, 0u, static_cast<unsigned>(SITE_SEQLENS));
+        }
+    }
     int u = static_cast<int>(blockIdx.x);
     auto next_unit = [&]() {
         Unit r;

@@ -356,10 +356,9 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
  *
  * Layouts, ownership, errors and streams as sdp_fwd and sdp_fwd_varlen (offsets are checked by
  * the kernel and reported by sdp_poll_status); fewer than 2^30 rows or keys. Keys and values
- * that a row does not see may hold infinities or NaN: they do not reach it. In a batch of up to
- * 512 sequences the work is the tiles that exist, beyond that the longest sequence's for each. A
- * launch runs the same kernel when it is captured; nothing is allocated after the first call on a
- * device. The wait limit and debug flags 1, 4 and 32 apply.
+ * that a row does not see may hold infinities or NaN: they do not reach it. The work of a packed
+ * batch is the tiles that exist. A launch runs the same kernel when it is captured; nothing is
+ * allocated after the first call on a device. The wait limit and debug flags 1, 4 and 32 apply.
  */
 int sdp_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq, int Hkv, int Sq,
                    int Skv, int D, float scale, int dtype, int window, int sinks, void *stream);

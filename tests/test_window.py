@@ -230,6 +230,26 @@ def test_many_sequences(nseq):
 
 
 @pytest.mark.gpu
+def test_one_long_sequence_among_many():
+    """The list of tiles that exist against a tile of the longest sequence for every sequence: the same bits."""
+    g = torch.Generator().manual_seed(3)
+    lq = torch.randint(0, 20, (1100,), generator=g)
+    lq[[5, 800]] = torch.tensor([1500, 300])
+    lk = lq + torch.randint(0, 9, (1100,), generator=g)
+    cu_q, cu_k = (torch.cat((torch.zeros(1, dtype=torch.int64), n.cumsum(0))).int().cuda() for n in (lq, lk))
+    q = torch.randn(int(lq.sum()), 8, 128, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(int(lk.sum()), 2, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    o, lse = sdp.fwd_varlen_window(q, k, v, cu_q, cu_k, 1500, 64, sinks=2)
+    old = sdp.set_debug_flags(32)
+    try:
+        of, lf = sdp.fwd_varlen_window(q, k, v, cu_q, cu_k, 1500, 64, sinks=2)
+    finally:
+        sdp.set_debug_flags(old)
+    assert sdp.poll_status() == sdp.SDP_OK
+    assert torch.equal(o, of) and torch.equal(lse, lf) and torch.isfinite(o).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [128, 256])
 @pytest.mark.parametrize("scale", [0.0, -0.1, 2.0])
 def test_scales_and_peaks(scale, D):
