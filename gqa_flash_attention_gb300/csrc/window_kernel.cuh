@@ -22,8 +22,9 @@
 //    a CTA at most has no next unit to go on with, and the hand-overs cost it 1.8 us of 8.3: it
 //    runs without them (OVERLAP). O leaves tensor memory 32 columns at a time, stored as it comes: taken
 //    out whole first, which frees it earlier, the first was slower (812 us), its unrolled code larger.
-//  - What bounds it: at D = 128 the softmax (1390 cycles a tile, 1024 of them the exponentials at their
-//    rate); at D = 256 the products (2048 cycles a tile at the tensor cores' rate, 2130 measured) and
+//  - What bounds it: at D = 128 the softmax warps' chain a tile (tensor-memory load, maximum, exponentials,
+//    store: 1390 cycles where the products take 1024, the exponentials' pipe at a third of its rate);
+//    at D = 256 the products (2048 cycles a tile at the tensor cores' rate, 2130 measured) and
 //    what is left at a unit's end, the last product, O's way out and the next unit's first product
 //    one after the other.
 //  - Only the tiles that cut a window or the diagonal (two or three a unit, plus the sinks') are
