@@ -377,6 +377,38 @@ def test_a_captured_step_follows_lengths_and_pages():
 
 
 @pytest.mark.gpu
+def test_two_graphs_at_once_with_a_workspace_each():
+    """Their joins start beside the attention of either; a following call in the graph reads what they wrote."""
+    g = torch.Generator().manual_seed(16)
+    lens = [[1500, 40, 0], [700, 900, 5]]
+    graphs, res, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for ln in lens:
+        cache, table, ks, vs = fill(ln, 2, 128, 32, torch.bfloat16, g)
+        q = torch.randn(3, 1, 8, 128, generator=g).bfloat16().cuda()
+        dl, t = torch.tensor(ln, dtype=torch.int32).cuda(), table.cuda()
+        ws = torch.empty(sdp.cache4_workspace_bytes(3, 1, 8, 2, 128, torch.bfloat16), dtype=torch.uint8, device="cuda")
+        o, lse, copy = torch.zeros_like(q), torch.zeros(3, 1, 8).cuda(), torch.zeros_like(q)
+        sdp.fwd_cache4(q, cache, dl, t, out=o, lse=lse, workspace=ws)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(3):
+                sdp.fwd_cache4(q, cache, dl, t, out=o, lse=lse, workspace=ws)
+                copy.copy_(o)
+                o.zero_()
+        graphs.append(graph)
+        res.append((q, copy, lse, ln, ks, vs, (cache, dl, t, ws, o)))
+    for _ in range(5):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for q, o, lse, ln, ks, vs, _ in res:
+        check(q, o, lse, ln, ks, vs, torch.bfloat16)
+    assert sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once_and_binding_checks():
     g = torch.Generator().manual_seed(15)
     lens = [3000, 1500, 64]

@@ -353,6 +353,36 @@ def test_a_large_batch_has_the_bits_of_its_parts(Sq, Skv, D, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_large_batches_in_graphs_on_two_streams(D):
+    """Two graphs with several units a CTA, replayed at once with new inputs."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    sets = [[torch.randn(6, h, 500, D, device="cuda", generator=g).half() for h in (16, 4, 4)] for _ in range(2)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(2)]
+    for q, k, v in sets:
+        sdp.fwd_window(q, k, v, 130, sinks=5)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(sdp.fwd_window(q, k, v, 130, sinks=5))
+        graphs.append(graph)
+    for step in range(3):
+        for x in sets:
+            for t in x:
+                t.copy_(torch.randn(t.shape, device="cuda", generator=g))
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for (q, k, v), (o, lse) in zip(sets, outs):
+            want, lwant = sdp.fwd_window(q, k, v, 130, sinks=5)
+            assert torch.equal(o, want) and torch.equal(lse, lwant)
+    assert sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
 def test_waits_that_run_out_end_a_large_batch():
     q, k, v = (torch.randn(8, 32, 300, 128, device="cuda").half() for _ in range(3))
     want, lwant = sdp.fwd_window(q, k, v, 70)
