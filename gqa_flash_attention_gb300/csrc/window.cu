@@ -93,6 +93,7 @@ extern "C" int sdp_fwd_window(const void *q, const void *k, const void *v, void 
     sdp::LaunchMaps m;
     if ((rc = sdp::tensor_map(&m.q, q, dtype, D, rows, planes_q, 128)) != SDP_OK ||
         (rc = sdp::tensor_map(&m.k, k, dtype, D, Skv, planes_kv, 128)) != SDP_OK ||
+        (rc = sdp::tensor_map(&m.k_half, k, dtype, D, Skv, planes_kv, 64)) != SDP_OK ||
         (rc = sdp::tensor_map(&m.v, v, dtype, D, Skv, planes_kv, 128)) != SDP_OK)
         return rc;
     p.k.Hq = heads;
@@ -141,6 +142,7 @@ extern "C" int sdp_fwd_varlen_window(const void *q, const void *k, const void *v
     sdp::LaunchMaps m;
     if ((rc = sdp::tensor_map_thd(&m.q, q, dtype, D, total_q, Hq, 128)) != SDP_OK ||
         (rc = sdp::tensor_map_thd(&m.k, k, dtype, D, kv_rows, Hkv, 128)) != SDP_OK ||
+        (rc = sdp::tensor_map_thd(&m.k_half, k, dtype, D, kv_rows, Hkv, 64)) != SDP_OK ||
         (rc = sdp::tensor_map_thd(&m.v, v, dtype, D, kv_rows, Hkv, 128)) != SDP_OK)
         return rc;
     p.k.Hq = Hq;

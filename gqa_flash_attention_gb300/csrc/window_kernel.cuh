@@ -20,13 +20,17 @@
 //    passed at each unit's end at D = 256 (1.1 us a tile), and 12 packed prompts (W = 1024, D = 256)
 //    took 903 us instead of 789, 16384 rows (W = 4096, D = 128) 697 instead of 634. A launch of one unit
 //    a CTA at most has no next unit to go on with, and the hand-overs cost it 1.8 us of 8.3: it
-//    runs without them (OVERLAP). O leaves tensor memory 32 columns at a time, stored as it comes: taken
+//    runs without them (WINDOW_ONE). O leaves tensor memory 32 columns at a time, stored as it comes: taken
 //    out whole first, which frees it earlier, the first was slower (812 us), its unrolled code larger.
-//  - What bounds it: at D = 128 the softmax warps' chain a tile (tensor-memory load, maximum, exponentials,
-//    store: 1390 cycles where the products take 1024, the exponentials' pipe at a third of its rate);
-//    at D = 256 the products (2048 cycles a tile at the tensor cores' rate, 2130 measured) and
-//    what is left at a unit's end, the last product, O's way out and the next unit's first product
-//    one after the other.
+//  - What bounds a tile on one SM is shared memory: the products read Q, K and V there and the copies write
+//    K and V, 160 KB a tile at D = 128 and 320 KB at D = 256, where an SM moves 128 bytes a cycle (1280 and
+//    2560 cycles; 1210 to 1390 and 2570 measured; the products alone take 1024 and 2048). So at D = 256 two CTAs
+//    run as a pair (WINDOW_PAIR): two heads of a group have the same window, each CTA holds half of
+//    each K and V tile, and one product of 256 rows reads both halves: 12 packed prompts 786 -> 724 us. At
+//    D = 128 the softmax warps' chain is nearly as long as the copies, and the pair's hand-overs between
+//    CTAs cost more than the copies saved (634 -> 704 us), so it keeps to one CTA. (Half of a tile's keys
+//    a thread, in two softmax warpgroups, took 699 us; handing P over in four parts, which a pair of the
+//    dense kernel gains from, 750 us for the prompts.)
 //  - Only the tiles that cut a window or the diagonal (two or three a unit, plus the sinks') are
 //    masked, from four 32-bit words of visible keys a row; the others run without a test.
 //  - A row may see nothing in a tile, or at all (more rows than keys): its maximum stays -inf, its
@@ -36,7 +40,7 @@
 //    lies outside a window stays outside. Rows that are finite pay one multiply-add an element.
 #pragma once
 
-#include "sdp_fwd_kernel.cuh"
+#include "sdp_fwd_pair.cuh"
 
 namespace sdp {
 
@@ -49,19 +53,26 @@ struct WindowParams {
     int pack_sq;  // > 0: a group's query heads run as one head of G * pack_sq rows
 };
 
-template <int D>
+// How a launch runs: a unit a CTA, several a CTA with a warpgroup that writes their rows, or the latter by pairs of
+// CTAs.
+enum WindowForm { WINDOW_ONE, WINDOW_MANY, WINDOW_PAIR };
+
+template <int D, bool PAIR>
 struct WindowLayout {
     using L = Layout<D>;
+    using PL = PairLayout<D>;
     static constexpr int BAR_AREA = 512;
     // Query tiles in shared memory: two at D=128 (the next unit's Q loads while this unit runs),
     // one at D=256 (two would leave too few ring slots).
     static constexpr int QB = D == 128 ? 2 : 1;
-    static constexpr int NSLOTS = (L::SMEM_LIMIT - BAR_AREA - 2 * L::BM * 4 - 4 * 48 - 1024 - QB * L::Q_BYTES) / L::CHUNK_BYTES;
+    static constexpr int SLOT_BYTES = PAIR ? PL::HALF_BYTES : L::CHUNK_BYTES;
+    static constexpr int CPT = PAIR ? 1 : L::CHUNKS_PER_TILE;  // slots a K tile (or a V tile)
+    static constexpr int NSLOTS = (L::SMEM_LIMIT - BAR_AREA - 2 * L::BM * 4 - 4 * 48 - 1024 - QB * L::Q_BYTES) / SLOT_BYTES;
     // q_full[QB], slot_full[NS], slot_empty[NS], s_full[NB], p_full[NB], o_done[ring], final[2],
     // q_free[QB], o_free, sum_full[2], sum_free[2], unit_full[UNITS], unit_free[UNITS]
     static constexpr int UNITS = 4;  // units looked up ahead
     static constexpr int NBARS = QB + 2 * NSLOTS + 2 * L::NSBUF + O_DONE_RING + 2 + QB + 1 + 4 + 2 * UNITS;
-    static constexpr int BAR_OFF = QB * L::Q_BYTES + NSLOTS * L::CHUNK_BYTES;
+    static constexpr int BAR_OFF = QB * L::Q_BYTES + NSLOTS * SLOT_BYTES;
     static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, then the abort flag
     static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;  // two units' row factors, for the rows' ends
     static constexpr int UNIT_OFF = SUM_OFF + 2 * L::BM * 4;
@@ -166,20 +177,26 @@ constexpr int window_threads(bool overlap) { return overlap ? 384 : 256; }
 
 // OVERLAP: a warpgroup of its own writes a unit's rows while the softmax goes on with the next unit; without it the
 // softmax warps do.
-template <int D, bool BF16, bool VARLEN, bool OVERLAP>
-__global__ void __launch_bounds__(window_threads(OVERLAP), 1)
+template <int D, bool BF16, bool VARLEN, WindowForm FORM>
+__global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const WindowParams wp)
 {
+    constexpr bool PAIR = FORM == WINDOW_PAIR, OVERLAP = FORM != WINDOW_ONE;
     using L = Layout<D>;
-    using WL = WindowLayout<D>;
+    using PL = PairLayout<D>;
+    using WL = WindowLayout<D, PAIR>;
     const KernelParams &p = wp.k;
     constexpr int NS = WL::NSLOTS;
     constexpr int NB = L::NSBUF;
-    constexpr int CPT = L::CHUNKS_PER_TILE;
+    constexpr int CPT = WL::CPT;
     constexpr int QB = WL::QB;
     constexpr uint32_t IDESC_S = ptx::idesc_f16_f32acc(128, L::BN, BF16, false);
     constexpr uint32_t IDESC_PV = ptx::idesc_f16_f32acc(128, 128, BF16, true);
+    constexpr uint32_t IDESC_S2 = ptx::idesc_f16_f32acc(256, L::BN, BF16, false);
+    constexpr uint32_t IDESC_PV2 = ptx::idesc_f16_f32acc(256, D, BF16, true);
+    const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+    const bool leader = rank == 0;  // issues the pair's products; its barriers count both CTAs' loads and arrivals
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = ptx::smem_addr(smem_raw);
@@ -298,20 +315,20 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
         }
         for (int i = 0; i < NB; ++i) {
             ptx::mbar_init(s_full0 + 8u * i, 1);
-            ptx::mbar_init(p_full0 + 8u * i, 128);
+            ptx::mbar_init(p_full0 + 8u * i, PAIR ? 8 : 128);
         }
         for (int i = 0; i < O_DONE_RING; ++i)
             ptx::mbar_init(o_done0 + 8u * i, 1);
         ptx::mbar_init(final0, 1);
         ptx::mbar_init(final0 + 8u, 1);
-        ptx::mbar_init(o_free, 4);  // one arrival a warp of the rows' ends
+        ptx::mbar_init(o_free, PAIR ? 8 : 4);  // one arrival a warp of the rows' ends
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(sum_full0 + 8u * b, 128);
             ptx::mbar_init(sum_free0 + 8u * b, 4);
         }
         for (int i = 0; i < WL::UNITS; ++i) {
             ptx::mbar_init(unit_full0 + 8u * i, 1);
-            ptx::mbar_init(unit_free0 + 8u * i, 11);  // the warps that read it
+            ptx::mbar_init(unit_free0 + 8u * i, leader ? 11 : 9);  // the warps that read it
         }
         *abort_flag = 0;
         ptx::fence_barrier_init();
@@ -322,8 +339,13 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
         ptx::prefetch_tmap(&tm_v);
     }
     if (warp == 5) {
-        ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
-        ptx::tmem_relinquish();
+        if constexpr (PAIR) {
+            ptx::tmem_alloc_pair(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
+            ptx::tmem_relinquish_pair();
+        } else {
+            ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
+            ptx::tmem_relinquish();
+        }
     }
     // OVERLAP: warp 7 looks up the units blockIdx.x, + gridDim.x, ... ahead of the others (in a batch of odd lengths
     // that takes a search and a few dependent loads) and hands those with rows on through a ring. Else a CTA has
@@ -351,17 +373,22 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
     if (!OVERLAP || warp == 7)
         ahead = next_unit();  // while tensor memory is allocated
     ptx::tc_fence_before();
-    __syncthreads();
+    if constexpr (PAIR)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     // Bounded waits as in the forward kernels, but inline: a call in a branch with registers of its own
     // (setmaxnreg) does not assemble. The limit holds a tile: who waits for `tiles` of them waits that much longer
     // (and stops with the others when the tile's own wait has run out).
-    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site, int tiles = 1) -> bool {
-        bool done = ptx::mbar_try_wait(bar, parity);
+    auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site, int tiles = 1, bool peer = false) -> bool {
+        // peer: the other CTA arrives, too
+        auto try_wait = [&]() { return peer ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+        bool done = try_wait();
         if (!__all_sync(0xffffffffu, done)) {
             const uint64_t t0 = ptx::globaltimer_ns();
-            for (uint32_t it = 1; !__all_sync(0xffffffffu, done = ptx::mbar_try_wait(bar, parity)); ++it) {
+            for (uint32_t it = 1; !__all_sync(0xffffffffu, done = try_wait()); ++it) {
                 if ((it & 15u) != 0)
                     continue;
                 const bool late = static_cast<float>(ptx::globaltimer_ns() - t0) > static_cast<float>(p.timeout_ns) * tiles;
@@ -383,6 +410,23 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
         }
     };
 
+    // a warp's arrival on a barrier of the leader
+    auto arrive_leader = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) {
+            if (leader)
+                ptx::mbar_arrive(bar);
+            else
+                ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 0));
+        }
+    };
+    // on a barrier, of a pair in both CTAs, once this warp's products so far are done
+    auto commit = [&](uint32_t bar) {
+        if constexpr (PAIR)
+            ptx::mma_commit_pair_w(bar);
+        else
+            ptx::mma_commit_w(bar);
+    };
     Unit *const ring = reinterpret_cast<Unit *>(smem + WL::UNIT_OFF);
     auto take = [&](int i, Unit &un) -> bool {  // unit i; false at the end or when a wait ran out
         if constexpr (!OVERLAP) {
@@ -461,9 +505,7 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                         make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
         }
         ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0)
-            ptx::mbar_arrive(o_free);
+        arrive_leader(o_free);
         unsigned again = __ballot_sync(0xffffffffu, row_ok && !none && probe != 0.f);
         while (again != 0u) {
             const int src = __ffs(again) - 1;
@@ -491,6 +533,12 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                 int slot = 0, k = 0;
                 uint32_t ph = 0, armed_mask = 0, armed_par = 0, q_armed = 0, q_par = 0;
                 bool ok = true;
+                auto load_box = [&](uint32_t dst, const CUtensorMap *map, uint32_t full, int x, int y, int z) {
+                    if constexpr (PAIR)
+                        ptx::tma_load_3d_pair_w(dst, map, full, x, y, z);
+                    else
+                        ptx::tma_load_3d_w(dst, map, full, x, y, z);
+                };
                 Unit un;
                 for (int i = 0; ok && take(i, un); ++i) {
                     const int n = un.n;
@@ -499,24 +547,38 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                     const int b = k % QB;
                     if (k >= QB && !(ok = wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL)))
                         break;
-                    ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, L::Q_BYTES);
+                    const uint32_t q_full = PAIR ? ptx::map_to_rank(q_full0 + 8u * b, 0) : q_full0 + 8u * b;
+                    if (leader)
+                        ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, (PAIR ? 2 : 1) * L::Q_BYTES);
 #pragma unroll
                     for (int c = 0; c < D / L::BOX_COLS; ++c)
-                        ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, &tm_q, q_full0 + 8u * b, c * L::BOX_COLS,
-                                           un.q_row, un.z_q);
+                        load_box(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, &tm_q, q_full, c * L::BOX_COLS, un.q_row, un.z_q);
                     q_armed |= 1u << b;
                     q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
-                    auto load_tile = [&](const CUtensorMap *map, int j) -> bool {
+                    // a K or V tile; of a pair each CTA loads its 64 keys of K and its half of V's columns
+                    auto load_tile = [&](bool of_k, int j) -> bool {
+                        const CUtensorMap *map = of_k ? &tm_k : &tm_v;
 #pragma unroll
                         for (int ch = 0; ch < CPT; ++ch) {
-                            const uint32_t full = slot_full0 + 8u * slot;
                             if (!wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY))
                                 return false;
-                            ptx::mbar_arrive_expect_tx_w(full, L::CHUNK_BYTES);
-                            const uint32_t dst = s_ring + slot * L::CHUNK_BYTES;
-                            const int y = un.kv_row0 + un.tile(j) * L::BN;
-                            ptx::tma_load_3d_w(dst, map, full, ch * 128, y, un.z_kv);
-                            ptx::tma_load_3d_w(dst + L::BOX_BYTES, map, full, ch * 128 + L::BOX_COLS, y, un.z_kv);
+                            const uint32_t own = slot_full0 + 8u * slot, full = PAIR ? ptx::map_to_rank(own, 0) : own;
+                            if (leader)
+                                ptx::mbar_arrive_expect_tx_w(own, (PAIR ? 2 : 1) * WL::SLOT_BYTES);
+                            const uint32_t dst = s_ring + slot * WL::SLOT_BYTES;
+                            const int y = un.kv_row0 + un.tile(j) * L::BN, r = static_cast<int>(rank);
+                            if constexpr (!PAIR) {
+                                load_box(dst, map, full, ch * 128, y, un.z_kv);
+                                load_box(dst + L::BOX_BYTES, map, full, ch * 128 + L::BOX_COLS, y, un.z_kv);
+                            } else if (of_k) {
+#pragma unroll
+                                for (int c = 0; c < D / 64; ++c)
+                                    load_box(dst + c * PL::K_BOX_BYTES, map, full, c * 64, y + 64 * r, un.z_kv);
+                            } else {
+#pragma unroll
+                                for (int c = 0; c < D / 128; ++c)
+                                    load_box(dst + c * PL::V_BOX_BYTES, map, full, r * (D / 2) + c * 64, y, un.z_kv);
+                            }
                             armed_mask |= 1u << slot;
                             armed_par = (armed_par & ~(1u << slot)) | (ph << slot);
                             if (++slot == NS) {
@@ -526,24 +588,27 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                         }
                         return true;
                     };
-                    ok = load_tile(&tm_k, 0);
+                    ok = load_tile(true, 0);
                     for (int j = 0; ok && j < n; ++j) {
                         if (j + 1 < n)
-                            ok = load_tile(&tm_k, j + 1);
+                            ok = load_tile(true, j + 1);
                         if (ok)
-                            ok = load_tile(&tm_v, j);
+                            ok = load_tile(false, j);
                     }
                     ++k;
                 }
-                // Every copy this thread issued lands before the CTA may exit.
-                for (int b = 0; b < QB; ++b)
-                    if (q_armed & (1u << b))
-                        drain(q_full0 + 8u * b, (q_par >> b) & 1u);
-                for (int s = 0; s < NS; ++s)
-                    if (armed_mask & (1u << s))
-                        drain(slot_full0 + 8u * s, (armed_par >> s) & 1u);
+                // Every copy this thread issued lands before the CTA may exit (a pair's count on the leader's
+                // barriers: its products have waited for them, and after a wait that ran out both CTAs linger).
+                if constexpr (!PAIR) {
+                    for (int b = 0; b < QB; ++b)
+                        if (q_armed & (1u << b))
+                            drain(q_full0 + 8u * b, (q_par >> b) & 1u);
+                    for (int s = 0; s < NS; ++s)
+                        if (armed_mask & (1u << s))
+                            drain(slot_full0 + 8u * s, (armed_par >> s) & 1u);
+                }
             }
-        } else if (warp == 5) {
+        } else if (warp == 5 && leader) {
             // ------------------------------------------- S = Q K^T issuer
             const uint64_t dk = ptx::smem_desc_sw128(s_ring, 16, 1024);
             bool issued = false, ok = true;
@@ -578,7 +643,18 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
 #pragma unroll
                     for (int ch = 0; ch < CPT; ++ch) {
                         const int slot = (p0 + ch) % NS;
-                        const uint64_t kslot = dk + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                        const uint64_t kslot = dk + static_cast<uint64_t>((slot * WL::SLOT_BYTES) >> 4);
+                        if constexpr (PAIR) {
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t box = kk >> 2, off = (kk & 3) * 32;
+                                ptx::mma_ss_pair_w(d_tmem, dq + ((box * PL::Q_BOX_BYTES + off) >> 4),
+                                                   kslot + ((box * PL::K_BOX_BYTES + off) >> 4), IDESC_S2, kk != 0);
+                            }
+                            issued = true;
+                            ptx::mma_commit_pair_w(slot_empty0 + 8u * slot);
+                            continue;
+                        }
                         const uint64_t qch = dq + static_cast<uint64_t>((2 * ch * L::BOX_BYTES) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk) {
@@ -588,20 +664,20 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                         issued = true;
                         ptx::mma_commit_w(slot_empty0 + 8u * slot);
                     }
-                    ptx::mma_commit_w(s_full0 + 8u * (gt % NB));
+                    commit(s_full0 + 8u * (gt % NB));
                 }
                 if (!ok)
                     break;
-                ptx::mma_commit_w(q_free0 + 8u * b);  // query tile b may take unit k + QB's Q
+                commit(q_free0 + 8u * b);  // query tile b may take unit k + QB's Q
                 g0 += n;
                 pos0 += 2 * CPT * n;
                 ++k;
             }
             if (issued) {  // all of this thread's MMAs complete before TMEM is freed
-                ptx::mma_commit_w(final0);
+                commit(final0);
                 drain(final0, 0);
             }
-        } else if (warp == 6) {
+        } else if (warp == 6 && leader) {
             // ------------------------------------------ O += P V issuer
             const uint64_t dv = ptx::smem_desc_sw128(s_ring, L::BOX_BYTES, 1024);
             bool issued = false, ok = true;
@@ -619,10 +695,10 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                         if (!(ok = wait_all(slot_full0 + 8u * (p0 % NS), (p0 / NS) & 1, SITE_SLOT_FULL)))
                             break;
                     }
-                    if (!(ok = wait_all(p_full0 + 8u * buf, (gj / NB) & 1, SITE_P_FULL)))
+                    if (!(ok = wait_all(p_full0 + 8u * buf, (gj / NB) & 1, SITE_P_FULL, 1, PAIR)))
                         break;
                     // a unit's first PV overwrites O: the previous unit's epilogue must have read it
-                    if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
+                    if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE, 1, PAIR)))
                         break;
                     ptx::tc_fence_after();
                     const uint32_t a_tmem = tmem + L::TM_S + buf * L::BN;
@@ -635,27 +711,32 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                                 break;
                             ptx::tc_fence_after();
                         }
-                        const uint64_t vslot = dv + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                        const uint64_t vslot = dv + static_cast<uint64_t>((slot * WL::SLOT_BYTES) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
-                                          (j > 0) || (kk > 0));
+                        for (int kk = 0; kk < 8; ++kk) {
+                            if constexpr (PAIR)
+                                ptx::mma_ts_pair_w(tmem + L::TM_O, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV2,
+                                                   (j > 0) || (kk > 0));
+                            else
+                                ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4),
+                                              IDESC_PV, (j > 0) || (kk > 0));
+                        }
                         issued = true;
-                        ptx::mma_commit_w(slot_empty0 + 8u * slot);
+                        commit(slot_empty0 + 8u * slot);
                     }
                     if (!ok)
                         break;
-                    ptx::mma_commit_w(o_done0 + 8u * (gj % O_DONE_RING));
+                    commit(o_done0 + 8u * (gj % O_DONE_RING));
                 }
                 g0 += n;
                 pos0 += 2 * CPT * n;
                 ++k;
             }
             if (issued) {
-                ptx::mma_commit_w(final0 + 8u);
+                commit(final0 + 8u);
                 drain(final0 + 8u, 0);
             }
-        } else if constexpr (OVERLAP) {
+        } else if (OVERLAP && warp == 7) {
             // ------------------------------------------ the units, ahead of the others
             int longest = 1;  // of the units so far: its end may be what a place in the ring waits for
             for (int i = 0;; ++i) {
@@ -804,7 +885,10 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
                     ptx::tmem_wait_st();
                 }
                 ptx::tc_fence_before();
-                ptx::mbar_arrive(p_full0 + 8u * buf);
+                if constexpr (PAIR)
+                    arrive_leader(p_full0 + 8u * buf);
+                else
+                    ptx::mbar_arrive(p_full0 + 8u * buf);
                 m_used = m_new;
             }
             if (!ok)
@@ -854,10 +938,22 @@ __global__ void __launch_bounds__(window_threads(OVERLAP), 1)
 
     ptx::tc_fence_before();
     __syncthreads();
+    if constexpr (PAIR) {
+        // After a wait that ran out copies may be on their way to the pair; give them time before it exits.
+        if (*abort_flag) {
+            for (int i = 0; i < 100; ++i)
+                ptx::nanosleep_ns(1000);
+        }
+        // Neither CTA leaves while the other may still signal its barriers or read its shared or tensor memory.
+        ptx::cluster_sync();
+    }
     if (warp == 5) {
         __syncwarp();
         ptx::tc_fence_after();
-        ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+        if constexpr (PAIR)
+            ptx::tmem_dealloc_pair(tmem, L::TMEM_COLS);
+        else
+            ptx::tmem_dealloc(tmem, L::TMEM_COLS);
     }
 }
 
@@ -865,17 +961,43 @@ template <int D, bool BF16>
 cudaError_t launch_window(const LaunchMaps &m, const WindowParams &p, cudaStream_t stream)
 {
     const bool vl = p.k.cu_q != nullptr;
-    const int ctas = p.k.units < p.k.num_sms ? p.k.units : p.k.num_sms;
-    // With a unit a CTA at most there is no next one to go on with, and the hand-over costs its latency.
-    const bool overlap = p.k.units > p.k.num_sms;
-    static unsigned long long set[2][2] = {};
-    auto kern = vl ? (overlap ? window_kernel<D, BF16, true, true> : window_kernel<D, BF16, true, false>)
-                   : (overlap ? window_kernel<D, BF16, false, true> : window_kernel<D, BF16, false, false>);
-    cudaError_t e = set_smem_once(kern, WindowLayout<D>::SMEM_BYTES, set[vl][overlap]);
-    if (e != cudaSuccess)
-        return e;
-    kern<<<ctas, window_threads(overlap), WindowLayout<D>::SMEM_BYTES, stream>>>(m.q, m.k, m.v, p);
-    return cudaGetLastError();
+    const int sms = p.k.num_sms;
+    // With a unit a CTA at most there is no next one to go on with, and the hand-over costs its latency (8.3 -> 10.1 us).
+    // Pairs are two heads of a group; what they gain at D = 256 and cost at D = 128 is at the top of the file.
+    const bool pairs = D == 256 && p.k.G % 2 == 0 && sms > 1 && !(p.k.debug_flags & DEBUG_SINGLE_CTA);
+    const WindowForm form = p.k.units <= sms ? WINDOW_ONE : pairs ? WINDOW_PAIR : WINDOW_MANY;
+    static unsigned long long set[2][3] = {};
+    auto go = [&](auto kern, auto layout, const CUtensorMap &k) -> cudaError_t {
+        constexpr int BYTES = decltype(layout)::SMEM_BYTES;
+        cudaError_t e = set_smem_once(kern, BYTES, set[vl][form]);
+        if (e != cudaSuccess)
+            return e;
+        cudaLaunchAttribute cluster{};
+        cluster.id = cudaLaunchAttributeClusterDimension;
+        cluster.val.clusterDim.x = form == WINDOW_PAIR ? 2 : 1;
+        cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+        cudaLaunchConfig_t config{};
+        const int most = form == WINDOW_PAIR ? sms / 2 * 2 : sms;
+        config.gridDim = dim3(p.k.units < most ? p.k.units : most);
+        config.blockDim = dim3(window_threads(form != WINDOW_ONE));
+        config.dynamicSmemBytes = BYTES;
+        config.stream = stream;
+        config.attrs = &cluster;
+        config.numAttrs = form == WINDOW_PAIR ? 1 : 0;
+        return cudaLaunchKernelEx(&config, kern, m.q, k, m.v, p);
+    };
+    using Single = WindowLayout<D, false>;
+    if constexpr (D == 256) {
+        using Pair = WindowLayout<D, true>;
+        if (form == WINDOW_PAIR)
+            return vl ? go(window_kernel<D, BF16, true, WINDOW_PAIR>, Pair{}, m.k_half)
+                      : go(window_kernel<D, BF16, false, WINDOW_PAIR>, Pair{}, m.k_half);
+    }
+    if (form == WINDOW_ONE)
+        return vl ? go(window_kernel<D, BF16, true, WINDOW_ONE>, Single{}, m.k)
+                  : go(window_kernel<D, BF16, false, WINDOW_ONE>, Single{}, m.k);
+    return vl ? go(window_kernel<D, BF16, true, WINDOW_MANY>, Single{}, m.k)
+              : go(window_kernel<D, BF16, false, WINDOW_MANY>, Single{}, m.k);
 }
 
 }  // namespace sdp

@@ -358,7 +358,7 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
  * the kernel and reported by sdp_poll_status); fewer than 2^30 rows or keys. Keys and values
  * that a row does not see may hold infinities or NaN: they do not reach it. The work of a packed
  * batch is the tiles that exist. A launch runs the same kernel when it is captured; nothing is
- * allocated after the first call on a device. The wait limit and debug flags 1, 4 and 32 apply.
+ * allocated after the first call on a device. The wait limit and debug flags 1, 2, 4 and 32 apply.
  */
 int sdp_fwd_window(const void *q, const void *k, const void *v, void *o, float *lse, int B, int Hq, int Hkv, int Sq,
                    int Skv, int D, float scale, int dtype, int window, int sinks, void *stream);

@@ -317,18 +317,23 @@ def test_nan_and_infinity_stay_outside_the_window(D, dt):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("D,dt", [(128, "bf16"), (256, "fp16")])
+@pytest.mark.parametrize("Hq,Hkv,flags", [(8, 2, 0), (8, 2, 2), (9, 3, 0)], ids=["pairs", "single", "odd_group"])
 @pytest.mark.parametrize("Sq,Skv", [(150, 100), (300, 300), (129, 700), (300, 5)])
-def test_a_large_batch_has_the_bits_of_its_parts(Sq, Skv, D, dt):
-    """Several units a CTA, whose rows a warpgroup of its own writes, against one unit a CTA at most; rows
-    without a key, and values that are not finite in and out of sight."""
+def test_a_large_batch_has_the_bits_of_its_parts(Sq, Skv, D, dt, Hq, Hkv, flags):
+    """Several units a CTA, or a pair of CTAs, whose rows a warpgroup of its own writes, against one unit a CTA at
+    most; rows without a key, and values that are not finite in and out of sight."""
     g = torch.Generator(device="cuda").manual_seed(Sq + Skv)
     dtype, W, sinks = DTYPES[dt], 40, 3
-    B, Hq, Hkv = 20, 8, 2
+    B = 20
     q = torch.randn(B, Hq, Sq, D, device="cuda", generator=g).to(dtype)
     k, v = (torch.randn(B, Hkv, Skv, D, device="cuda", generator=g).to(dtype) for _ in range(2))
     v[1, 0, Skv // 2, 3], v[2, 1, 0, 7], k[3, 1, Skv - 1, 0] = math.inf, math.nan, math.nan
     q[4, 5, Sq // 2, 1] = math.nan
-    o, lse = sdp.fwd_window(q, k, v, W, sinks=sinks)
+    old = sdp.set_debug_flags(flags)
+    try:
+        o, lse = sdp.fwd_window(q, k, v, W, sinks=sinks)
+    finally:
+        sdp.set_debug_flags(old)
     for b in range(B):
         ob, lb = sdp.fwd_window(q[b:b + 1], k[b:b + 1], v[b:b + 1], W, sinks=sinks)
         assert torch.equal(ob[0].view(torch.int16), o[b].view(torch.int16)) or torch.equal(
@@ -383,8 +388,9 @@ def test_large_batches_in_graphs_on_two_streams(D):
 
 
 @pytest.mark.gpu
-def test_waits_that_run_out_end_a_large_batch():
-    q, k, v = (torch.randn(8, 32, 300, 128, device="cuda").half() for _ in range(3))
+@pytest.mark.parametrize("D,Hkv", [(128, 32), (256, 4), (256, 32)])
+def test_waits_that_run_out_end_a_large_batch(D, Hkv):
+    q, k, v = (torch.randn(8, h, 300, D, device="cuda").half() for h in (32, Hkv, Hkv))
     want, lwant = sdp.fwd_window(q, k, v, 70)
     old_ms, old = sdp.set_wait_timeout_ms(20), sdp.set_debug_flags(1)
     try:
