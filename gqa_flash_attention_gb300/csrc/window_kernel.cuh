@@ -384,7 +384,12 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
     // (and stops with the others when the tile's own wait has run out).
     auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site, int tiles = 1, bool peer = false) -> bool {
         // peer: the other CTA arrives, too
-        auto try_wait = [&]() { return peer ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity); };
+        auto try_wait = [&]() {
+            if constexpr (PAIR)
+                return peer ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity);
+            else
+                return ptx::mbar_try_wait(bar, parity);
+        };
         bool done = try_wait();
         if (!__all_sync(0xffffffffu, done)) {
             const uint64_t t0 = ptx::globaltimer_ns();
@@ -413,12 +418,14 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
     // a warp's arrival on a barrier of the leader
     auto arrive_leader = [&](uint32_t bar) {
         __syncwarp();
-        if (lane == 0) {
-            if (leader)
-                ptx::mbar_arrive(bar);
-            else
-                ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 0));
-        }
+        if (lane != 0)
+            return;
+        if constexpr (!PAIR)
+            ptx::mbar_arrive(bar);
+        else if (leader)
+            ptx::mbar_arrive(bar);
+        else
+            ptx::mbar_arrive_cluster(ptx::map_to_rank(bar, 0));
     };
     // on a barrier, of a pair in both CTAs, once this warp's products so far are done
     auto commit = [&](uint32_t bar) {
@@ -736,7 +743,7 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
                 commit(final0 + 8u);
                 drain(final0 + 8u, 0);
             }
-        } else if (OVERLAP && warp == 7) {
+        } else if (OVERLAP && (!PAIR || warp == 7)) {
             // ------------------------------------------ the units, ahead of the others
             int longest = 1;  // of the units so far: its end may be what a place in the ring waits for
             for (int i = 0;; ++i) {
