@@ -5,7 +5,7 @@
 //     O = softmax(scale * Q K^T) V over them, LSE = ln sum exp; a row that sees none: 0 and -inf.
 //
 // The G query heads of a KV head and the n rows are the columns of one problem per (sequence, KV
-// head): 8 * NT columns a CTA, so that the codes are unpacked once for all of them.
+// head): 8 * NT columns a warp, so that the codes are unpacked once for all of them.
 //
 // Bound: HBM, 4.5 bits a channel once per KV head. The tensor work is small, but the codes have to
 // pass through registers, so the kernel is built to keep the instructions per code few. Both
