@@ -34,7 +34,7 @@
 //   few columns fill the n side. p s turns from S's layout (token rows) to P's (column rows) by one
 //   movmatrix.
 //
-// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 57.7 us with the join): the
+// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 54.1 us with the join): the
 // latency between dependent instructions at four warps a scheduler, with half of the integer units' and
 // 58 % of the issue slots' rate in use; O, the ring and a tile's fragments leave registers for no more
 // warps. DRAM is at 40 % and the tensor pipe at 17 %. With 16 columns at D = 256 (two warps a scheduler) the
@@ -92,7 +92,9 @@ struct Cache4AttnParams {
 namespace c4 {
 
 constexpr int TILE = 32;     // tokens a warp step
-constexpr int OVERHEAD = 1;  // tiles that a problem's start and end cost as much as
+// Tiles that a problem's start and end cost as much as: with 1, 2, 3, 5 the 64 ragged sequences took 57.7, 54.1, 56.7,
+// 56.6 us, 4 x 32768 keys with 4 rows 80.5, 78.5, 78.1, 78.4, 256 x 600 keys 65.5, 65.6, 69.5, 69.8.
+constexpr int OVERHEAD = 2;
 constexpr int MERGE_THREADS = 256;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr float RESCALE = 8.f;               // weights stay below 2^8 of the reference
