@@ -34,11 +34,11 @@
 //   few columns fill the n side. p s turns from S's layout (token rows) to P's (column rows) by one
 //   movmatrix.
 //
-// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 54.1 us with the join): the
+// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 53.5 us with the join): the
 // latency between dependent instructions at four warps a scheduler, with half of the integer units' and
 // 58 % of the issue slots' rate in use; O, the ring and a tile's fragments leave registers for no more
 // warps. DRAM is at 40 % and the tensor pipe at 17 %. With 16 columns at D = 256 (two warps a scheduler) the
-// slots are 31 % busy: 56 us for 8 x 16384. (The products on tcgen05 with e4m3 codes, the unpacked codes
+// slots are 31 % busy: 54 us for 8 x 16384. (The products on tcgen05 with e4m3 codes, the unpacked codes
 // passing through tensor and shared memory between warps of different roles, took 89 and 76 us: a tile's
 // chain of hand-overs is longer than its share of the copy rate, and neither two CTAs an SM nor deeper
 // rings hid it.)
@@ -148,7 +148,7 @@ __host__ __device__ constexpr long long part_floats(int cols)
     return static_cast<long long>(cols) * (D + 4);
 }
 
-// Warps a CTA and ring slots a warp, by the registers and the shared memory that are left: O alone
+// Warps a CTA, by the registers that are left: O alone
 // takes D / 16 * NT * 4 registers a thread.
 template <int D, int NT>
 struct Plan {
@@ -159,7 +159,10 @@ struct Plan {
     static constexpr int CODE = TILE * D / 2;    // bytes of a tile's K (or V) codes
     static constexpr int SCALE = TILE * GQ * 4;  // and of its scales
     static constexpr int SLOT = CODE + SCALE;
-    static constexpr int NSLOT = D == 128 ? (NT == 1 ? 5 : 6) : (NT == 1 ? 3 : 4);
+    // More slots leave less L1 to what does not fit the registers: with all that fit (5, 6, 3 and 4) the 64 ragged
+    // sequences took 54.1 instead of 53.5 us, 4 x 32768 keys with 4 rows 78.5 instead of 76.2, 8 x 16384 at D = 256
+    // 55.6 instead of 53.9.
+    static constexpr int NSLOT = 3;
     static constexpr int KSTEPS = D / 16;
     // bf16 parts of a group's sum of q: three where s is multiplied by -128 times it
     static constexpr int BIAS_STEPS = GQ == 2 ? 1 : 2;
