@@ -92,8 +92,8 @@ def rope_inv_freq(dim: int, base: float = 10000.0, scaling: str | None = None, f
     "linear" (every frequency divided by factor), "ntk" (the base raised so that the lowest
     frequency is divided by factor and the highest kept) or "yarn" (frequencies that turn more than
     beta_fast times in original_length kept, those below beta_slow turns divided by factor, a
-    linear ramp over the channel index between; its attention factor 0.1 ln(factor) + 1 is the
-    table's mscale, see rope_table).
+    linear ramp over the channel index between, its ends rounded outwards to whole pairs; its
+    attention factor 0.1 ln(factor) + 1 is the table's mscale, see rope_table).
     """
     if dim < 0 or dim % 2:
         raise ValueError("dim must be even")
@@ -112,7 +112,8 @@ def rope_inv_freq(dim: int, base: float = 10000.0, scaling: str | None = None, f
         def index(turns):  # channel pair that turns that many times in original_length
             return dim * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-        low, high = max(0, math.floor(index(beta_fast))), min(dim // 2 - 1, math.ceil(index(beta_slow)))
+        # the upper end may lie past the last pair, which then is not divided in full
+        low, high = max(0, math.floor(index(beta_fast))), min(dim - 1, math.ceil(index(beta_slow)))
         ramp = ((i - low) / max(high - low, 1e-3)).clamp(0, 1)
         return f * (1 - ramp) + f / factor * ramp
     if scaling not in (None, "ntk"):
