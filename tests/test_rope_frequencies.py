@@ -3,6 +3,8 @@
 Tolerance: a dozen roundings in 64 bits, one of them in an exponent of at most 15: 1e-13 relative.
 """
 import math
+import os
+import re
 
 import pytest
 
@@ -50,3 +52,12 @@ def test_yarn_keeps_every_pair_of_a_length_in_which_all_turn_often():
     """Both ends lie past the last pair."""
     f = sdp.rope_inv_freq(64, 100.0, scaling="yarn", factor=8.0, original_length=1 << 24)
     assert (f == sdp.rope_inv_freq(64, 100.0)).all()
+
+
+def test_the_documented_yarn_table_carries_its_attention_factor():
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as readme:
+        lines = re.findall(r"^(?:f|table) = .*$", readme.read(), re.M)
+    scope = {"sdp": sdp, "math": math}
+    exec("\n".join(lines).replace('device="cuda"', 'device="cpu"'), scope)
+    assert "yarn" in lines[0] and scope["table"].turns.shape == (64,)
+    assert abs(scope["table"].mscale - (0.1 * math.log(4) + 1)) < 1e-12
