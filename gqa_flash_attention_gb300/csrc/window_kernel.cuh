@@ -36,8 +36,11 @@
 //  - A row may see nothing in a tile, or at all (more rows than keys): its maximum stays -inf, its
 //    weights 0, and at the end O = 0 and LSE = -inf.
 //  - Masked weights are exactly 0, but 0 times an infinity or a NaN in V is NaN: a row whose O is
-//    not finite is computed again at the end from the keys it sees alone (recompute_row), so what
-//    lies outside a window stays outside. Rows that are finite pay one multiply-add an element.
+//    not finite is computed again from the keys it sees alone (recompute_row), so what lies outside
+//    a window stays outside. Rows that are finite pay one multiply-add an element. A row computed
+//    again takes microseconds for every 32 keys, which over a long window is longer than any wait of
+//    the pipeline may last, so it is only marked in O while units run, and computed once the CTA's
+//    last unit is written, when no warp waits for another.
 #pragma once
 
 #include "sdp_fwd_pair.cuh"
@@ -88,6 +91,10 @@ struct WindowLayout {
 
 // Keys [0, n) of 32 as a bit mask.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+// The mark of a row to be computed again, in its first element: a NaN in both types, and no other row that has been
+// written holds one.
+constexpr uint16_t ROW_AGAIN = 0x7fff;
 
 // One row again, over the keys it sees alone: key ranges [0, a1) and [b0, b1) of the row's K/V plane.
 // Called by a whole warp (the rare path of rows whose O is not finite). 32 keys a step, one a lane, for
@@ -464,8 +471,9 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
             *lse_of(un, row) = -INFINITY;
     };
     // A unit's rows, 32 of them by each of four warps (w4): O, complete with tile `last`, times inv_l (negative: the
-    // row saw no key) to global memory, and O's tensor memory to the next unit's first PV.
-    auto write_rows = [&](const Unit &un, int w4, int last, float inv_l) -> bool {
+    // row saw no key) to global memory, and O's tensor memory to the next unit's first PV. `marked` is set where a
+    // row has to be computed again.
+    auto write_rows = [&](const Unit &un, int w4, int last, float inv_l, bool &marked) -> bool {
         const int row = w4 * 32 + lane;
         const uint32_t t_o = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + L::TM_O;
         uint16_t *const o_tile = o_tile_of(un);
@@ -513,23 +521,31 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
         }
         ptx::tc_fence_before();
         arrive_leader(o_free);
-        unsigned again = __ballot_sync(0xffffffffu, row_ok && !none && probe != 0.f);
-        while (again != 0u) {
-            const int src = __ffs(again) - 1;
-            again &= again - 1u;
-            const int r = w4 * 32 + src;
+        const bool again = row_ok && !none && probe != 0.f;
+        if (__any_sync(0xffffffffu, again)) {
+            __syncwarp();  // the row's stores, by other lanes, before its mark
+            if (again)
+                o_tile[row * wp.q_row] = ROW_AGAIN;
+            marked = true;
+        }
+        return true;
+    };
+    // The marked ones of the rows that this warp has written (the others hold no NaN), from the keys that they see.
+    auto write_again = [&](const Unit &un, int w4) {
+        const int row = w4 * 32 + lane;
+        const bool mine = un.q0 + row < un.sq && o_tile_of(un)[row * wp.q_row] == ROW_AGAIN;
+        for (unsigned left = __ballot_sync(0xffffffffu, mine); left != 0u; left &= left - 1u) {
+            const int r = w4 * 32 + __ffs(left) - 1;
             const int at = un.pos0 + (wp.pack_sq > 0 ? (un.q0 + r) % wp.pack_sq : un.q0 + r);
             const int b0 = max(0, at - wp.window + 1);
             const long long q_off = un.z_q * wp.q_plane + static_cast<long long>(un.q_row + r) * wp.q_row;
             const long long kv_off = un.z_kv * wp.kv_plane + static_cast<long long>(un.kv_row0) * wp.kv_row;
-            __syncwarp();  // the row's first stores before those that replace them
             recompute_row<D, BF16>(static_cast<const uint16_t *>(wp.q) + q_off,
                                    static_cast<const uint16_t *>(wp.kk) + kv_off,
                                    static_cast<const uint16_t *>(wp.v) + kv_off, wp.kv_row, min(wp.sinks, b0), b0,
                                    at + 1, p.c, static_cast<uint16_t *>(p.o) + q_off,
                                    lse_of(un, r));
         }
-        return true;
     };
     if (warp >= 4 && warp < 8) {
         if constexpr (OVERLAP)
@@ -911,8 +927,12 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
                     break;
                 row_factor[b * L::BM + row] = inv_l;
                 ptx::mbar_arrive(sum_full0 + 8u * b);
-            } else if (!(ok = write_rows(un, warp, g0 + n - 1, inv_l))) {
-                break;
+            } else {
+                bool marked = false;
+                if (!(ok = write_rows(un, warp, g0 + n - 1, inv_l, marked)))
+                    break;
+                if (marked)
+                    write_again(un, warp);
             }
             g0 += n;
             ++k;
@@ -920,7 +940,7 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
     } else {
         // --------------------------------------- rows' ends: O times its factor, to global memory
         const int w4 = warp & 3, row = w4 * 32 + lane;
-        bool ok = true;
+        bool ok = true, marked = false;
         int g0 = 0, k = 0;
         Unit un;
         for (int i = 0; ok && take(i, un); ++i) {
@@ -936,10 +956,15 @@ __global__ void __launch_bounds__(window_threads(FORM != WINDOW_ONE), 1)
             __syncwarp();
             if (lane == 0)
                 ptx::mbar_arrive(sum_free0 + 8u * b);
-            if (!(ok = write_rows(un, w4, g0 + n - 1, inv_l)))
+            if (!(ok = write_rows(un, w4, g0 + n - 1, inv_l, marked)))
                 break;
             g0 += n;
             ++k;
+        }
+        if (marked && !*abort_flag) {  // (the ring is done with: the units are looked up again)
+            for (un = next_unit(); un.n >= 0; un = next_unit())
+                if (un.n > 0)
+                    write_again(un, w4);
         }
     }
 
