@@ -696,7 +696,11 @@ __global__ void __launch_bounds__(c4::Plan<D, NT>::THREADS, 1) cache4_attn_kerne
     auto look_up = [&]() {
         if (ahead.done())
             return;
-        const int tok = ahead.sp.tile(ae) * TILE + half * piece_tokens;
+        int tok = ahead.sp.tile(ae) * TILE + half * piece_tokens;
+        // A half between the sinks and the first row's window may lie in a page that is no longer there. The tile's
+        // other half, which some row sees, is copied in its place, and masked.
+        if (p.window > 0 && tok >= p.sinks && tok + piece_tokens + p.n - 1 <= ahead.sp.len - p.window)
+            tok ^= piece_tokens;
         const int slot = tok / p.page_size;
         page_off = tok - slot * p.page_size;
         // a half behind the last page is copied from that page and masked

@@ -245,7 +245,8 @@ def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_t
     q: [nseq, Hq, D], or [nseq, rows, Hq, D] with up to 32 rows (drafted tokens): row i of sequence s
     is its token cache_lens[s] - rows + i and sees the keys up to itself, already in the cache; with
     window > 0 only the last `window` of them and the sequence's first `sinks`. Contiguous, fp16 or
-    bf16. cache_lens: int32 [nseq]; block_table: int32 [nseq, max_pages]. Returns (o like q, lse fp32
+    bf16. cache_lens: int32 [nseq]; block_table: int32 [nseq, max_pages], of which only entries of pages
+    that some row sees are read. Returns (o like q, lse fp32
     without the last dimension, or None); a row that sees no key gives 0 and -inf.
 
     workspace: a contiguous CUDA tensor of cache4_workspace_bytes, not used by another call that may

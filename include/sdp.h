@@ -324,6 +324,8 @@ int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_c
  * sequence s is at position p = cache_lens[s] - rows + i and sees keys j <= p; with
  * window > 0 only those with j > p - window or j < sinks (window 0: all, sinks unused).
  * A row that sees no key (an empty sequence, a position below 0) gets O = 0, LSE = -inf.
+ * Of the block table only entries of pages that hold a key some row sees are read: pages between the
+ * sinks and the first row's window may have been given up.
  *
  * q, o   device, dtype [nseq, rows, Hq, D] contiguous; lse fp32 [nseq, rows, Hq] or NULL.
  *        The rows' own keys must be in the cache (append first).
