@@ -10,7 +10,9 @@
 //
 //     (a, b) -> m * (a cos t - b sin t, a sin t + b cos t),   t = position * f_i.
 //
-// Everything is in fp32, rounded once when the row is stored.
+// Everything is in fp32, rounded once when the row is stored. Squares of bf16 values can leave fp32's
+// range, and the norm's factor, applied last, would then meet an infinity: such a row (found by one test
+// of its mean square) is brought near 1 by a power of two first, which the factor takes along.
 //
 // Angles: fp32 products lose the angle at far positions (position 1e6 leaves an error of 0.06
 // rad), so the table holds each frequency in turns per position as a 64-bit binary fraction,
@@ -44,6 +46,10 @@ using sdp::unpack8;
 constexpr int kWarps = 4;
 constexpr int kPassUnroll = 4;
 constexpr unsigned FULL = 0xffffffffu;
+// Rows whose mean square (with eps) lies between are normed as they are: their squares do not vanish, and times any
+// weight up to 2^100 they stay finite. The others, which only bf16 can hold (or zeros without an eps), are brought
+// near 1 by a power of two first.
+constexpr float MEAN_LOW = 0x1p-80f, MEAN_HIGH = 0x1p40f;
 
 struct RopeParams {
     const uint16_t *q, *k;
@@ -167,6 +173,51 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
         }
     };
 
+    auto mean_square = [&](const uint64_t (&x)[4]) {
+        uint64_t sq = mul2(x[0], x[0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            sq = sdp::ptx::f2_fma(x[j], x[j], sq);
+        float s0, s1;
+        sdp::ptx::f2_unpack(sq, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int off = LPR / 2; off > 0; off >>= 1)
+            ss += __shfl_xor_sync(FULL, ss, off);
+        return ss * (1.f / D);
+    };
+    // y = A x + B x' of the row x, whose words are w; `down`: a pair that x has been multiplied by, or an int
+    auto weigh = [&](const uint64_t (&x)[4], uint64_t (&y)[4], const uint32_t (&w)[4], auto down) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            y[j] = mul2(x[j], fa[j]);
+        if (half == 0)
+            return;
+        uint32_t o[4];
+        if constexpr (!INTERLEAVED) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                o[j] = __shfl_sync(FULL, w[j], partner);
+        }
+        if (!turns_here)  // outside the rotation B is no factor: 0 times an infinity is NaN
+            return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint64_t other;
+            if constexpr (INTERLEAVED) {
+                float lo, hi;
+                sdp::ptx::f2_unpack(x[j], lo, hi);
+                other = sdp::ptx::f2_pack(hi, lo);
+            } else {
+                const float2 f = sdp::unpack16<BF16>(o[j]);
+                other = sdp::ptx::f2_pack(f.x, f.y);
+                if constexpr (sizeof(down) == 8)
+                    other = mul2(other, down);
+            }
+            y[j] = sdp::ptx::f2_fma(other, fb[j], y[j]);
+        }
+    };
+
     for (int seg = q_first ? 0 : 1; seg < 2; ++seg) {
         const bool of_q = seg == 0;
         const int passes = of_q ? end_q - pass0 : pass1 - max(pass0, p.passes_q);
@@ -198,42 +249,35 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
                 for (int j = 0; j < 4; ++j) {
                     const float2 f = sdp::unpack16<BF16>(w[j]);
                     x[j] = sdp::ptx::f2_pack(f.x, f.y);
-                    y[j] = mul2(x[j], fa[j]);
                 }
-                if (half > 0) {
-                    uint32_t o[4];
-                    if constexpr (!INTERLEAVED) {
+                weigh(x, y, w, 0);
+                if (normed) {
+                    const float t = mean_square(x) + p.eps;
+                    float r = rsqrtf(t);
+                    if constexpr (BF16) {
+                        const bool odd = live > 0 && !(t > MEAN_LOW && t < MEAN_HIGH);
+                        if (__any_sync(FULL, odd)) {
+                            float mx = sqrtf(p.eps);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            o[j] = __shfl_sync(FULL, w[j], partner);
-                    }
-                    if (turns_here) {  // outside the rotation B is no factor: 0 times an infinity is NaN
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float2 f;
-                            if constexpr (INTERLEAVED) {
-                                float lo, hi;
-                                sdp::ptx::f2_unpack(x[j], lo, hi);
-                                f = make_float2(hi, lo);
-                            } else {
-                                f = sdp::unpack16<BF16>(o[j]);
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 f = sdp::unpack16<BF16>(w[j]);
+                                mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
                             }
-                            y[j] = sdp::ptx::f2_fma(sdp::ptx::f2_pack(f.x, f.y), fb[j], y[j]);
+#pragma unroll
+                            for (int off = LPR / 2; off > 0; off >>= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, off));
+                            // 2^-e for mx in [2^e, 2^(e + 1)), where both are normal numbers
+                            const int e = min(126, max(-126, static_cast<int>(__float_as_uint(mx) >> 23) - 127));
+                            const float down = odd ? __uint_as_float(static_cast<uint32_t>(127 - e) << 23) : 1.f;
+                            const uint64_t down2 = sdp::ptx::f2_pack(down, down);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[j] = mul2(x[j], down2);
+                            weigh(x, y, w, down2);
+                            const float scaled = rsqrtf(mean_square(x) + p.eps * down * down);
+                            r = odd ? scaled : r;  // a row's bits do not depend on its neighbours in the warp
                         }
                     }
-                }
-                if (normed) {
-                    uint64_t sq = mul2(x[0], x[0]);
-#pragma unroll
-                    for (int j = 1; j < 4; ++j)
-                        sq = sdp::ptx::f2_fma(x[j], x[j], sq);
-                    float s0, s1;
-                    sdp::ptx::f2_unpack(sq, s0, s1);
-                    float ss = s0 + s1;
-#pragma unroll
-                    for (int off = LPR / 2; off > 0; off >>= 1)
-                        ss += __shfl_xor_sync(FULL, ss, off);
-                    const float r = rsqrtf(ss * (1.f / D) + p.eps);
                     const uint64_t rr = sdp::ptx::f2_pack(r, r);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)

@@ -254,7 +254,8 @@ int sdp_fwd_noalloc_status(void *stream);
  * or, interleaved != 0, (y_2i, y_{2i+1}):
  *     (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),  t = position * f_i;
  * the other channels are left as the norm gives them. Sums, angles and products in
- * fp32 (the angle's fraction of a turn exactly, at any position), rounded once.
+ * fp32 (the angle's fraction of a turn exactly, at any position), rounded once; a row
+ * whose squares leave fp32's range is normed against a power of two near it.
  *
  * q, q_out  device, dtype, rows of D at strides (batch, token, head) in elements,
  *           multiples of 8; 16-byte aligned. q_out may be q with q's strides (in
