@@ -126,6 +126,10 @@ extern "C" int sdp_fwd_varlen_window(const void *q, const void *k, const void *v
         return SDP_OK;  // no query rows (empty tensors may have null pointers): nothing to compute
     if (cu_seqlens_q == nullptr || cu_seqlens_k == nullptr || max_seqlen_q == 0)
         return SDP_ERR_INVALID_ARG;
+    // A batch without a single key (empty tensors may have null pointers): its rows get O = 0 and LSE = -inf, and
+    // the maps of K and V, from which nothing is loaded, are made over q.
+    if (total_k == 0)
+        k = v = q;
     int rc = common_checks(q, k, v, o, lse, D, scale, window, sinks);
     if (rc != SDP_OK)
         return rc;
@@ -138,7 +142,7 @@ extern "C" int sdp_fwd_varlen_window(const void *q, const void *k, const void *v
     sdp::WindowParams p{};
     if ((rc = fill(p, q, k, v, o, lse, scale, window, sinks)) != SDP_OK)
         return rc;
-    const long long kv_rows = total_k > 0 ? total_k : 1;  // a batch without keys still gets valid maps
+    const long long kv_rows = total_k > 0 ? total_k : 1;
     sdp::LaunchMaps m;
     if ((rc = sdp::tensor_map_thd(&m.q, q, dtype, D, total_q, Hq, 128)) != SDP_OK ||
         (rc = sdp::tensor_map_thd(&m.k, k, dtype, D, kv_rows, Hkv, 128)) != SDP_OK ||
