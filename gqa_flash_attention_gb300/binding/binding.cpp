@@ -360,6 +360,8 @@ PyObject *cache4_append(PyObject *const *a)
     const int *cp = int32_ptr(cu, p.nseq + 1LL, dev, "cu_seqlens must be a contiguous int32 tensor [nseq + 1] on the inputs' device");
     const int *lp = int32_ptr(lens, p.nseq, dev, "cache_lens must be a contiguous int32 tensor [nseq] on the inputs' device");
     const Place at(dev, a[6]);
+    if (p.nseq == 0)
+        return answer(SDP_OK, {});
     const int rc = sdp_cache4_append(p.kc, p.ks, p.vc, p.vs, p.pages, p.page, p.table, p.stride, p.max_pages, k.data_ptr(),
                                      k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), cp, lp, p.nseq,
                                      size32(k.size(0), "tokens"), p.Hkv, p.D, dt, at.handle());
@@ -388,6 +390,8 @@ PyObject *cache4_gather(PyObject *const *a)
                       (*t)->stride(2) == 1,
                   "k_out and v_out must be [total, Hkv, D] of dtype on the cache's device, the last dimension contiguous");
     }
+    if (p.nseq == 0)
+        return answer(SDP_OK, {&ko, &vo});
     const int rc = sdp_cache4_gather(p.kc, p.ks, p.vc, p.vs, p.pages, p.page, p.table, p.stride, p.max_pages, ko->data_ptr(),
                                      ko->stride(0), ko->stride(1), vo->data_ptr(), vo->stride(0), vo->stride(1), cp, p.nseq,
                                      total, p.Hkv, p.D, bf16 ? SDP_BF16 : SDP_FP16, at.handle());

@@ -204,7 +204,8 @@ def cache4_append(cache: Cache4, k: torch.Tensor, v: torch.Tensor, cu_seqlens: t
     cu_seqlens[i + 1] - 1 become the last tokens of sequence i, whose length with them is
     cache_lens[i]; token t goes to place t % page_size of page block_table[i, t // page_size].
     cu_seqlens, cache_lens: int32 [nseq + 1] and [nseq] on the device. Pages that sequences share
-    must not be written. Bad offsets, lengths and pages are skipped and show in poll_status().
+    must not be written. Bad offsets, lengths and pages are skipped and show in poll_status(); a batch
+    of no sequences writes nothing.
     """
     rc, = _binding.cache4_append(cache, k, v, cu_seqlens, cache_lens, block_table, stream)
     if rc != SDP_OK:
