@@ -8,7 +8,7 @@ window and first tokens that stay visible.
 
 The work runs in libsdp.so (``include/sdp.h`` states layouts, ownership and errors); PyTorch supplies
 memory and streams, and there is no fallback. Arguments are checked, outputs made and the C calls
-issued by ``_serving.so`` (binding/binding.cpp), built beside the library: a decode step's kernels take
+issued by ``_serving.*.so`` (binding/binding.cpp), built beside the library: a decode step's kernels take
 a few microseconds, less than checking their arguments in Python does. These functions compute
 forward passes only: a tensor that requires grad is refused while grad mode is on.
 """
@@ -18,6 +18,8 @@ import ctypes
 import importlib.util
 import math
 import os
+import re
+import sysconfig
 from typing import NamedTuple
 
 import torch
@@ -59,7 +61,14 @@ def _lib() -> ctypes.CDLL:
     return _declared
 
 
-BINDING_PATH = os.path.join(os.path.dirname(LIB_PATH), "_serving.so")
+def _binding_path(torch_version: str) -> str:
+    """The binding built for this Python and that torch. Its name carries both, so that one built for others (before an
+    upgrade, or in another environment over the same files) is never loaded: their C++ layouts differ."""
+    tag = f"{sysconfig.get_config_var('SOABI')}-torch{torch_version}"
+    return os.path.join(os.path.dirname(LIB_PATH), "_serving." + re.sub(r"[^A-Za-z0-9_.+-]", "_", tag) + ".so")
+
+
+BINDING_PATH = _binding_path(torch.__version__)
 
 
 class _Binding:
