@@ -81,9 +81,9 @@ __device__ __forceinline__ long long locate(const RowsParams &p, int token0, int
     bool ok = first >= 0 && end <= p.tokens && first <= token;
     int pos = ok ? token - first : 0;
     if (ok && p.lens != nullptr) {
-        const int before = __ldg(p.lens + lo) - (end - first);  // tokens that were there already
-        ok = before >= 0;
-        pos = ok && pos <= INT32_MAX - before ? pos + before : INT32_MAX;
+        const int len = __ldg(p.lens + lo);
+        ok = len >= end - first;
+        pos += ok ? len - (end - first) : 0;  // below len
     }
     const int slot = ok ? pos / p.c.page_size : 0;
     if (!ok || slot >= p.c.max_pages) {
