@@ -57,6 +57,16 @@ double number(PyObject *o, const char *name)
     return x;
 }
 
+bool truth(PyObject *o, const char *name)
+{
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) {
+        PyErr_Clear();
+        throw Refused(std::string(name) + " must be true or false");
+    }
+    return x != 0;
+}
+
 // A whole number that fits the ABI's int.
 int whole(PyObject *o, const char *name)
 {
@@ -298,7 +308,7 @@ PyObject *qk_norm_rope(PyObject *const *a)
         q.data_ptr(), rq.sb, rq.ss, rq.sh, k ? k->data_ptr() : nullptr, rk.sb, rk.ss, rk.sh, qo->data_ptr(), oq.sb, oq.ss,
         oq.sh, ko ? ko->data_ptr() : nullptr, ok.sb, ok.ss, ok.sh, pos, sb, ss, wide, turns, size32(R, "the table"),
         static_cast<float>(mscale), wq ? wq->data_ptr() : nullptr, wk ? wk->data_ptr() : nullptr, wt && *wt == at::kFloat,
-        static_cast<float>(number(a[6], "eps")), PyObject_IsTrue(a[7]), size32(rq.B, "B"), size32(rq.S, "S"),
+        static_cast<float>(number(a[6], "eps")), truth(a[7], "interleaved"), size32(rq.B, "B"), size32(rq.S, "S"),
         size32(rq.H, "Hq"), size32(rk.H, "Hkv"), size32(D, "D"), dt, at.handle());
     return answer(rc, {&qo, &ko});
 }
@@ -373,7 +383,7 @@ PyObject *cache4_gather(PyObject *const *a)
     const at::Tensor &cu = tensor(a[1], "cu_seqlens"), &table = tensor(a[2], "block_table");
     const int total = whole(a[3], "total");
     check(total >= 0, "total must not be negative");
-    const bool bf16 = PyObject_IsTrue(a[4]);  // serving.py has looked the dtype over
+    const bool bf16 = truth(a[4], "dtype");  // serving.py has looked the dtype over
     OptTensor ko = opt_tensor(a[5], "k_out"), vo = opt_tensor(a[6], "v_out");
     const int dev = cuda_index(table);
     check(dev >= 0, "the cache and the block table must be on a CUDA device");
@@ -411,7 +421,7 @@ PyObject *fwd_cache4(PyObject *const *a)
     const int rows = q.dim() == 4 ? size32(q.size(1), "rows") : 1, Hq = size32(q.size(-2), "Hq");
     const Place at(dev, a[11]);
     const OptTensor out = output_like(opt_tensor(a[7], "out"), q, dev, at);
-    const OptTensor lse = lse_of(opt_tensor(a[8], "lse"), PyObject_IsTrue(a[9]), q.sizes().slice(0, q.dim() - 1), dev, at);
+    const OptTensor lse = lse_of(opt_tensor(a[8], "lse"), truth(a[9], "return_lse"), q.sizes().slice(0, q.dim() - 1), dev, at);
     if (p.nseq == 0 || rows == 0)
         return answer(SDP_OK, {&out, &lse});
     const double scale = a[4] == Py_None ? 1.0 / std::sqrt(static_cast<double>(p.D)) : number(a[4], "scale");
@@ -455,7 +465,7 @@ PyObject *fwd_window(PyObject *const *a)
     check(k.size(0) == q.size(0), "q, k and v must have the same batch");
     const Place at(dev, a[9]);
     const OptTensor out = output_like(opt_tensor(a[6], "out"), q, dev, at);
-    const OptTensor lse = lse_of(opt_tensor(a[7], "lse"), PyObject_IsTrue(a[8]), q.sizes().slice(0, 3), dev, at);
+    const OptTensor lse = lse_of(opt_tensor(a[7], "lse"), truth(a[8], "return_lse"), q.sizes().slice(0, 3), dev, at);
     const int rc = sdp_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out->data_ptr(), lse_ptr(lse),
                                   size32(q.size(0), "B"), size32(q.size(1), "Hq"), size32(k.size(1), "Hkv"),
                                   size32(q.size(2), "Sq"), size32(k.size(2), "Skv"), size32(q.size(3), "D"),
@@ -476,7 +486,7 @@ PyObject *fwd_varlen_window(PyObject *const *a)
     const Place at(dev, a[12]);
     const OptTensor out = output_like(opt_tensor(a[9], "out"), q, dev, at);
     const int64_t shape[2] = {q.size(1), q.size(0)};
-    const OptTensor lse = lse_of(opt_tensor(a[10], "lse"), PyObject_IsTrue(a[11]), shape, dev, at);
+    const OptTensor lse = lse_of(opt_tensor(a[10], "lse"), truth(a[11], "return_lse"), shape, dev, at);
     const int rc = sdp_fwd_varlen_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out->data_ptr(), lse_ptr(lse), qp, kp,
                                          size32(n - 1, "nseq"), size32(q.size(1), "Hq"), size32(k.size(1), "Hkv"),
                                          size32(q.size(0), "total_q"), size32(k.size(0), "total_k"),
