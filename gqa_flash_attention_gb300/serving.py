@@ -241,6 +241,8 @@ def cache4_gather(cache: Cache4, cu_seqlens: torch.Tensor, block_table: torch.Te
 
 def cache4_workspace_bytes(nseq: int, rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype) -> int:
     """Bytes of workspace that fwd_cache4 needs for these sizes on the current device."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be float16 or bfloat16")
     rc = _lib().sdp_fwd_cache4_workspace_bytes(nseq, rows, Hq, Hkv, D, _DTYPE_CODE[dtype])
     _check(min(rc, 0))
     return rc

@@ -24,3 +24,9 @@ def test_truth_values():
     assert (out == 3).all() and sdp.poll_status() == sdp.SDP_OK
     o, lse = sdp.fwd_window(x, x, x, 9, return_lse=0)  # what Python takes for true or false is
     assert lse is None
+
+
+def test_types_of_a_workspace():
+    for dtype in (torch.float32, None):
+        with pytest.raises(ValueError):
+            sdp.cache4_workspace_bytes(1, 1, 8, 2, 128, dtype)
