@@ -9,14 +9,16 @@
 // System/6000 processor", 1990): three operations an element where a division takes a dozen. The
 // extremes are found on the 16-bit pairs as loaded, minimum and negated maximum in one register.
 //
-// Both kernels are elementwise passes over HBM, bounded in practice by their instructions (at 62529 tokens
-// of 2 heads of 256 channels, cold: 46 us written, 36 us read back, where the bytes alone take 23 us each; a
-// writer's group costs a reduction, a division and a reciprocal before its elements begin). A warp takes a few
+// Both kernels are elementwise passes over HBM at about half of its rate: 62529 tokens of 2 heads of 256
+// channels take 43 us written and 32 us read back where the bytes alone take 24 us each (apart, in runs of
+// calls; 42.6 and 29.4 us under ncu). The writer issues 2.7 instructions a cycle of 4, its integer units half
+// busy: a group costs a reduction, a division and a reciprocal before its elements begin. The reader waits for
+// its loads (5.5 of some 10 stalled warps an issue), with the 32 warps an SM that plan() gives it. A warp takes a few
 // consecutive tokens and runs over their 2 Hkv rows each (K heads, then V heads), D/16 lanes a row. A lane
 // holds two chunks of eight channels of one group, each one 16-byte access on the 16-bit side and one 4-byte
 // word of codes on the other, so that four lanes share what a group costs. (With one chunk a lane, eight
-// lanes a group, the two took 65 and 46 us; with four, 75 and 40: half the warps with twice the registers
-// leave the loads' latency open.) Each lane looks up the place of one of the warp's tokens (a chain of
+// lanes a group, the two took 65 and 46 us, cold, with four 75 and 40, and with two 46 and 36: half the warps
+// with twice the registers leave the loads' latency open.) Each lane looks up the place of one of the warp's tokens (a chain of
 // dependent loads, which one token a warp left exposed).
 #include <cuda_runtime.h>
 

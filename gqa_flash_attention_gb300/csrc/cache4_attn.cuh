@@ -34,11 +34,14 @@
 //   few columns fill the n side. p s turns from S's layout (token rows) to P's (column rows) by one
 //   movmatrix.
 //
-// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 53.5 us with the join): the
+// What bounds it now (64 ragged sequences, window 4096, D = 128, 4 columns: 53.3 us with the join): the
 // latency between dependent instructions at four warps a scheduler, with half of the integer units' and
-// 58 % of the issue slots' rate in use; O, the ring and a tile's fragments leave registers for no more
-// warps. DRAM is at 40 % and the tensor pipe at 17 %. With 16 columns at D = 256 (two warps a scheduler) the
-// slots are 31 % busy: 54 us for 8 x 16384. (The products on tcgen05 with e4m3 codes, the unpacked codes
+// 60 % of the issue slots' rate in use; O, the ring and a tile's fragments leave registers for no more
+// warps. DRAM is at 42 % and the tensor pipe at 17 %. With 16 columns at D = 256 (two warps a scheduler) the
+// slots are 32 % busy: 55.5 us for 8 x 16384 keys, of which the attention alone takes 51 us and the join of
+// 76 parts a problem 15 us where nothing runs beside it. More than 16 columns (heads of a group times rows)
+// are several problems, each of which reads and unpacks the sequence again: there, in bf16, 16 columns take 51 us,
+// 32 take 76 and 64 take 127. (The products on tcgen05 with e4m3 codes, the unpacked codes
 // passing through tensor and shared memory between warps of different roles, took 89 and 76 us: a tile's
 // chain of hand-overs is longer than its share of the copy rate, and neither two CTAs an SM nor deeper
 // rings hid it.)
@@ -164,7 +167,7 @@ struct Plan {
     // 55.6 instead of 53.9.
     static constexpr int NSLOT = 3;
     static constexpr int KSTEPS = D / 16;
-    // bf16 parts of a group's sum of q: three where s is multiplied by -128 times it
+    // steps that hold the three bf16 parts (24 bits) of each group's sum of q, eight (s, b) pairs a step
     static constexpr int BIAS_STEPS = GQ == 2 ? 1 : 2;
     static constexpr int QF = (KSTEPS + BIAS_STEPS) * NT * 32 * 8;  // B fragments of a warp
     static constexpr int Q_FRAG = WARPS * NSLOT * SLOT;

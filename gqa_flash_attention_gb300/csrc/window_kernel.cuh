@@ -5,7 +5,9 @@
 //
 // Arithmetic and roles are those of the single-CTA kernel (sdp_fwd_kernel.cuh): 128-row query
 // tiles, 128-key tiles through a TMA ring, S = Q K^T and O += P V on tcgen05 with both
-// accumulators in tensor memory, one thread a row for the softmax with a lazily moved maximum.
+// accumulators in tensor memory, one thread a row for the softmax with a lazily moved maximum. As
+// there, scores, weights and sums are fp32 and the weights are rounded to the 16-bit type for P V, whose
+// operands have one type: half a step of each weight (2^-9 of it in bf16), of the order of the output's own rounding.
 // What the window changes:
 //
 //  - A unit (query tile, head) reads only the tiles of the sinks and those from its first row's
@@ -20,14 +22,17 @@
 //    passed at each unit's end at D = 256 (1.1 us a tile), and 12 packed prompts (W = 1024, D = 256)
 //    took 903 us instead of 789, 16384 rows (W = 4096, D = 128) 697 instead of 634. A launch of one unit
 //    a CTA at most has no next unit to go on with, and the hand-overs cost it 1.8 us of 8.3: it
-//    runs without them (WINDOW_ONE). O leaves tensor memory 32 columns at a time, stored as it comes: taken
+//    runs without them (WINDOW_ONE). (The figures of these comments are of 20 calls in a row; in runs of hundreds
+//    the clocks settle lower, at 800 instead of 724 us for the prompts and 690 instead of 634 for the 16384 rows.) O leaves tensor memory 32 columns at a time, stored as it comes: taken
 //    out whole first, which frees it earlier, the first was slower (812 us), its unrolled code larger.
-//  - What bounds a tile on one SM is shared memory: the products read Q, K and V there and the copies write
-//    K and V, 160 KB a tile at D = 128 and 320 KB at D = 256, where an SM moves 128 bytes a cycle (1280 and
-//    2560 cycles; 1210 to 1390 and 2570 measured; the products alone take 1024 and 2048). So at D = 256 two CTAs
+//  - What bounds a tile at D = 256 is shared memory: the products read Q, K and V there and the copies write
+//    K and V, 320 KB a tile, where an SM moves 128 bytes a cycle (2560 cycles; 2570 measured; the products alone
+//    take 2048). At D = 128 a tile takes 1210 to 1390 cycles, with 160 KB (1280 cycles), products of 1024 and a
+//    softmax chain of about as long: which of them is the bound has not been told apart, since what shortens
+//    one adds hand-overs (below). So at D = 256 two CTAs
 //    run as a pair (WINDOW_PAIR): two heads of a group have the same window, each CTA holds half of
 //    each K and V tile, and one product of 256 rows reads both halves: 12 packed prompts 786 -> 724 us. At
-//    D = 128 the softmax warps' chain is nearly as long as the copies, and the pair's hand-overs between
+//    D = 128 the pair's hand-overs between
 //    CTAs cost more than the copies saved (634 -> 704 us), so it keeps to one CTA. (Half of a tile's keys
 //    a thread, in two softmax warpgroups, took 699 us; handing P over in four parts, which a pair of the
 //    dense kernel gains from, 750 us for the prompts.)

@@ -259,7 +259,8 @@ def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_t
     window > 0 only the last `window` of them and the sequence's first `sinks`. Contiguous, fp16 or
     bf16. cache_lens: int32 [nseq]; block_table: int32 [nseq, max_pages], of which only entries of pages
     that some row sees are read. Returns (o like q, lse fp32
-    without the last dimension, or None); a row that sees no key gives 0 and -inf.
+    without the last dimension, or None); a row that sees no key gives 0 and -inf. The cache is read once
+    for each 16 of a KV head's (Hq / Hkv) * rows columns.
 
     workspace: a contiguous CUDA tensor of cache4_workspace_bytes, not used by another call that may
     overlap; when None it comes from torch's allocator. Enqueued on `stream` (default: the current

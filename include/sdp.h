@@ -337,9 +337,10 @@ int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_c
  *        before and are unspecified after.
  * Scores, weights and sums in fp32; the products take the 4-bit codes as they are and the
  * queries and weights in fp16 against powers of two that fit each row of q and the scales seen
- * (one fp16 a weight for bf16 outputs, two for fp16). The same call gives the same bits. A bad length leaves that sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a
- * page outside the pool leaves them unspecified (SDP_ERR_BAD_PAGES), a wait that runs out
- * all rows (SDP_ERR_DEVICE_TIMEOUT). Two kernels are enqueued on `stream`. The workspace
+ * (one fp16 a weight for bf16 outputs, two for fp16). The same call gives the same bits. The cache is
+ * read once for each 16 of a KV head's (Hq / Hkv) * rows columns. A bad length leaves that sequence's rows
+ * unwritten (SDP_ERR_BAD_SEQLENS); a page outside the pool leaves them unspecified (SDP_ERR_BAD_PAGES), a wait that
+ * runs out all rows (SDP_ERR_DEVICE_TIMEOUT). Two kernels are enqueued on `stream`. The workspace
  * size depends on the current device; a negative value is a status code.
  */
 long long sdp_fwd_cache4_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype);
@@ -355,7 +356,9 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
  * cached prefix has its place; sdp_fwd_causal aligns at the top instead) and sees the keys
  * j <= p with j > p - window or j < sinks. A row that sees none (p < 0) gets O = 0 and
  * LSE = -inf. window >= 1 and sinks >= 0; a window of skv or more is plain causal attention.
- * Tiles of 128 keys outside a query tile's window are not read.
+ * Tiles of 128 keys outside a query tile's window are not read. Scores, weights and sums are fp32; the weights
+ * are rounded to dtype for the product with V, as in sdp_fwd. The keys are not split: B * Hkv CTAs (batch and KV
+ * heads) walk the window where Sq is small.
  *
  * Layouts, ownership, errors and streams as sdp_fwd and sdp_fwd_varlen (offsets are checked by
  * the kernel and reported by sdp_poll_status); fewer than 2^30 rows or keys. k and v are not used (and may be
