@@ -43,9 +43,10 @@
 //  - Masked weights are exactly 0, but 0 times an infinity or a NaN in V is NaN: a row whose O is
 //    not finite is computed again from the keys it sees alone (recompute_row), so what lies outside
 //    a window stays outside. Rows that are finite pay one multiply-add an element. A row computed
-//    again takes microseconds for every 32 keys, which over a long window is longer than any wait of
-//    the pipeline may last, so it is only marked in O while units run, and computed once the CTA's
-//    last unit is written, when no warp waits for another.
+//    again takes 10 (D = 128) to 13 us (D = 256) for every 32 keys, which over a long window is longer
+//    than any wait of the pipeline may last, so it is only marked in O while units run, and computed once
+//    the CTA's last unit is written, when no warp waits for another. (9000 rows of 8 heads that all see an
+//    infinity in 4000 keys: 112 ms, of finite values 0.11.)
 #pragma once
 
 #include "sdp_fwd_pair.cuh"

@@ -363,7 +363,8 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
  * Layouts, ownership, errors and streams as sdp_fwd and sdp_fwd_varlen (offsets are checked by
  * the kernel and reported by sdp_poll_status); fewer than 2^30 rows or keys. k and v are not used (and may be
  * NULL) where total_k is 0. Keys and values
- * that a row does not see may hold infinities or NaN: they do not reach it. The work of a packed
+ * that a row does not see may hold infinities or NaN: they do not reach it. (A row in one of whose 128-key tiles
+ * there is one is computed apart, in some 10 us for every 32 keys that it sees.) The work of a packed
  * batch is the tiles that exist. A launch runs the same kernel when it is captured; nothing is
  * allocated after the first call on a device. The wait limit and debug flags 1, 2, 4 and 32 apply.
  */
