@@ -337,7 +337,8 @@ int sdp_cache4_gather(const void *k_codes, const void *k_scales, const void *v_c
  *        before and are unspecified after.
  * Scores, weights and sums in fp32; the products take the 4-bit codes as they are and the
  * queries and weights in fp16 against powers of two that fit each row of q and the scales seen
- * (one fp16 a weight for bf16 outputs, two for fp16). The same call gives the same bits. The cache is
+ * (one fp16 a weight for bf16 outputs, two for fp16). The same call gives the same bits. |q| * |scale| is
+ * to stay below 2^117 (no fp16 value reaches it), past which a row may hold NaN. The cache is
  * read once for each 16 of a KV head's (Hq / Hkv) * rows columns. A bad length leaves that sequence's rows
  * unwritten (SDP_ERR_BAD_SEQLENS); a page outside the pool leaves them unspecified (SDP_ERR_BAD_PAGES), a wait that
  * runs out all rows (SDP_ERR_DEVICE_TIMEOUT). Two kernels are enqueued on `stream`. The workspace
