@@ -233,6 +233,43 @@ Rows rows_of(const at::Tensor &t)
     return Rows{t.stride(0), t.stride(2), t.stride(1), t.size(0), t.size(2), t.size(1)};
 }
 
+// What rope_table made; nothing of None.
+struct Turns {
+    int64_t R = 0;
+    const unsigned long long *turns = nullptr;
+    double mscale = 1.0;
+};
+
+Turns turns_of(PyObject *o, int dev)
+{
+    Turns r;
+    if (o == Py_None)
+        return r;
+    check(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 2, "table must be rope_table's");
+    const at::Tensor &t = tensor(PyTuple_GET_ITEM(o, 0), "table.turns");
+    r.mscale = number(PyTuple_GET_ITEM(o, 1), "table.mscale");
+    check(cuda_index(t) == dev && t.scalar_type() == at::kLong && t.is_contiguous(), "table must be rope_table's, on q's device");
+    r.R = 2 * t.numel();
+    r.turns = reinterpret_cast<const unsigned long long *>(t.data_ptr<int64_t>());
+    return r;
+}
+
+// Whether the norms' weights, of rows like x's, are fp32.
+bool weights_fp32(const OptTensor &wq, const OptTensor &wk, const at::Tensor &x, int64_t D, int dev)
+{
+    std::optional<at::ScalarType> wt;
+    for (const OptTensor *w : {&wq, &wk}) {
+        if (!*w)
+            continue;
+        check((*w)->dim() == 1 && (*w)->size(0) == D && (*w)->is_contiguous() && cuda_index(**w) == dev &&
+                  ((*w)->scalar_type() == x.scalar_type() || (*w)->scalar_type() == at::kFloat),
+              "weights must be contiguous [D] tensors of q's dtype or float32 on its device");
+        check(!wt || *wt == (*w)->scalar_type(), "both weights must have one dtype");
+        wt = (*w)->scalar_type();
+    }
+    return wt && *wt == at::kFloat;
+}
+
 PyObject *qk_norm_rope(PyObject *const *a)
 {
     const at::Tensor &q = tensor(a[0], "q");
@@ -268,18 +305,11 @@ PyObject *qk_norm_rope(PyObject *const *a)
     } else {
         check(!ko && !wk, "k_out and k_weight need k");
     }
-    int64_t R = 0, sb = 0, ss = 0;
-    const unsigned long long *turns = nullptr;
+    const Turns table = turns_of(a[3], dev);
+    int64_t sb = 0, ss = 0;
     const void *pos = nullptr;
-    double mscale = 1.0;
     bool wide = false;
     if (a[3] != Py_None) {
-        check(PyTuple_Check(a[3]) && PyTuple_GET_SIZE(a[3]) == 2, "table must be rope_table's");
-        const at::Tensor &t = tensor(PyTuple_GET_ITEM(a[3], 0), "table.turns");
-        mscale = number(PyTuple_GET_ITEM(a[3], 1), "table.mscale");
-        check(cuda_index(t) == dev && t.scalar_type() == at::kLong && t.is_contiguous(), "table must be rope_table's, on q's device");
-        R = 2 * t.numel();
-        turns = reinterpret_cast<const unsigned long long *>(t.data_ptr<int64_t>());
         check(positions && cuda_index(*positions) == dev &&
                   (positions->scalar_type() == at::kInt || positions->scalar_type() == at::kLong),
               "positions must be an int32 or int64 tensor on q's device");
@@ -294,20 +324,11 @@ PyObject *qk_norm_rope(PyObject *const *a)
         wide = positions->scalar_type() == at::kLong;
         pos = positions->data_ptr();
     }
-    std::optional<at::ScalarType> wt;
-    for (const OptTensor *w : {&wq, &wk}) {
-        if (!*w)
-            continue;
-        check((*w)->dim() == 1 && (*w)->size(0) == D && (*w)->is_contiguous() && cuda_index(**w) == dev &&
-                  ((*w)->scalar_type() == q.scalar_type() || (*w)->scalar_type() == at::kFloat),
-              "weights must be contiguous [D] tensors of q's dtype or float32 on its device");
-        check(!wt || *wt == (*w)->scalar_type(), "both weights must have one dtype");
-        wt = (*w)->scalar_type();
-    }
+    const bool w32 = weights_fp32(wq, wk, q, D, dev);
     const int rc = sdp_qk_norm_rope(
         q.data_ptr(), rq.sb, rq.ss, rq.sh, k ? k->data_ptr() : nullptr, rk.sb, rk.ss, rk.sh, qo->data_ptr(), oq.sb, oq.ss,
-        oq.sh, ko ? ko->data_ptr() : nullptr, ok.sb, ok.ss, ok.sh, pos, sb, ss, wide, turns, size32(R, "the table"),
-        static_cast<float>(mscale), wq ? wq->data_ptr() : nullptr, wk ? wk->data_ptr() : nullptr, wt && *wt == at::kFloat,
+        oq.sh, ko ? ko->data_ptr() : nullptr, ok.sb, ok.ss, ok.sh, pos, sb, ss, wide, table.turns, size32(table.R, "the table"),
+        static_cast<float>(table.mscale), wq ? wq->data_ptr() : nullptr, wk ? wk->data_ptr() : nullptr, w32,
         static_cast<float>(number(a[6], "eps")), truth(a[7], "interleaved"), size32(rq.B, "B"), size32(rq.S, "S"),
         size32(rq.H, "Hq"), size32(rk.H, "Hkv"), size32(D, "D"), dt, at.handle());
     return answer(rc, {&qo, &ko});
@@ -440,6 +461,145 @@ PyObject *fwd_cache4(PyObject *const *a)
     return answer(rc, {&out, &lse});
 }
 
+// ------------------------------------------------------------------ the 16-bit paged cache
+
+struct Pool16 {
+    const at::Tensor &k, &v;
+    int pages, page, Hkv, D;
+};
+
+Pool16 pool16_of(PyObject *cache, at::ScalarType type, int dev)
+{
+    check(PyTuple_Check(cache) && PyTuple_GET_SIZE(cache) == 2, "cache must be a Cache16");
+    const at::Tensor &k = tensor(PyTuple_GET_ITEM(cache, 0), "cache.k"), &v = tensor(PyTuple_GET_ITEM(cache, 1), "cache.v");
+    check(k.dim() == 4 && v.sizes() == k.sizes() && k.scalar_type() == type && v.scalar_type() == type,
+          "the cache must be [num_pages, Hkv, page_size, D] tensors of the inputs' dtype");
+    check(k.is_contiguous() && v.is_contiguous() && cuda_index(k) == dev && cuda_index(v) == dev,
+          "the cache must be contiguous on the inputs' device");
+    return Pool16{k, v, size32(k.size(0), "num_pages"), size32(k.size(2), "page_size"), size32(k.size(1), "Hkv"),
+                  size32(k.size(3), "D")};
+}
+
+void check_table(const at::Tensor &table, int dev)
+{
+    check(table.dim() == 2 && table.scalar_type() == at::kInt && (table.size(1) <= 1 || table.stride(1) == 1) &&
+              cuda_index(table) == dev,
+          "block tables must be int32 [rows, max_pages] on the inputs' device, the last dimension contiguous");
+}
+
+PyObject *cache16_append(PyObject *const *a)
+{
+    const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const at::Tensor &cu = tensor(a[3], "cu_seqlens"), &lens = tensor(a[4], "cache_lens"), &table = tensor(a[5], "block_table");
+    const OptTensor q = opt_tensor(a[7], "q"), positions = opt_tensor(a[8], "positions");
+    const OptTensor wq = opt_tensor(a[9], "q_weight"), wk = opt_tensor(a[10], "k_weight");
+    OptTensor qo = opt_tensor(a[13], "q_out");
+    const int dev = cuda_index(k), dt = type_code(k);
+    check(dev >= 0 && dt >= 0 && v.scalar_type() == k.scalar_type() && cuda_index(v) == dev,
+          "k and v must be CUDA tensors on one device of one dtype, float16 or bfloat16");
+    forward_only({&k, &v, q ? &*q : nullptr, wq ? &*wq : nullptr, wk ? &*wk : nullptr});
+    const Pool16 p = pool16_of(a[0], k.scalar_type(), dev);
+    check(k.dim() == 3 && v.sizes() == k.sizes() && k.size(1) == p.Hkv && k.size(2) == p.D,
+          "k and v must be [tokens, Hkv, D] of the cache's heads and head dim");
+    check(k.stride(2) == 1 && v.stride(2) == 1, "the last dimension of k and v must be contiguous");
+    check_table(table, dev);
+    const int64_t nseq = table.size(0), tokens = k.size(0);
+    const int *cp = int32_ptr(cu, nseq + 1, dev, "cu_seqlens must be a contiguous int32 tensor [nseq + 1] on the inputs' device");
+    const int *lp = int32_ptr(lens, nseq, dev, "cache_lens must be a contiguous int32 tensor [nseq] on the inputs' device");
+    const Place at(dev, a[14]);
+    if (q) {
+        check(q->dim() == 3 && q->scalar_type() == k.scalar_type() && cuda_index(*q) == dev && q->size(0) == tokens &&
+                  q->size(2) == p.D && q->stride(2) == 1,
+              "q must be [tokens, Hq, D] of k's dtype and device, its last dimension contiguous");
+        if (!qo)
+            qo = at.empty(q->sizes(), q->scalar_type());
+        else
+            check(qo->sizes() == q->sizes() && qo->scalar_type() == q->scalar_type() && cuda_index(*qo) == dev &&
+                      qo->stride(2) == 1,
+                  "q_out must be shaped and typed like q, its last dimension contiguous");
+    } else {
+        check(!qo && !wq, "q_out and q_weight need q");
+    }
+    const Turns rope = turns_of(a[6], dev);
+    const void *pos = nullptr;
+    int64_t ps = 0;
+    bool wide = false;
+    if (positions) {
+        check(a[6] != Py_None, "positions need a rotation");
+        check(cuda_index(*positions) == dev && positions->dim() == 1 && positions->size(0) == tokens &&
+                  (positions->scalar_type() == at::kInt || positions->scalar_type() == at::kLong),
+              "positions must be an int32 or int64 tensor [tokens] on the inputs' device");
+        ps = positions->stride(0);
+        wide = positions->scalar_type() == at::kLong;
+        pos = positions->data_ptr();
+    }
+    const bool w32 = weights_fp32(wq, wk, k, p.D, dev);
+    if (nseq == 0)
+        return answer(SDP_OK, {&qo});
+    const int rc = sdp_cache16_append(
+        p.k.data_ptr(), p.v.data_ptr(), p.pages, p.page, table.data_ptr<int>(), table.stride(0),
+        size32(table.size(1), "max_pages"), q ? q->data_ptr() : nullptr, q ? q->stride(0) : 0, q ? q->stride(1) : 0,
+        qo ? qo->data_ptr() : nullptr, qo ? qo->stride(0) : 0, qo ? qo->stride(1) : 0, k.data_ptr(), k.stride(0), k.stride(1),
+        v.data_ptr(), v.stride(0), v.stride(1), cp, lp, size32(nseq, "nseq"), size32(tokens, "tokens"), pos, ps, wide,
+        rope.turns, size32(rope.R, "the table"), static_cast<float>(rope.mscale), wq ? wq->data_ptr() : nullptr,
+        wk ? wk->data_ptr() : nullptr, w32, static_cast<float>(number(a[11], "eps")), truth(a[12], "interleaved"),
+        q ? size32(q->size(1), "Hq") : 0, p.Hkv, p.D, dt, at.handle());
+    return answer(rc, {&qo});
+}
+
+PyObject *fwd_cache16(PyObject *const *a)
+{
+    const at::Tensor &q = tensor(a[0], "q"), &lens = tensor(a[2], "cache_lens"), &table = tensor(a[3], "block_table");
+    const OptTensor prefix = opt_tensor(a[4], "prefix_table"), prefix_lens = opt_tensor(a[5], "prefix_lens");
+    const OptTensor groups = opt_tensor(a[6], "cu_groups");
+    check(q.dim() == 3 || q.dim() == 4, "q must be [nseq, Hq, D] or [nseq, rows, Hq, D]");
+    const int dev = cuda_index(q), dt = type_code(q);
+    check(dev >= 0 && dt >= 0 && q.is_contiguous(), "q must be a contiguous float16 or bfloat16 CUDA tensor");
+    forward_only({&q});
+    const Pool16 p = pool16_of(a[1], q.scalar_type(), dev);
+    check_table(table, dev);
+    const int64_t nseq = q.size(0);
+    check(table.size(0) == nseq && p.D == q.size(-1), "q, the block table and the cache must agree in sequences and head dim");
+    const int *lp = int32_ptr(lens, nseq, dev, "cache_lens must be a contiguous int32 tensor [nseq] on q's device");
+    int64_t ngroups = 0;
+    const int *pl = nullptr, *gp = nullptr;
+    if (prefix) {
+        check_table(*prefix, dev);
+        ngroups = prefix->size(0);
+        check(prefix_lens.has_value(), "prefix_table needs prefix_lens");
+        pl = int32_ptr(*prefix_lens, ngroups, dev, "prefix_lens must be a contiguous int32 tensor [groups] on q's device");
+        check(groups || ngroups <= 1, "several groups need cu_groups");
+        if (groups)
+            gp = int32_ptr(*groups, ngroups + 1, dev, "cu_groups must be a contiguous int32 tensor [groups + 1] on q's device");
+    } else {
+        check(!prefix_lens && !groups, "prefix_lens and cu_groups need prefix_table");
+    }
+    const int rows = q.dim() == 4 ? size32(q.size(1), "rows") : 1, Hq = size32(q.size(-2), "Hq");
+    const Place at(dev, a[12]);
+    const OptTensor out = output_like(opt_tensor(a[8], "out"), q, dev, at);
+    const OptTensor lse = lse_of(opt_tensor(a[9], "lse"), truth(a[10], "return_lse"), q.sizes().slice(0, q.dim() - 1), dev, at);
+    if (nseq == 0 || rows == 0)
+        return answer(SDP_OK, {&out, &lse});
+    const double scale = a[7] == Py_None ? 1.0 / std::sqrt(static_cast<double>(p.D)) : number(a[7], "scale");
+    const int n = size32(nseq, "nseq"), ng = size32(ngroups, "the number of groups");
+    OptTensor ws = opt_tensor(a[11], "workspace");
+    if (!ws) {
+        const long long need = sdp_fwd_cache16_workspace_bytes(n, rows, Hq, p.Hkv, p.D, dt, ng);
+        if (need < 0)
+            return answer(need, {&out, &lse});
+        ws = at.empty({need}, at::kByte);
+    } else {
+        check(cuda_index(*ws) == dev && ws->is_contiguous(), "workspace must be a contiguous tensor on q's device");
+    }
+    const int rc = sdp_fwd_cache16(q.data_ptr(), p.k.data_ptr(), p.v.data_ptr(), p.pages, p.page, table.data_ptr<int>(),
+                                   table.stride(0), size32(table.size(1), "max_pages"), lp,
+                                   ng > 0 ? prefix->data_ptr<int>() : nullptr, ng > 0 ? prefix->stride(0) : 0,
+                                   ng > 0 ? size32(prefix->size(1), "the prefixes' pages") : 0, pl, gp, ng, out->data_ptr(),
+                                   lse_ptr(lse), n, rows, Hq, p.Hkv, p.D, static_cast<float>(scale), dt, ws->data_ptr(),
+                                   ws->nbytes(), at.handle());
+    return answer(rc, {&out, &lse});
+}
+
 // ------------------------------------------------------------------ sliding windows
 
 // What both window calls want of q, k and v; their device and dtype code.
@@ -533,6 +693,8 @@ PyMethodDef methods[] = {
     method<cache4_append, 7>("cache4_append"),
     method<cache4_gather, 8>("cache4_gather"),
     method<fwd_cache4, 12>("fwd_cache4"),
+    method<cache16_append, 15>("cache16_append"),
+    method<fwd_cache16, 13>("fwd_cache16"),
     method<fwd_window, 10>("fwd_window"),
     method<fwd_varlen_window, 13>("fwd_varlen_window"),
     {nullptr, nullptr, 0, nullptr},

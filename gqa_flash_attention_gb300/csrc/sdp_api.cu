@@ -182,6 +182,29 @@ int encode_map_thd_uncached(CUtensorMap *map, const void *base, int dtype, int D
     return SDP_OK;
 }
 
+// 3-D map over the same tensor with the heads next to the columns: (column, head, token) coordinates, box = 64
+// columns x box_heads heads x box_rows tokens, so that a box holds the heads of one token, then the next token's.
+int encode_map_tokens_uncached(CUtensorMap *map, const void *base, int dtype, int D, long long tokens, long long heads,
+                               unsigned box_heads, unsigned box_tokens)
+{
+    EncodeTiledFn enc = encoder();
+    if (enc == nullptr)
+        return cuda_fail(cudaErrorNotSupported);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(heads) * D * 2};
+    const cuuint32_t box[3] = {64, box_heads, box_tokens};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    const CUresult r = encode_in_context([&] {
+        return enc(map, dtype == SDP_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                   const_cast<void *>(base), dims, strides, box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+    if (r != CUDA_SUCCESS)
+        return cuda_fail(cudaErrorInvalidValue);
+    return SDP_OK;
+}
+
 // Encoded maps are a pure function of (address, dtype, D, rows, planes, box
 // rows, layout), so repeated calls on the same buffers reuse them instead of
 // re-encoding (a few microseconds of host time per map): a small table,
@@ -192,10 +215,11 @@ struct MapKey {
     long long rows, planes;
     unsigned box_rows;
     bool thd;
+    unsigned box_heads = 0;  // not 0: a map whose boxes hold that many heads of each token
     bool operator==(const MapKey &o) const
     {
         return base == o.base && dtype == o.dtype && D == o.D && rows == o.rows && planes == o.planes &&
-               box_rows == o.box_rows && thd == o.thd;
+               box_rows == o.box_rows && thd == o.thd && box_heads == o.box_heads;
     }
 };
 constexpr int kMapCacheSize = 64;
@@ -218,8 +242,11 @@ int encode_cached(CUtensorMap *map, const MapKey &key)
                 return SDP_OK;
             }
     }
-    const int rc = key.thd ? encode_map_thd_uncached(map, key.base, key.dtype, key.D, key.rows, key.planes, key.box_rows)
-                           : encode_map_uncached(map, key.base, key.dtype, key.D, key.rows, key.planes, key.box_rows);
+    const int rc = key.box_heads != 0
+                       ? encode_map_tokens_uncached(map, key.base, key.dtype, key.D, key.rows, key.planes, key.box_heads,
+                                                    key.box_rows)
+                   : key.thd ? encode_map_thd_uncached(map, key.base, key.dtype, key.D, key.rows, key.planes, key.box_rows)
+                             : encode_map_uncached(map, key.base, key.dtype, key.D, key.rows, key.planes, key.box_rows);
     if (rc != SDP_OK)
         return rc;
     std::lock_guard<std::mutex> lk(g_map_mu);
@@ -511,6 +538,12 @@ int tensor_map_thd(CUtensorMap *map, const void *base, int dtype, int D, long lo
                    unsigned box_rows)
 {
     return encode_map_thd(map, base, dtype, D, rows, heads, box_rows);
+}
+
+int tensor_map_tokens(CUtensorMap *map, const void *base, int dtype, int D, long long tokens, long long heads,
+                      unsigned box_heads, unsigned box_tokens)
+{
+    return encode_cached(map, MapKey{base, dtype, D, tokens, heads, box_tokens, true, box_heads});
 }
 
 }  // namespace sdp

@@ -35,6 +35,10 @@ int tensor_map(CUtensorMap *map, const void *base, int dtype, int D, long long r
 int tensor_map_thd(CUtensorMap *map, const void *base, int dtype, int D, long long rows, long long heads,
                    unsigned box_rows);
 
+// (token, head, dim) again, with boxes of 64 columns x box_heads heads x box_tokens tokens: coordinates (column, head, token).
+int tensor_map_tokens(CUtensorMap *map, const void *base, int dtype, int D, long long tokens, long long heads,
+                      unsigned box_heads, unsigned box_tokens);
+
 inline bool is_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace sdp

@@ -3,7 +3,8 @@
 ``qk_norm_rope``: norms and position rotation of the query and key heads in one pass, with
 ``rope_inv_freq`` and ``rope_table`` for its frequencies. ``Cache4``: a paged cache held in 4 bits,
 written by ``cache4_append`` and read back by ``cache4_gather``; ``fwd_cache4``: the attention of each
-sequence's last tokens over it. ``fwd_window`` and ``fwd_varlen_window``: prefill attention with a sliding
+sequence's last tokens over it. ``Cache16``: a paged cache in 16 bits, written by ``cache16_append`` with norms and
+rotation on the way; ``fwd_cache16``: the attention over it, of batches that share prefixes too. ``fwd_window`` and ``fwd_varlen_window``: prefill attention with a sliding
 window and first tokens that stay visible.
 
 The work runs in libsdp.so (``include/sdp.h`` states layouts, ownership and errors); PyTorch supplies
@@ -27,7 +28,8 @@ import torch
 from . import LIB_PATH, SDP_OK, _check, _DTYPE_CODE, lib
 
 __all__ = ["rope_inv_freq", "rope_table", "RopeTable", "qk_norm_rope", "Cache4", "cache4_empty", "cache4_append",
-           "cache4_gather", "CACHE4_GROUP", "fwd_cache4", "cache4_workspace_bytes",
+           "cache4_gather", "CACHE4_GROUP", "fwd_cache4", "cache4_workspace_bytes", "Cache16", "cache16_empty",
+           "cache16_append", "fwd_cache16", "cache16_workspace_bytes",
            "fwd_window", "fwd_varlen_window"]
 
 CACHE4_GROUP = 64  # channels that share one scale and bias
@@ -53,6 +55,14 @@ def _lib() -> ctypes.CDLL:
         L.sdp_fwd_cache4_workspace_bytes.restype = ll
         L.sdp_fwd_cache4.argtypes = [vp, *pool, vp, vp, vp, i, i, i, i, i, f, i, i, i, vp, ctypes.c_ulonglong, vp]
         L.sdp_fwd_cache4.restype = i
+        L.sdp_cache16_append.argtypes = [vp, vp, i, i, vp, ll, i, vp, ll, ll, vp, ll, ll, vp, ll, ll, vp, ll, ll, vp, vp, i, i,
+                                         vp, ll, i, vp, i, f, vp, vp, i, f, i, i, i, i, i, vp]
+        L.sdp_cache16_append.restype = i
+        L.sdp_fwd_cache16_workspace_bytes.argtypes = [i] * 7
+        L.sdp_fwd_cache16_workspace_bytes.restype = ll
+        L.sdp_fwd_cache16.argtypes = [vp, vp, vp, i, i, vp, ll, i, vp, vp, ll, i, vp, vp, i, vp, vp, i, i, i, i, i, f, i, vp,
+                                      ctypes.c_ulonglong, vp]
+        L.sdp_fwd_cache16.restype = i
         L.sdp_fwd_window.argtypes = [vp] * 5 + [i] * 6 + [f, i, i, i, vp]
         L.sdp_fwd_window.restype = i
         L.sdp_fwd_varlen_window.argtypes = [vp] * 7 + [i] * 7 + [f, i, i, i, vp]
@@ -82,7 +92,8 @@ class _Binding:
         spec = importlib.util.spec_from_file_location("_serving", BINDING_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        for f in ("qk_norm_rope", "cache4_append", "cache4_gather", "fwd_cache4", "fwd_window", "fwd_varlen_window"):
+        for f in ("qk_norm_rope", "cache4_append", "cache4_gather", "fwd_cache4", "cache16_append", "fwd_cache16", "fwd_window",
+                  "fwd_varlen_window"):
             setattr(self, f, getattr(module, f))
         return self.__dict__[name]
 
@@ -268,6 +279,84 @@ def fwd_cache4(q: torch.Tensor, cache: Cache4, cache_lens: torch.Tensor, block_t
     """
     rc, out, lse = _binding.fwd_cache4(q, cache, cache_lens, block_table, scale, window, sinks, out, lse, return_lse,
                                        workspace, stream)
+    if rc != SDP_OK:
+        _check(rc)
+    return out, lse
+
+
+# ------------------------------------------------------------------ the 16-bit paged cache
+
+
+class Cache16(NamedTuple):
+    """A pool of pages that hold keys and values in 16 bits: float16 or bfloat16 [num_pages, Hkv, page_size, D] each,
+    page_size a multiple of 16, contiguous on one device."""
+    k: torch.Tensor
+    v: torch.Tensor
+
+
+def cache16_empty(num_pages: int, Hkv: int, D: int, page_size: int = 64, dtype: torch.dtype = torch.bfloat16,
+                  device="cuda") -> Cache16:
+    """A pool of zeroed pages."""
+    if D not in (128, 256) or page_size <= 0 or page_size % 16 or num_pages <= 0 or Hkv <= 0 or dtype not in _DTYPE_CODE:
+        raise ValueError("D must be 128 or 256, page_size a multiple of 16, sizes positive, dtype float16 or bfloat16")
+    return Cache16(*(torch.zeros(num_pages, Hkv, page_size, D, dtype=dtype, device=device) for _ in range(2)))
+
+
+def cache16_append(cache: Cache16, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor,
+                   block_table: torch.Tensor, rope: RopeTable | None = None, q: torch.Tensor | None = None,
+                   positions: torch.Tensor | None = None, q_weight: torch.Tensor | None = None,
+                   k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None, stream=None):
+    """Writes new rows into the cache, the keys normed and rotated on the way, and norms and rotates their queries.
+
+    k, v: [tokens, Hkv, D] and q (or None): [tokens, Hq, D] of the cache's dtype with free token and head strides, as views
+    of a fused projection: rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 become the last tokens of sequence i, as
+    cache4_append has them. rope (rope_table's), weights, eps and interleaved are qk_norm_rope's, with its results;
+    positions: int32 or int64 [tokens], by default each token's place in its sequence. Returns q's rows: a contiguous
+    tensor, or q_out, which may be q itself; None without q. Rows in no sequence, and those of bad offsets and
+    lengths, are left out; those and pages outside the pool show in poll_status(). Enqueued on `stream` (default: the
+    current stream), not synchronised.
+    """
+    rc, q_out = _binding.cache16_append(cache, k, v, cu_seqlens, cache_lens, block_table, rope, q, positions, q_weight,
+                                        k_weight, eps, interleaved, q_out, stream)
+    if rc != SDP_OK:
+        _check(rc)
+    return q_out
+
+
+def cache16_workspace_bytes(nseq: int, rows: int, Hq: int, Hkv: int, D: int, dtype: torch.dtype, groups: int = 0) -> int:
+    """Bytes of workspace that fwd_cache16 needs for these sizes and that many groups on the current device."""
+    if dtype not in _DTYPE_CODE:
+        raise ValueError("dtype must be float16 or bfloat16")
+    rc = _lib().sdp_fwd_cache16_workspace_bytes(nseq, rows, Hq, Hkv, D, _DTYPE_CODE[dtype], groups)
+    _check(min(rc, 0))
+    return rc
+
+
+def fwd_cache16(q: torch.Tensor, cache: Cache16, cache_lens: torch.Tensor, block_table: torch.Tensor,
+                prefix_table: torch.Tensor | None = None, prefix_lens: torch.Tensor | None = None,
+                cu_groups: torch.Tensor | None = None, scale: float | None = None, out: torch.Tensor | None = None,
+                lse: torch.Tensor | None = None, return_lse: bool = True, workspace: torch.Tensor | None = None,
+                stream=None):
+    """Attention of each sequence's last rows over the 16-bit cache (decoding), shared prefixes computed once.
+
+    q: [nseq, Hq, D], or [nseq, rows, Hq, D] with up to 32 rows (drafted tokens): row i of sequence s is its token
+    cache_lens[s] - rows + i and sees the keys up to itself, already in the cache. Contiguous, of the cache's dtype.
+    cache_lens: int32 [nseq]; block_table: int32 [nseq, max_pages].
+
+    Sequences cu_groups[g] .. cu_groups[g + 1] - 1 have their first prefix_lens[g] tokens in common, in the pages of
+    prefix_table[g] (int32 [groups, pages]; for one group of all sequences cu_groups may be None). These are read
+    and multiplied once for the whole group, and entries of its sequences' block tables for pages that the prefix fills are
+    not read, except of sequences shorter than the prefix and rows - 1 more, which go through their own pages. A
+    prefix may end inside a page. All on the device: a captured step stays valid when lengths and tables change.
+
+    Returns (o like q, lse fp32 without the last dimension, or None); a row that sees no key gives 0 and -inf. workspace: a
+    contiguous CUDA tensor of cache16_workspace_bytes, not used by another call that may overlap; when None it comes
+    from torch's allocator. Enqueued on `stream` (default: the current stream), not synchronised; bad lengths, groups
+    and pages show in poll_status().
+    """
+    rc, out, lse = _binding.fwd_cache16(q, cache, cache_lens, block_table, prefix_table, prefix_lens, cu_groups, scale, out,
+                                        lse, return_lse, workspace, stream)
     if rc != SDP_OK:
         _check(rc)
     return out, lse

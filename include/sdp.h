@@ -351,6 +351,69 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
                    int dtype, int window, int sinks, void *workspace, unsigned long long workspace_bytes, void *stream);
 
 /*
+ * The paged cache held in 16 bits: pools k_cache and v_cache of dtype [num_pages, Hkv, page_size, D] (page_size a
+ * multiple of 16; 16-byte aligned, contiguous), with block tables as the 4-bit cache has them.
+ *
+ * sdp_cache16_append — writes new rows into the cache, k's with sdp_qk_norm_rope's norm and rotation applied on
+ * the way, v's as they are, and norms and rotates the same tokens' queries into q_out: that call and the copies in one
+ * pass. Arguments of the same names are those of sdp_qk_norm_rope (the same results, bit for bit) and of sdp_cache4_append:
+ *   q, q_out    device, dtype [tokens, Hq, D] at token and head strides in elements, multiples of 8; q_out may be q
+ *               with q's strides. Hq 0 leaves them out (they may be NULL)
+ *   k, v        device, dtype [tokens, Hkv, D] likewise
+ *   cu_seqlens, cache_lens  as sdp_cache4_append. Rows in no sequence are left out, q's too
+ *   positions   device, int32 or (positions_64) int64 at stride p_st: each token's position for the rotation; NULL:
+ *               its place in its sequence
+ *   turns, rot_dim (0: no rotation), mscale, q_weight, k_weight (NULL: no norm), weight_fp32, eps, interleaved
+ * Bad offsets and lengths (SDP_ERR_BAD_SEQLENS: the sequence's rows are left out) and pages outside the pool
+ * (SDP_ERR_BAD_PAGES: k's and v's rows are) are found by the kernel and reported by the next sdp_poll_status. A page that
+ * two sequences write at the same places holds either's rows. Errors, streams and the status word's first-call
+ * allocation as sdp_fwd.
+ */
+int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_size, const int *block_table,
+                       long long table_stride, int max_pages, const void *q, long long q_st, long long q_sh, void *q_out,
+                       long long qo_st, long long qo_sh, const void *k, long long k_st, long long k_sh, const void *v,
+                       long long v_st, long long v_sh, const int *cu_seqlens, const int *cache_lens, int nseq, int tokens,
+                       const void *positions, long long p_st, int positions_64, const unsigned long long *turns,
+                       int rot_dim, float mscale, const void *q_weight, const void *k_weight, int weight_fp32, float eps,
+                       int interleaved, int Hq, int Hkv, int D, int dtype, void *stream);
+
+/*
+ * sdp_fwd_cache16 — attention of each sequence's last `rows` tokens (at most 32) over the 16-bit cache, for batches whose
+ * sequences share prefixes: row i of sequence s is at position p = cache_lens[s] - rows + i and sees keys j <= p. A row
+ * that sees no key gets O = 0, LSE = -inf.
+ *
+ * Groups of consecutive sequences may share their first tokens: group g has the sequences cu_groups[g] ..
+ * cu_groups[g + 1] - 1, whose first prefix_lens[g] tokens are the same and stand in the pages of prefix_table's row g. Those
+ * keys are read once for the group (and for each further 128 of its (Hq / Hkv) * rows * sequences rows, which
+ * find them in L2), and each sequence's own pages supply the rest: entries of its block table for pages that the prefix
+ * fills are not read. A prefix may end inside a page; the sequence's own page there need not hold the prefix's tokens.
+ * A sequence whose first row does not see the whole prefix (shorter than prefix + rows - 1, or empty: a padded batch) goes
+ * through its own pages alone, and so does a group of one sequence, so block tables are to be complete for those.
+ *
+ * q, o   device, dtype [nseq, rows, Hq, D] contiguous; lse fp32 [nseq, rows, Hq] or NULL.
+ *        The rows' own keys must be in the cache (append first).
+ * block_table, cache_lens  device int32 [nseq, max_pages] at row stride table_stride, and [nseq]
+ * prefix_table, prefix_lens, cu_groups  device int32 [ngroups, prefix_pages] at row stride prefix_stride, [ngroups] and
+ *        [ngroups + 1], non-decreasing in [0, nseq]. cu_groups NULL with ngroups 1: all sequences. ngroups 0: no prefix is
+ *        shared (the others may be NULL). Sequences in no group share none; a prefix of length 0 is none.
+ * workspace  device scratch of at least sdp_fwd_cache16_workspace_bytes, 16-byte aligned, not overlapping the other
+ *        buffers and not shared with a call that may overlap on the GPU (two graphs replayed at once need two); its
+ *        contents do not matter before and are unspecified after.
+ * Scores, weights and sums are fp32; the weights are rounded to dtype for the product with V, as in sdp_fwd. The same call
+ * gives the same bits. Keys and values that a row does not see may hold infinities or NaN. Bad lengths leave that
+ * sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a bad prefix length or group is not shared, and reported the same; a
+ * page outside the pool leaves rows unspecified (SDP_ERR_BAD_PAGES), a wait that runs out all rows
+ * (SDP_ERR_DEVICE_TIMEOUT). Errors, streams and the status word's first-call allocation as sdp_fwd. Two kernels are enqueued
+ * on `stream`. The workspace size depends on the current device; a negative value is a status code.
+ */
+long long sdp_fwd_cache16_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups);
+int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,
+                    const int *block_table, long long table_stride, int max_pages, const int *cache_lens,
+                    const int *prefix_table, long long prefix_stride, int prefix_pages, const int *prefix_lens,
+                    const int *cu_groups, int ngroups, void *o, float *lse, int nseq, int rows, int Hq, int Hkv, int D,
+                    float scale, int dtype, void *workspace, unsigned long long workspace_bytes, void *stream);
+
+/*
  * sdp_fwd_window, sdp_fwd_varlen_window — sdp_fwd and sdp_fwd_varlen with a sliding
  * window and first tokens that stay visible: row i of a sequence with sq query rows and
  * skv keys is at position p = skv - sq + i (its rows are the last ones, so a chunk behind a
