@@ -16,7 +16,8 @@ struct Shape {
     long long rows_o, rows_p, joins_o, joins_p, bytes;
 };
 
-long long align16(long long x) { return (x + 15) / 16 * 16; }
+// Sections of the workspace begin on 32 bytes of it, after at most 16 bytes that its own start lacks.
+long long align32(long long x) { return (x + 31) / 32 * 32; }
 
 int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups, Shape *sh)
 {
@@ -46,14 +47,15 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
         return rc;
     const long long part = D == 128 ? sdp::c16::part_floats<128>(sh->part_rows) : sdp::c16::part_floats<256>(sh->part_rows);
     const long long problems = static_cast<long long>(nseq) * Hkv * sh->head_blocks;
-    const long long whole = ngroups > 0 ? align16(tokens * Hq * (D + 2) * 4) : 0;  // O, m and l of every row
-    sh->rows_o = align16(2 * sh->sms * part * 4);
+    const long long whole = ngroups > 0 ? align32(tokens * Hq * (D + 2) * 4) : 0;  // O, m and l of every row
+    sh->rows_o = align32(2 * sh->sms * part * 4);
     sh->rows_p = sh->rows_o + whole;
     sh->joins_o = sh->rows_p + whole;
-    sh->joins_p = sh->joins_o + align16(problems * sh->blocks_o * static_cast<long long>(sizeof(int2)));
-    sh->bytes = sh->joins_p + (ngroups > 0 ? align16(problems * ((rows + sh->toks_p - 1) / sh->toks_p) *
+    sh->joins_p = sh->joins_o + align32(problems * sh->blocks_o * static_cast<long long>(sizeof(int2)));
+    sh->bytes = sh->joins_p + (ngroups > 0 ? align32(problems * ((rows + sh->toks_p - 1) / sh->toks_p) *
                                                      static_cast<long long>(sizeof(int2)))
                                            : 0);
+    sh->bytes += 16;
     return SDP_OK;
 }
 
@@ -115,7 +117,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
         (rc = sdp::tensor_map(&m.k, k_cache, dtype, D, page_size, planes, box)) != SDP_OK ||
         (rc = sdp::tensor_map(&m.v, v_cache, dtype, D, page_size, planes, box)) != SDP_OK)
         return rc;
-    char *const ws = static_cast<char *>(workspace);
+    char *const ws = static_cast<char *>(workspace) + (sdp::is_aligned(workspace, 32) ? 0 : 16);
     p.o = static_cast<uint16_t *>(o);
     p.lse = lse;
     p.v = static_cast<const uint16_t *>(v_cache);
@@ -151,6 +153,8 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     p.timeout_ns = sdp::wait_timeout_ns();
     p.no_copies = sdp::debug_flags() & 1;
     p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+    if (p.c == 0.f)
+        p.c = 1e-37f;  // scores of 0, where those that a row does not see are still -inf
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (D == 128)

@@ -122,7 +122,7 @@ struct Span {
     bool bad;
 };
 
-__device__ __forceinline__ Span span_of(const Cache16AttnParams &p, int e)
+static __device__ __noinline__ Span span_of(const Cache16AttnParams &p, int e)
 {
     Span r{};
     if (e < p.ngroups) {
@@ -139,12 +139,12 @@ __device__ __forceinline__ Span span_of(const Cache16AttnParams &p, int e)
         return r;
     }
     const int s = e - p.ngroups, len = __ldg(p.lens + s);
+    const Share a = share_of(p, s);
     r.bad = len < 0 || len > p.max_pages * p.page_size;  // (the join reports it, and leaves the rows)
     r.hi = r.bad ? 0 : len;
-    const Share a = share_of(p, s);
     // a sequence whose first row does not see the whole prefix goes through its own pages
     r.lo = a.P > 0 && r.hi >= a.P + p.n - 1 ? a.P : 0;
-    r.k0 = r.lo / p.box * p.box;
+    r.k0 = r.lo & -p.box;
     r.first = s * p.n;
     r.toks = p.n;
     r.problems = p.Hkv * p.head_blocks * p.blocks_o;
@@ -157,15 +157,28 @@ __device__ __forceinline__ long long entry_length(const Span &s)
     return s.tiles > 0 ? static_cast<long long>(s.problems) * (s.tiles + OVERHEAD) : 0;
 }
 
-// First position of run i of n.
-__device__ __forceinline__ long long run_start(long long total, int i, int n) { return total * i / n; }
+// Positions cut into n runs: run i begins at floor(total * i / n).
+struct Cut {
+    long long total, q;
+    int r, n;
+    __device__ __forceinline__ Cut(long long positions, int most) : total(positions)
+    {
+        n = total < most ? static_cast<int>(total) : most;
+        const int d = max(n, 1);
+        // (a 64-bit division takes a few hundred cycles of a launch's first microseconds)
+        q = total <= 0xffffffffll ? static_cast<uint32_t>(total) / static_cast<uint32_t>(d) : total / d;
+        r = static_cast<int>(total - q * d);
+    }
+    __device__ __forceinline__ long long start(int i) const { return i * q + i * r / n; }
+    __device__ __forceinline__ int run_of(long long x) const { return static_cast<int>(((x + 1) * n - 1) / total); }
+};
 
 // Floats of a part: O [rows][D] (over its own l, so that no part is larger than the values it joins), then m and l of
-// each row, in all a multiple of 4.
+// each row, in all a multiple of 8 (O is stored 32 bytes at a time).
 template <int D>
 __host__ __device__ constexpr long long part_floats(int rows)
 {
-    return static_cast<long long>(rows) * (D + 4);
+    return static_cast<long long>(rows) * (D + 8);
 }
 
 constexpr int DEST_DIRECT = -1, DEST_ROWS = -2;  // else the part's number
@@ -200,7 +213,7 @@ struct Plan {
     static_assert(HOLDER_OFF + 12 <= BAR_OFF + BAR_AREA, "barrier area");
     static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
     static_assert(sizeof(Unit) == 64 && UNIT_OFF % 16 == 0, "unit ring");
-    static_assert(8 * (THREADS + THREADS / 32) <= NSLOTS * L::CHUNK_BYTES, "the sums of the problems' lengths");
+    static_assert(8 * (THREADS + THREADS / 32) + THREADS * static_cast<int>(sizeof(Span)) <= NSLOTS * L::CHUNK_BYTES, "the sums of the problems' lengths");
     // ring parity across units of any lengths: as the windowed kernel's, whose order of waits this one has
     static_assert(NSLOTS >= 4 && L::NSBUF <= 3, "ring parity soundness across units");
 };
@@ -216,33 +229,50 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)
     return ((w & E) == E ? 0xffffu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xffff0000u : 0u);
 }
 
-// Four lanes' rows by four 16-byte units, transposed in two exchanges: lane l then holds unit l & 3 of the rows l, l ^ 1,
-// l ^ 2 and l ^ 3, so that four lanes write 64 bytes of a row at once.
-__device__ __forceinline__ void transpose4(const uint32_t (&u)[16], uint32_t (&out)[4][4], int lane)
+// Eight words to a 32-byte boundary: a whole sector of a row.
+__device__ __forceinline__ void st_global_v8(void *at, const uint32_t *w)
 {
-    const bool odd = lane & 1, high = lane & 2;
-    uint32_t own[2][4], next[2][4];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const uint32_t u0 = u[8 * h + x], u1 = u[8 * h + 4 + x];
-            own[h][x] = odd ? u1 : u0;
-            next[h][x] = __shfl_xor_sync(FULL, odd ? u0 : u1, 1);
-        }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        out[0][x] = high ? own[1][x] : own[0][x];
-        out[1][x] = high ? next[1][x] : next[0][x];
-        out[2][x] = __shfl_xor_sync(FULL, high ? own[0][x] : own[1][x], 2);
-        out[3][x] = __shfl_xor_sync(FULL, high ? next[0][x] : next[1][x], 2);
-    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
 }
 
-// Registers a thread of each warpgroup (softmax; loading and issuing; writing): the block launches with LAUNCH each, and
-// the softmax takes what the second group gives back.
-constexpr int LAUNCH_REGS = 168, SOFTMAX_REGS = 232, ISSUE_REGS = 104;
-static_assert(SOFTMAX_REGS + ISSUE_REGS <= 2 * LAUNCH_REGS, "registers of the launch");
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_of(const uint32_t (&s)[32], int i)
+{
+    return pack2<BF16>(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+}
+
+__device__ __forceinline__ uint64_t f2_of(const uint32_t (&s)[32], int i)
+{
+    return ptx::f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+}
+
+// The values of keys pos0 + 1 + b (bit b of `odd`, all of which the row sees) that are not finite, and so were left out of
+// the product, onto a row that has been written: whatever their weights, which are positive, these decide.
+template <int D, bool BF16>
+static __device__ __noinline__ void add_odd(const Cache16AttnParams &p, const Unit &un, uint32_t odd, char *row, bool direct)
+{
+    for (; odd != 0u; odd &= odd - 1u) {
+        const int key = un.pos0 + __ffs(odd), page = key / p.page_size;
+        const int id = p.table[un.table * p.table_stride + page];
+        if (id < 0 || id >= p.num_pages)
+            return;
+        const uint16_t *v = p.v + ((static_cast<long long>(id) * p.Hkv + un.kv) * p.page_size + (key - page * p.page_size)) * D;
+        for (int i = 0; i < D; ++i) {
+            const uint32_t w = v[i];
+            if (not_finite<BF16>(w) == 0u)
+                continue;
+            const float x = unpack16<BF16>(w).x;
+            if (direct) {
+                uint16_t *o = reinterpret_cast<uint16_t *>(row) + i;
+                *o = static_cast<uint16_t>(pack2<BF16>(unpack16<BF16>(*o).x + x, 0.f));
+            } else {
+                reinterpret_cast<float *>(row)[i] += x;
+            }
+        }
+    }
+}
 
 }  // namespace c16
 
@@ -330,16 +360,22 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    // The join's blocks may be launched: they find no room beside a CTA of this kernel (its registers), so they start on
+    // the SMs whose CTA has ended, and wait there for the last one.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- the lengths of all entries, summed up: each thread has some consecutive ones. In the ring, which is not in
     // use before the first unit is known.
     const int entries = p.ngroups + p.nseq;
     const int per = (entries + THREADS - 1) / THREADS;
     long long *const prefix = reinterpret_cast<long long *>(smem + QB * L::Q_BYTES), *const warp_sum = prefix + THREADS;
+    Span *const stash = reinterpret_cast<Span *>(warp_sum + THREADS / 32);  // (of thread e's first entry, where that is e)
     {
         const int e0 = min(entries, static_cast<int>(threadIdx.x) * per), e1 = min(entries, e0 + per);
         long long sum = 0;
         for (int e = e0; e < e1; ++e) {
             const Span s = span_of(p, e);
+            if (e == static_cast<int>(threadIdx.x))
+                stash[e] = s;
             sum += entry_length(s);
             if (s.bad && e < p.ngroups && run == 0)
                 atomicCAS(p.status, 0u, static_cast<unsigned>(SITE_SEQLENS));
@@ -360,32 +396,13 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
-    // Bounded waits, inline: a call in a branch with registers of its own (setmaxnreg) does not assemble. The limit
-    // holds a tile: who waits for `tiles` of them waits that much longer.
+    // A whole warp's bounded wait. The limit holds a tile: who waits for `tiles` of them waits that much longer.
     auto wait_all = [&](uint32_t bar, uint32_t parity, uint32_t site, int tiles = 1) -> bool {
-        bool done = ptx::mbar_try_wait(bar, parity);
-        if (!__all_sync(FULL, done)) {
-            const uint64_t t0 = ptx::globaltimer_ns();
-            for (uint32_t it = 1; !__all_sync(FULL, done = ptx::mbar_try_wait(bar, parity)); ++it) {
-                if ((it & 15u) != 0)
-                    continue;
-                const bool late = static_cast<float>(ptx::globaltimer_ns() - t0) > static_cast<float>(p.timeout_ns) * tiles;
-                if (__any_sync(FULL, late || *abort_flag)) {
-                    if (late && !done) {
-                        *abort_flag = 1;
-                        const uint32_t cta = blockIdx.x < 0xFFFFFFu ? blockIdx.x : 0xFFFFFFu;
-                        atomicCAS(p.status, 0u, site | (cta << 8));
-                    }
-                    return false;
-                }
-            }
-        }
-        return true;
+        return __all_sync(FULL, ptx::mbar_try_wait(bar, parity) ||
+                                    wait_slow(bar, parity, abort_flag, p.status, p.timeout_ns * tiles, site));
     };
     auto drain = [&](uint32_t bar, uint32_t parity) {  // of what this warp issued itself
-        const uint64_t t0 = ptx::globaltimer_ns();
-        while (!ptx::mbar_try_wait(bar, parity) && ptx::globaltimer_ns() - t0 <= p.timeout_ns) {
-        }
+        wait_drain(bar, parity, p.timeout_ns);
     };
     auto arrive = [&](uint32_t bar) {  // once a warp
         __syncwarp();
@@ -402,7 +419,6 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     };
 
     if (warp >= 4 && warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE_REGS));
         if (warp == 4) {
             // ------------------------------------------------------ TMA producer
             if (!p.no_copies) {  // whole warp; one elected lane issues
@@ -450,14 +466,29 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                         }
                         return r;
                     };
-                    auto load_tile = [&](const CUtensorMap *map, const Boxes &t) -> bool {
-#pragma unroll
+                    // K_0, then K_{t + 1} (if any) and V_t for each tile: one loop, for the sake of the instruction cache
+                    Boxes next{}, last_k{}, before{};
+                    int looked = 0;  // tiles looked up
+#pragma unroll 1
+                    for (int x = -1; ok && x < 2 * un.n; ++x) {
+                        const bool of_k = x <= 0 || ((x & 1) && (x + 1) / 2 < un.n);
+                        if (of_k) {
+                            before = last_k;
+                            last_k = next;
+                            next = look_up(looked++);
+                        }
+                        if (x < 0)
+                            continue;
+                        const CUtensorMap *const map = of_k ? &tm_k : &tm_v;
+                        const Boxes &t = of_k || (x == 2 * un.n - 1) ? last_k : before;
+#pragma unroll 1
                         for (int ch = 0; ch < CPT; ++ch) {
-                            if (!wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY))
-                                return false;
+                            if (!(ok = wait_all(slot_empty0 + 8u * slot, ph ^ 1u, SITE_SLOT_EMPTY)))
+                                break;
                             const uint32_t full = slot_full0 + 8u * slot;
                             ptx::mbar_arrive_expect_tx_w(full, t.n * p.box * 256);
                             uint32_t dst = s_ring + slot * L::CHUNK_BYTES;
+#pragma unroll 1
                             for (int i = 0; i < t.n; ++i) {
                                 const int plane = __shfl_sync(FULL, t.plane, i), off = __shfl_sync(FULL, t.off, i);
                                 ptx::tma_load_3d_w(dst, map, full, ch * 128, off, plane);
@@ -471,24 +502,14 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                                 ph ^= 1u;
                             }
                         }
-                        return true;
-                    };
-                    Boxes now = look_up(0), next = look_up(1);
-                    ok = load_tile(&tm_k, now);
-                    for (int j = 0; ok && j < un.n; ++j) {
-                        const Boxes after = look_up(j + 2);
-                        if (j + 1 < un.n)
-                            ok = load_tile(&tm_k, next);
-                        if (ok)
-                            ok = load_tile(&tm_v, now);
-                        now = next;
-                        next = after;
                     }
                 }
                 // Every copy this warp issued lands before the CTA may exit.
+#pragma unroll 1
                 for (int b = 0; b < QB; ++b)
                     if (q_armed & (1u << b))
                         drain(q_full0 + 8u * b, (q_par >> b) & 1u);
+#pragma unroll 1
                 for (int s = 0; s < NS; ++s)
                     if (armed_mask & (1u << s))
                         drain(slot_full0 + 8u * s, (armed_par >> s) & 1u);
@@ -512,19 +533,13 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                         if (!(ok = wait_all(o_done0 + 8u * (pv % O_DONE_RING), (pv / O_DONE_RING) & 1, SITE_O_DONE)))
                             break;
                     }
-#pragma unroll
-                    for (int ch = 0; ch < CPT; ++ch) {
-                        const int pos = p0 + ch;
-                        if (!(ok = wait_all(slot_full0 + 8u * (pos % NS), (pos / NS) & 1, SITE_SLOT_FULL)))
-                            break;
-                    }
-                    if (!ok)
-                        break;
-                    ptx::tc_fence_after();
                     const uint32_t d_tmem = tmem + L::TM_S + (gt % NB) * TILE;
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < CPT; ++ch) {
-                        const int slot = (p0 + ch) % NS;
+                        const int pos = p0 + ch, slot = pos % NS;
+                        if (!(ok = wait_all(slot_full0 + 8u * slot, (pos / NS) & 1, SITE_SLOT_FULL)))
+                            break;
+                        ptx::tc_fence_after();
                         const uint64_t kslot = dk + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
                         const uint64_t qch = dq + static_cast<uint64_t>((2 * ch * L::BOX_BYTES) >> 4);
 #pragma unroll
@@ -535,6 +550,8 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                         issued = true;
                         ptx::mma_commit_w(slot_empty0 + 8u * slot);
                     }
+                    if (!ok)
+                        break;
                     ptx::mma_commit_w(s_full0 + 8u * (gt % NB));
                 }
                 if (!ok)
@@ -580,7 +597,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                     const bool ragged = r1 > r0 && ((r0 | r1) & 15) != 0;
                     const int a0 = max(r0, own - key0), a1 = un.prefix || p.n == 1 ? 0 : r1;  // keys that some rows do not see
                     const uint32_t a_tmem = tmem + L::TM_S + buf * TILE;
-#pragma unroll
+#pragma unroll 1
                     for (int ch = 0; ch < CPT; ++ch) {
                         const int pos = p0 + ch;
                         const int slot = pos % NS;
@@ -623,11 +640,17 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                             __syncwarp();
                         }
                         const uint64_t vslot = dv + static_cast<uint64_t>((slot * L::CHUNK_BYTES) >> 4);
+                        if (kk0 == 0 && kk1 == 8) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            if (kk >= kk0 && kk < kk1)
+                            for (int kk = 0; kk < 8; ++kk)
+                                ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
+                                              kk == 0 ? onto : 1u);
+                        } else {
+#pragma unroll 1
+                            for (int kk = kk0; kk < kk1; ++kk)
                                 ptx::mma_ts_w(tmem + L::TM_O + ch * 128, a_tmem + kk * 8, vslot + ((kk * 2048) >> 4), IDESC_PV,
                                               onto | (kk > kk0 ? 1u : 0u));
+                        }
                         issued = true;
                         ptx::mma_commit_w(slot_empty0 + 8u * slot);
                     }
@@ -654,12 +677,12 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < THREADS / 32; ++i)
                 total += warp_sum[i];
-            const int runs = total < gridDim.x ? static_cast<int>(total) : static_cast<int>(gridDim.x);
+            const Cut cut(total, gridDim.x);
             long long off = 0, left = 0;  // position in the entry's problems, positions left in the run
             int e = 0;
-            if (run < runs) {
-                const long long x = run_start(total, run, runs);
-                left = run_start(total, run + 1, runs) - x;
+            if (run < cut.n) {
+                const long long x = cut.start(run);
+                left = cut.start(run + 1) - x;
                 int w0 = 0;  // the last thread whose entries start at or before x
                 while (before + warp_sum[w0] <= x)
                     before += warp_sum[w0++];
@@ -669,38 +692,54 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 e = owner * per;
             }
             int base = -32;  // the lanes have entries base .. base + 31
+            bool fresh = true;  // the next problem is the one at `off` of entry e, else those below say which
+            int u = 0, in = 0, b = 0, blocks = 1, heads = 0, hb = 0, kv = 0;
+            const int blocks_p = (p.n + p.toks_p - 1) / p.toks_p, all_heads = p.Hkv * p.head_blocks;
             Span mine{};
             int longest = 1;  // of the units so far: its end may be what a place in the ring waits for
             for (int i = 0;; ++i) {
                 Unit un;
                 un.n = -1;
+                bool first_run = false;
+                int tiles_after = 0;
+                int2 *join = nullptr;
                 while (left > 0) {
                     if (e >= base + 32) {
+                        const int at = min(e + lane, entries - 1);
+                        mine = base < 0 && per == 1 ? stash[at] : span_of(p, at);  // (later the ring is in use)
                         base = e;
-                        mine = span_of(p, min(e + lane, entries - 1));
                     }
                     const int from = e - base;
                     const int tiles = __shfl_sync(FULL, mine.tiles, from), problems = __shfl_sync(FULL, mine.problems, from);
-                    const long long len = tiles + OVERHEAD;
-                    if (tiles == 0 || off >= len * problems) {  // `left` counts positions that exist: an entry follows
-                        off -= tiles == 0 ? 0 : len * problems;
-                        ++e;
-                        continue;
+                    const int len = tiles + OVERHEAD;
+                    if (fresh) {  // which of the entry's problems the run begins with
+                        if (tiles == 0 || off >= static_cast<long long>(len) * problems) {
+                            off -= tiles == 0 ? 0 : static_cast<long long>(len) * problems;
+                            ++e;  // the positions left exist: an entry follows
+                            continue;
+                        }
+                        u = off <= 0x7fffffffll ? static_cast<int>(off) / len : static_cast<int>(off / len);
+                        in = static_cast<int>(off - static_cast<long long>(u) * len);
+                        off = 0;
                     }
-                    const int u = static_cast<int>(off / len);
-                    const long long in = off - u * len, take_n = min(left, len - in);
-                    const int t0 = static_cast<int>(max(0ll, in - OVERHEAD)), t1 = static_cast<int>(in + take_n - OVERHEAD);
-                    off += take_n;
-                    left -= take_n;
-                    if (t1 <= t0)
-                        continue;  // the run ends inside the problem's start
-                    const int lo = __shfl_sync(FULL, mine.lo, from), hi = __shfl_sync(FULL, mine.hi, from);
                     const int first = __shfl_sync(FULL, mine.first, from), toks = __shfl_sync(FULL, mine.toks, from);
-                    const int k0 = __shfl_sync(FULL, mine.k0, from);
                     un.prefix = e < p.ngroups;
-                    const int block = un.prefix ? p.toks_p : p.toks_o, blocks = (toks + block - 1) / block;
-                    const int b = u % blocks, hb = u / blocks % p.head_blocks;
-                    un.kv = u / blocks / p.head_blocks;
+                    const int block = un.prefix ? p.toks_p : p.toks_o;
+                    if (fresh) {
+                        blocks = (toks + block - 1) / block;
+                        b = u % blocks;
+                        heads = u / blocks;
+                        kv = heads / p.head_blocks;
+                        hb = heads - kv * p.head_blocks;
+                        fresh = false;
+                    }
+                    // the problem's positions [in, in + take_n)
+                    const int take_n = static_cast<int>(min(left, static_cast<long long>(len - in)));
+                    const int t0 = max(0, in - OVERHEAD), t1 = in + take_n - OVERHEAD;
+                    left -= take_n;
+                    const int lo = __shfl_sync(FULL, mine.lo, from), hi = __shfl_sync(FULL, mine.hi, from);
+                    const int k0 = __shfl_sync(FULL, mine.k0, from);
+                    un.kv = kv;
                     un.n = t1 - t0;
                     un.tile0 = k0 + t0 * TILE;
                     un.lo = lo;
@@ -715,19 +754,28 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                     const bool whole = t0 == 0 && t1 == tiles;
                     const bool joined = un.prefix || lo > 0;
                     un.dest = !whole ? 2 * run + (t0 == 0 ? 1 : 0) : joined ? DEST_ROWS : DEST_DIRECT;
-                    if (t0 == 0 && lane == 0) {  // for the join
-                        int parts = 1;
-                        if (!whole) {  // the run ends in the problem, whose last tile some run after it holds
-                            const long long last = run_start(total, run + 1, runs) + (tiles - t1) - 1;
-                            parts = static_cast<int>(((last + 1) * runs - 1) / total) - run + 1;
+                    first_run = t0 == 0;
+                    tiles_after = tiles - t1;
+                    join = un.prefix ? p.joins_p : p.joins_o;
+                    join += (static_cast<long long>(un.prefix ? first / p.n * blocks_p : un.table * p.blocks_o) + b) * all_heads + heads;
+                    // on to the next problem, where the run has positions left
+                    in = 0;
+                    kv = un.kv;
+                    if (++b == blocks) {
+                        b = 0;
+                        ++heads;
+                        if (++hb == p.head_blocks) {
+                            hb = 0;
+                            ++kv;
                         }
-                        const int heads = un.kv * p.head_blocks + hb;
-                        if (un.prefix)
-                            p.joins_p[(static_cast<long long>(first / p.n) * ((p.n + p.toks_p - 1) / p.toks_p) + b) *
-                                          (p.Hkv * p.head_blocks) + heads] = make_int2(run, parts);
-                        else
-                            p.joins_o[(static_cast<long long>(un.table) * p.blocks_o + b) * (p.Hkv * p.head_blocks) +
-                                      heads] = make_int2(run, parts);
+                    }
+                    if (kv == p.Hkv) {
+                        fresh = true;
+                        ++e;
+                    }
+                    if (un.n <= 0) {  // the run ends inside the problem's start
+                        un.n = -1;
+                        continue;
                     }
                     break;
                 }
@@ -738,6 +786,8 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 if (lane == 0) {
                     ring[at] = un;
                     ptx::mbar_arrive(unit_full0 + 8u * at);
+                    if (un.n >= 0 && first_run)  // for the join; the problem's last tile lies in this run or in one after it
+                        *join = make_int2(run, tiles_after == 0 ? 1 : cut.run_of(cut.start(run + 1) + tiles_after - 1) - run + 1);
                 }
                 if (un.n < 0)
                     break;
@@ -745,13 +795,14 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         }
     } else if (warp < 4) {
         // --------------------------------------- softmax / correction
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SOFTMAX_REGS));
         const int row = threadIdx.x;  // row within the tile = TMEM lane
         const int row_tok = row / p.heads, row_head = row - row_tok * p.heads;
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t t_s = tmem + lane_off + L::TM_S;
         const uint32_t t_o = tmem + lane_off + L::TM_O;
-        const float c = p.c;
+        const float c = p.c;  // not 0
+        const uint64_t c2 = ptx::f2_pack(c, c);
+        const uint32_t unseen = c > 0.f ? 0xff800000u : 0x7f800000u;  // -inf or inf
         bool ok = true;
         int g0 = 0;
         Unit un;
@@ -777,82 +828,88 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t ts = t_s + buf * TILE;
-                uint32_t sr[128];
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    ptx::tmem_ld32(ts + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * q]));
-                ptx::tmem_wait_ld();
-                float s[128];
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    s[i] = __uint_as_float(sr[i]);
-
-                // Only a tile that holds a key some row of the warp must not see is masked: the
-                // masked scores come out scaled (-inf where not seen), the others as they are.
+                // Columns [w0, w1) hold the tile's keys: the product takes no others.
                 const int k0 = un.tile0 + j * TILE;
+                const int w0 = max(0, un.lo - k0) & -64, w1 = min(TILE, (un.hi - k0 + 63) & -64);
+                // Scores of keys that a row does not see become -inf (times c)
                 const int hi = pos + 1 - k0, lo = un.lo - k0;
-                const bool masked = __any_sync(FULL, hi < TILE || lo > 0);
-                if (masked) {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const uint32_t vis = below(hi - 32 * w) & ~below(lo - 32 * w);
+                if (__any_sync(FULL, hi < w1 || lo > w0)) {
+#pragma unroll 1
+                    for (int w = w0; w < w1; w += 32) {
+                        const uint32_t vis = below(hi - w) & ~below(lo - w);
+                        if (__all_sync(FULL, vis == 0xffffffffu))
+                            continue;
+                        uint32_t s[32];
+                        ptx::tmem_ld32(ts + w, s);
+                        ptx::tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            s[32 * w + i] = (vis & (1u << i)) ? s[32 * w + i] * c : -INFINITY;
+                            s[i] = (vis & (1u << i)) ? s[i] : unseen;
+                        ptx::tmem_st32(ts + w, s);
                     }
+                    ptx::tmem_wait_st();
                 }
-                const float ce = masked ? 1.f : c;
-                float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
-                if (ce >= 0.f) {
+                // Two passes over the tile, 32 scores at a time, the next ones on their way meanwhile.
+                uint32_t a[32], b[32];
+                auto largest = [&](const uint32_t (&s)[32], float &mx0, float &mx1) {
 #pragma unroll
-                    for (int i = 4; i < 124; i += 8) {
-                        mx0 = ptx::max3(mx0, s[i], s[i + 1]);
-                        mx1 = ptx::max3(mx1, s[i + 2], s[i + 3]);
-                        mx2 = ptx::max3(mx2, s[i + 4], s[i + 5]);
-                        mx3 = ptx::max3(mx3, s[i + 6], s[i + 7]);
+                    for (int i = 0; i < 32; i += 4) {
+                        float x0, x1, x2, x3;
+                        ptx::f2_unpack(mul2(f2_of(s, i), c2), x0, x1);
+                        ptx::f2_unpack(mul2(f2_of(s, i + 2), c2), x2, x3);
+                        mx0 = ptx::max3(mx0, x0, x1);
+                        mx1 = ptx::max3(mx1, x2, x3);
                     }
-                    mx0 = ptx::max3(mx0, s[124], s[125]);
-                    mx1 = ptx::max3(mx1, s[126], s[127]);
-                    mx0 = ptx::max3(mx0, mx1, fmaxf(mx2, mx3));
-                } else {
-#pragma unroll
-                    for (int i = 4; i < 124; i += 8) {
-                        mx0 = ptx::min3(mx0, s[i], s[i + 1]);
-                        mx1 = ptx::min3(mx1, s[i + 2], s[i + 3]);
-                        mx2 = ptx::min3(mx2, s[i + 4], s[i + 5]);
-                        mx3 = ptx::min3(mx3, s[i + 6], s[i + 7]);
-                    }
-                    mx0 = ptx::min3(mx0, s[124], s[125]);
-                    mx1 = ptx::min3(mx1, s[126], s[127]);
-                    mx0 = ptx::min3(mx0, mx1, fminf(mx2, mx3));
+                };
+                float mx0 = -INFINITY, mx1 = -INFINITY;
+                if (w0 < w1)
+                    ptx::tmem_ld32(ts + w0, a);
+#pragma unroll 1
+                for (int w = w0; w < w1; w += 64) {
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(ts + w + 32, b);
+                    largest(a, mx0, mx1);
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(ts + (w + 64 < w1 ? w + 64 : w0), a);  // (the second pass begins with the first scores)
+                    largest(b, mx0, mx1);
                 }
                 // -inf while the row has seen no key (and its weights are 2^(-inf - 0) = 0); a dead row's maximum stays there
-                const float m_tile = mx0 * ce;
+                const float m_tile = fmaxf(mx0, mx1);
                 const float m_new = !dead && m_tile > m_used + RESCALE_THRESHOLD ? m_tile : m_used;
                 const float alpha = m_new == m_used ? 1.f : ptx::ex2(m_used - m_new);
                 const float neg_m = m_new == -INFINITY ? 0.f : -m_new;
-
-                uint32_t pk[64];
-                const uint64_t c2 = ptx::f2_pack(ce, ce), negm2 = ptx::f2_pack(neg_m, neg_m);
+                const uint64_t negm2 = ptx::f2_pack(neg_m, neg_m);
                 uint64_t sum01 = ptx::f2_pack(0.f, 0.f), sum23 = sum01;
+                auto weights = [&](const uint32_t (&s)[32], uint32_t to) {
+                    uint32_t pk[16];
 #pragma unroll
-                for (int i = 0; i < 64; i += 2) {
-                    float x0, x1, x2, x3;
-                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[2 * i], s[2 * i + 1]), c2, negm2), x0, x1);
-                    ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[2 * i + 2], s[2 * i + 3]), c2, negm2), x2, x3);
-                    const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1), p2 = ptx::ex2(x2), p3 = ptx::ex2(x3);
-                    sum01 = ptx::f2_add(sum01, ptx::f2_pack(p0, p1));
-                    sum23 = ptx::f2_add(sum23, ptx::f2_pack(p2, p3));
-                    pk[i] = pack2<BF16>(p0, p1);
-                    pk[i + 1] = pack2<BF16>(p2, p3);
+                    for (int i = 0; i < 16; i += 2) {
+                        float x0, x1, x2, x3;
+                        ptx::f2_unpack(ptx::f2_fma(f2_of(s, 2 * i), c2, negm2), x0, x1);
+                        ptx::f2_unpack(ptx::f2_fma(f2_of(s, 2 * i + 2), c2, negm2), x2, x3);
+                        const float p0 = ptx::ex2(x0), p1 = ptx::ex2(x1), p2 = ptx::ex2(x2), p3 = ptx::ex2(x3);
+                        sum01 = ptx::f2_add(sum01, ptx::f2_pack(p0, p1));
+                        sum23 = ptx::f2_add(sum23, ptx::f2_pack(p2, p3));
+                        pk[i] = pack2<BF16>(p0, p1);
+                        pk[i + 1] = pack2<BF16>(p2, p3);
+                    }
+                    ptx::tmem_st16(to, pk);  // P overwrites scores that both passes have read
+                };
+#pragma unroll 1
+                for (int w = w0; w < w1; w += 64) {
+                    ptx::tmem_wait_ld();
+                    ptx::tmem_ld32(ts + w + 32, b);
+                    weights(a, ts + w / 2);
+                    ptx::tmem_wait_ld();
+                    if (w + 64 < w1)
+                        ptx::tmem_ld32(ts + w + 64, a);
+                    weights(b, ts + w / 2 + 16);
                 }
                 // Poll S_{j+1}'s barrier now (same unit), so the answer returns while P_j is stored and handed off.
                 s_seen = j + 1 < n && ptx::mbar_test_wait(s_full0 + 8u * ((gj + 1) % NB), ((gj + 1) / NB) & 1);
                 float sum0, sum1, sum2, sum3;
                 ptx::f2_unpack(sum01, sum0, sum1);
                 ptx::f2_unpack(sum23, sum2, sum3);
-                ptx::tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-                ptx::tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
                 ptx::tmem_wait_st();
                 l = fmaf(l, alpha, (sum0 + sum1) + (sum2 + sum3));
 
@@ -890,6 +947,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     } else {
         // --------------------------------------- rows' ends: O over l, to the output or to the workspace
         const int w4 = warp & 3, row = w4 * 32 + lane;
+        const int row_tok = row / p.heads, row_head = row - row_tok * p.heads;
         const uint32_t t_o = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + L::TM_O;
         bool ok = true;
         int g0 = 0;
@@ -908,84 +966,52 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 ptx::tc_fence_after();
                 const bool none = l == 0.f;  // the row saw no key
                 const float inv = 1.f / l;
-                // rows row, row ^ 1, row ^ 2 and row ^ 3 as rows of q (and o), -1 where there is none
-                int at[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t = (row ^ i) / p.heads, h = (row ^ i) - t * p.heads;
-                    at[i] = t < un.toks && h < un.live ? (un.q_tok + t) * p.Hq + un.head + h : -1;
-                }
-                const bool slot = un.dest >= 0;
+                // the row of q and o, -1 where there is none
+                const int at = row_tok < un.toks && row_head < un.live ? (un.q_tok + row_tok) * p.Hq + un.head + row_head : -1;
+                const bool slot = un.dest >= 0, direct = un.dest == DEST_DIRECT;
                 float *const part = slot ? p.parts + un.dest * part_floats<D>(p.part_rows) : un.prefix ? p.rows_p : p.rows_o;
-                const int tok = row / p.heads;
+                char *const to = direct ? reinterpret_cast<char *>(p.o + static_cast<long long>(at) * D)
+                                        : reinterpret_cast<char *>(part + static_cast<long long>(slot ? row : at) * D);
 #pragma unroll 1
-                for (int cc = 0; cc < D / 32; ++cc) {
+                for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
-                    ptx::tmem_ld32(t_o + 32 * cc, o);
+                    ptx::tmem_ld32(t_o + c0, o);
                     ptx::tmem_wait_ld();
+                    if (at >= 0) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-                    if (odd != 0u) {
-                        // key pos0 + 1 + b is seen by tokens b + 1 and on
-#pragma unroll 1
-                        for (uint32_t left = odd & below(tok); left != 0u; left &= left - 1u) {
-                            const int key = un.pos0 + __ffs(left), page = key / p.page_size;
-                            const int id = p.table[un.table * p.table_stride + page];
-                            if (at[0] < 0 || id < 0 || id >= p.num_pages)
-                                continue;
-                            const uint16_t *v = p.v + ((static_cast<long long>(id) * p.Hkv + un.kv) * p.page_size +
-                                                       (key - page * p.page_size)) * D + cc * 32;
+                        for (int x = 0; x < 32; ++x)
+                            o[x] = none ? 0u : __float_as_uint(__uint_as_float(o[x]) * inv);
+                        if (direct) {
 #pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const uint32_t w = *reinterpret_cast<const uint32_t *>(v + i), x = not_finite<BF16>(w);
-                                const float2 f = unpack16<BF16>(w);
-                                if (x & 0xffffu)
-                                    o[i] = __float_as_uint(__uint_as_float(o[i]) + f.x);
-                                if (x >> 16)
-                                    o[i + 1] = __float_as_uint(__uint_as_float(o[i + 1]) + f.y);
-                            }
-                        }
-                        __syncwarp();
-                    }
-                    uint32_t out[4][4];
-                    if (un.dest == DEST_DIRECT) {
-                        uint32_t pk[16];
+                            for (int x = 0; x < 32; x += 8)
+                                reinterpret_cast<uint4 *>(to + 2 * c0)[x / 8] = make_uint4(
+                                    pack_of<BF16>(o, x), pack_of<BF16>(o, x + 2), pack_of<BF16>(o, x + 4), pack_of<BF16>(o, x + 6));
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            pk[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
-                        transpose4(pk, out, lane);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (at[i] >= 0)
-                                reinterpret_cast<uint4 *>(p.o + static_cast<long long>(at[i]) * D)[4 * cc + (lane & 3)] =
-                                    make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
-                    } else {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            transpose4(*reinterpret_cast<uint32_t(*)[16]>(&o[16 * h]), out, lane);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (at[i] >= 0)
-                                    reinterpret_cast<uint4 *>(part + static_cast<long long>(slot ? row ^ i : at[i]) * D)[8 * cc + 4 * h + (lane & 3)] =
-                                        make_uint4(out[i][0], out[i][1], out[i][2], out[i][3]);
+                            for (int x = 0; x < 32; x += 8)
+                                st_global_v8(to + 4 * (c0 + x), &o[x]);
                         }
                     }
+                    __syncwarp();
                 }
-                if (at[0] >= 0) {
-                    if (un.dest == DEST_DIRECT) {
+                ptx::tc_fence_before();
+                arrive(o_free);
+                if (at >= 0) {
+                    if (odd != 0u)
+                        add_odd<D, BF16>(p, un, odd & below(row_tok), to, direct);
+                    if (direct) {
                         if (p.lse != nullptr)
-                            p.lse[at[0]] = none ? -INFINITY : (m + log2f(l)) * LN2;
+                            p.lse[at] = none ? -INFINITY : (m + log2f(l)) * LN2;
                     } else if (slot) {
                         part[static_cast<long long>(p.part_rows) * D + row] = m;
                         part[static_cast<long long>(p.part_rows) * (D + 1) + row] = l;
                     } else {
-                        reinterpret_cast<float2 *>(part + static_cast<long long>(p.nseq) * p.n * p.Hq * D)[at[0]] = make_float2(m, l);
+                        reinterpret_cast<float2 *>(part + static_cast<long long>(p.nseq) * p.n * p.Hq * D)[at] = make_float2(m, l);
                     }
                 }
-                ptx::tc_fence_before();
+            } else {
+                arrive(o_free);
             }
-            arrive(o_free);
             g0 += n;
         }
     }
