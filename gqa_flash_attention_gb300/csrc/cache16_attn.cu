@@ -11,7 +11,7 @@ namespace {
 constexpr int kMaxRows = 32;  // a bit each in the mask of a unit's keys whose V is not finite
 
 struct Shape {
-    int heads, head_blocks, toks_p, toks_o, blocks_o, part_rows, sms;
+    int heads, head_blocks, toks_p, toks_o, blocks_o, blocks_p, part_rows, sms;
     // the workspace: parts; rows and joins of the sequences, then of the prefixes
     long long rows_o, rows_p, joins_o, joins_p, bytes;
 };
@@ -39,6 +39,7 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
     sh->toks_p = sdp::c16::TILE / sh->heads;
     sh->toks_o = std::min(rows, sh->toks_p);
     sh->blocks_o = (rows + sh->toks_o - 1) / sh->toks_o;
+    sh->blocks_p = (rows + sh->toks_p - 1) / sh->toks_p;
     const int most = ngroups > 0 ? static_cast<int>(std::min<long long>(sh->toks_p, tokens)) : sh->toks_o;
     sh->part_rows = most * sh->heads;
     int dev = 0;
@@ -52,8 +53,7 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
     sh->rows_p = sh->rows_o + whole;
     sh->joins_o = sh->rows_p + whole;
     sh->joins_p = sh->joins_o + align32(problems * sh->blocks_o * static_cast<long long>(sizeof(int2)));
-    sh->bytes = sh->joins_p + (ngroups > 0 ? align32(problems * ((rows + sh->toks_p - 1) / sh->toks_p) *
-                                                     static_cast<long long>(sizeof(int2)))
+    sh->bytes = sh->joins_p + (ngroups > 0 ? align32(problems * sh->blocks_p * static_cast<long long>(sizeof(int2)))
                                            : 0);
     sh->bytes += 16;
     return SDP_OK;
@@ -106,7 +106,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     int dev = 0, sms = 0;
     if ((rc = sdp::current_device(&dev, &sms)) != SDP_OK)
         return rc;
-    sdp::Cache16AttnParams p{};
+    sdp::Cache16Params p{};
     if ((rc = sdp::status_word(dev, &p.status)) != SDP_OK)
         return rc;
     const int box = std::min(page_size & -page_size, 128);  // the largest power of two that divides a page
@@ -115,7 +115,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     if ((rc = sdp::tensor_map_tokens(&m.q_prefix, q, dtype, D, tokens, Hq, sh.heads, sh.toks_p)) != SDP_OK ||
         (rc = sdp::tensor_map_tokens(&m.q_own, q, dtype, D, tokens, Hq, sh.heads, sh.toks_o)) != SDP_OK ||
         (rc = sdp::tensor_map(&m.k, k_cache, dtype, D, page_size, planes, box)) != SDP_OK ||
-        (rc = sdp::tensor_map(&m.v, v_cache, dtype, D, page_size, planes, box)) != SDP_OK)
+        (rc = sdp::tensor_map(&m.v, v_cache, dtype, D, page_size, planes, std::min(box, 64))) != SDP_OK)
         return rc;
     char *const ws = static_cast<char *>(workspace) + (sdp::is_aligned(workspace, 32) ? 0 : 16);
     p.o = static_cast<uint16_t *>(o);
@@ -130,6 +130,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     p.prefix_stride = prefix_stride;
     p.num_pages = num_pages;
     p.page_size = page_size;
+    p.page_inverse = page_size == 16 ? 0xffffffffu : static_cast<unsigned>((1ull << 32) / (page_size / 16));
     p.max_pages = max_pages;
     p.prefix_pages = prefix_pages;
     p.nseq = nseq;
@@ -143,7 +144,11 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     p.toks_p = sh.toks_p;
     p.toks_o = sh.toks_o;
     p.blocks_o = sh.blocks_o;
+    p.blocks_p = sh.blocks_p;
     p.box = box;
+    for (p.box_log2 = 4; (1 << p.box_log2) < box;)
+        ++p.box_log2;
+    p.sms = sms;
     p.part_rows = sh.part_rows;
     p.parts = reinterpret_cast<float *>(ws);
     p.rows_o = reinterpret_cast<float *>(ws + sh.rows_o);
@@ -158,8 +163,8 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (D == 128)
-        e = dtype == SDP_BF16 ? sdp::cache16_attn_d128_bf16(m, p, sms, st) : sdp::cache16_attn_d128_fp16(m, p, sms, st);
+        e = dtype == SDP_BF16 ? sdp::cache16_attn_d128_bf16(m, p, st) : sdp::cache16_attn_d128_fp16(m, p, st);
     else
-        e = dtype == SDP_BF16 ? sdp::cache16_attn_d256_bf16(m, p, sms, st) : sdp::cache16_attn_d256_fp16(m, p, sms, st);
+        e = dtype == SDP_BF16 ? sdp::cache16_attn_d256_bf16(m, p, st) : sdp::cache16_attn_d256_fp16(m, p, st);
     return e == cudaSuccess ? SDP_OK : sdp::record_cuda_error(e);
 }

@@ -3,9 +3,9 @@
 
 namespace sdp {
 
-cudaError_t cache16_attn_d128_fp16(const Cache16Maps &m, const Cache16AttnParams &p, int sms, cudaStream_t st)
+cudaError_t cache16_attn_d128_fp16(const Cache16Maps &m, const Cache16Params &p, cudaStream_t st)
 {
-    return launch_cache16_attn<128, false>(m, p, sms, st);
+    return launch_cache16_attn<128, false>(m, p, st);
 }
 
 }  // namespace sdp
