@@ -224,6 +224,7 @@ struct Runs {
     };
     int entries, per;
     Cut cut{0, 1};
+    long long upto;  // lane w: the entries' lengths before warp w's
 
     // The lengths of all entries, summed up: each thread has some consecutive ones. Ends with __syncthreads().
     __device__ __forceinline__ void begin(const Cache16Params &p, Shared &sh)
@@ -253,11 +254,17 @@ struct Runs {
         if (lane == 31)
             sh.sum[tid >> 5] = incl;
         __syncthreads();
-        long long total = 0;
-#pragma unroll 1
-        for (int i = 0; i < THREADS / 32; ++i)
-            total += sh.sum[i];
-        cut = Cut(total, p.sms);
+        // the warps' sums, a lane each
+        const long long of_warp = lane < THREADS / 32 ? sh.sum[lane] : 0;
+        upto = of_warp;
+#pragma unroll
+        for (int d = 1; d < THREADS / 32; d <<= 1) {
+            const long long x = __shfl_up_sync(FULL, upto, d);
+            if (lane >= d)
+                upto += x;
+        }
+        cut = Cut(__shfl_sync(FULL, upto, THREADS / 32 - 1), p.sms);
+        upto -= of_warp;
     }
 
     // The walk over run `run`, problem by problem, by a whole warp.
@@ -271,12 +278,12 @@ struct Runs {
     {
         const int lane = threadIdx.x & 31;
         const int run = static_cast<int>(blockIdx.x);
-        const long long x = cut.start(run);
-        left = static_cast<int>(cut.start(run + 1) - x);
-        long long before = 0;
-        int w0 = 0;  // the last thread whose entries start at or before x
-        while (before + sh.sum[w0] <= x)
-            before += sh.sum[w0++];
+        const int over = run * cut.r / cut.n;  // (start(run), and start(run + 1) with no division of its own)
+        const long long x = run * cut.q + over;
+        left = static_cast<int>(cut.q) + (run * cut.r - over * cut.n + cut.r >= cut.n ? 1 : 0);
+        // the last warp, and the last thread of it, whose entries start at or before x
+        const int w0 = 31 - __clz(__ballot_sync(FULL, lane < THREADS / 32 && upto <= x));
+        const long long before = __shfl_sync(FULL, upto, w0);
         const unsigned hit = __ballot_sync(FULL, before + sh.prefix[w0 * 32 + lane] <= x);
         const int owner = w0 * 32 + 31 - __clz(hit);
         skip = x - before - sh.prefix[owner];

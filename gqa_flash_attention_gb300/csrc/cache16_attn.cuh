@@ -74,8 +74,8 @@ struct Plan {
     static constexpr int RING_OFF = QB * L::Q_BYTES, V_OFF = RING_OFF + NK * K_SLOT;
     static constexpr int BAR_OFF = V_OFF + NV * V_SLOT;
     static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, -, mask of keys that are not finite, -, Waits
-    static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;      // the rows' maxima so far, and their l from the two groups of softmax warps
-    static constexpr int UNIT_OFF = SUM_OFF + 3 * TILE * 4;
+    static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;      // the rows' maxima so far; of a unit, their m and l from the two groups of softmax warps
+    static constexpr int UNIT_OFF = SUM_OFF + 4 * TILE * 4;
     static constexpr int SMEM_BYTES = UNIT_OFF + UNITS * static_cast<int>(sizeof(Unit));
     static_assert(HOLDER_OFF % 8 == 0 && HOLDER_OFF + 24 + sizeof(Waits) <= BAR_OFF + BAR_AREA, "barrier area");
     static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
@@ -91,8 +91,17 @@ __device__ __forceinline__ void st_global_v8(void *at, const uint32_t *w)
                  : "memory");
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack_of(const uint32_t (&s)[32], int i)
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+
+template <bool BF16, int N>
+__device__ __forceinline__ uint32_t pack_of(const uint32_t (&s)[N], int i)
 {
     return pack2<BF16>(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
 }
@@ -141,7 +150,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     const uint32_t odd_full = sum_free + 8u;  // the mask of its keys that are not finite is there
     const uint32_t unit_full0 = odd_full + 8u, unit_free0 = unit_full0 + 8u * PL::UNITS;  // + 8 (i % UNITS)
     const uint32_t max_full0 = unit_free0 + 8u * PL::UNITS;  // + 32 (tile % 2) + 8 (warp of a group)
-    float *const row_max = reinterpret_cast<float *>(smem + PL::SUM_OFF), *const row_l = row_max + TILE;
+    float *const row_max = reinterpret_cast<float *>(smem + PL::SUM_OFF), *const row_m = row_max + TILE, *const row_l = row_m + TILE;
     Unit *const ring = reinterpret_cast<Unit *>(smem + PL::UNIT_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + PL::HOLDER_OFF);
     Waits *const waits = reinterpret_cast<Waits *>(tmem_holder + 6);
@@ -467,12 +476,8 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             const bool dead = row_tok >= un.toks || row_head >= un.live;
             // the row sees keys [lo, pos]
             const int pos = min(un.hi - 1, un.prefix() ? un.pos0 : un.pos0 + row_tok);
-            // The rows' maxima go from tile to tile, from one group to the other; a group's first of a unit may have to wait for
-            // the end of the unit before, which reads them too.
-            auto turn = [&](int j, int gj) {
-                return (j >= 2 || k == 0 || wait_all(sum_free, (k - 1) & 1, SITE_O_DONE)) &&
-                       (gj == 0 || wait_all(max_other, ((gj - 1) >> 1) & 1, SITE_S_FULL));
-            };
+            // The rows' maxima go from tile to tile, from one group to the other: it is tile gj's turn.
+            auto turn = [&](int gj) { return gj == 0 || wait_all(max_other, ((gj - 1) >> 1) & 1, SITE_S_FULL); };
             float m_used = -INFINITY, l = 0.f;  // l: of this group's tiles, in units of 2^m_used
             for (int j = (g0 + group) & 1; j < n; j += 2) {
                 const int gj = g0 + j;
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 if (!(ok = wait_all(s_full0 + 8u * buf, (gj / NB) & 1, SITE_S_FULL)))
                     break;
                 if (idle) {  // whatever its lanes of P hold meets no other row
-                    if (!(ok = turn(j, gj)))
+                    if (!(ok = turn(gj)))
                         break;
                     arrive(max_mine);
                     arrive(p_full0 + 16u * buf);
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 }
                 // -inf while the row has seen no key (and its weights are 2^(-inf - 0) = 0); a dead row's maximum stays there
                 const float m_tile = fmaxf(mx0, mx1);
-                if (!(ok = turn(j, gj)))
+                if (!(ok = turn(gj)))
                     break;
                 const float m_old = j > 0 ? row_max[row] : -INFINITY;
                 const float m_new = !dead && m_tile > m_old + RESCALE_THRESHOLD ? m_tile : m_old;
@@ -604,12 +609,17 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             }
             if (!ok)
                 break;
-            if (((g0 + n - 1) & 1) != group) {  // the other group has the last tile, and the maximum of all
-                if (!(ok = turn(n == 1 ? 0 : 2, g0 + n)))
+            const bool latest = ((g0 + n - 1) & 1) == group;
+            if (!latest) {  // the other group has the last tile, and the maximum of all
+                if (!(ok = turn(g0 + n)))
                     break;
                 if (l != 0.f)
                     l *= ptx::ex2(m_used - row_max[row]);
             }
+            if (k > 0 && !(ok = wait_all(sum_free, (k - 1) & 1, SITE_O_DONE)))
+                break;
+            if (latest)
+                row_m[row] = m_used;
             row_l[group * TILE + row] = l;
             arrive(sum_full);
             g0 += n;
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 (un.prefix() ? p.joins_p : p.joins_o)[un.join] = make_int2(run, runs.parts_of(un.after));
             if (!(ok = wait_all(sum_full, k & 1, SITE_O_DONE, n)))
                 break;
-            const float m = row_max[row], l = row_l[row] + row_l[TILE + row];
+            const float m = row_m[row], l = row_l[row] + row_l[TILE + row];
             arrive(sum_free);
             if (!(ok = wait_all(o_done0 + 8u * (last % O_DONE_RING), (last / O_DONE_RING) & 1, SITE_O_DONE)) ||
                 !(ok = wait_all(odd_full, k & 1, SITE_O_DONE)))
@@ -644,32 +654,38 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 float *const part = slot ? p.parts + un.dest * part_floats<D>(p.part_rows) : un.prefix() ? p.rows_p : p.rows_o;
                 char *const to = direct ? reinterpret_cast<char *>(p.o + static_cast<long long>(at) * D)
                                         : reinterpret_cast<char *>(part + static_cast<long long>(slot ? row : at) * D);
+                // (rolled, 16 channels at a time: run once a unit, straight code is fetched as it runs, at some 9 cycles an instruction)
+                uint32_t a[16], b[16];
+                auto store = [&](uint32_t (&o)[16], int c0) {
+                    if (at < 0)
+                        return;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+                        o[x] = none ? 0u : __float_as_uint(__uint_as_float(o[x]) * inv);
+#pragma unroll
+                    for (int x = 0; x < 16; x += 8) {
+                        if (direct)
+                            reinterpret_cast<uint4 *>(to + 2 * c0)[x / 8] =
+                                make_uint4(pack_of<BF16>(o, x), pack_of<BF16>(o, x + 2), pack_of<BF16>(o, x + 4), pack_of<BF16>(o, x + 6));
+                        else
+                            st_global_v8(to + 4 * (c0 + x), &o[x]);
+                    }
+                };
+                tmem_ld16(t_o, a);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 64) {
-                    uint32_t o[2][32];
-                    ptx::tmem_ld32(t_o + c0, o[0]);
-                    ptx::tmem_ld32(t_o + c0 + 32, o[1]);
+                for (int c0 = 0; c0 < D; c0 += 32) {
                     ptx::tmem_wait_ld();
-                    if (c0 + 64 == D) {  // the next unit's product may begin
+                    tmem_ld16(t_o + c0 + 16, b);
+                    store(a, c0);
+                    __syncwarp();
+                    ptx::tmem_wait_ld();
+                    if (c0 + 32 < D) {
+                        tmem_ld16(t_o + c0 + 32, a);
+                    } else {  // the next unit's product may begin
                         ptx::tc_fence_before();
                         arrive(o_free);
                     }
-                    if (at >= 0) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                o[h][x] = none ? 0u : __float_as_uint(__uint_as_float(o[h][x]) * inv);
-#pragma unroll
-                            for (int x = 0; x < 32; x += 8) {
-                                if (direct)
-                                    reinterpret_cast<uint4 *>(to + 2 * c0)[4 * h + x / 8] = make_uint4(
-                                        pack_of<BF16>(o[h], x), pack_of<BF16>(o[h], x + 2), pack_of<BF16>(o[h], x + 4), pack_of<BF16>(o[h], x + 6));
-                                else
-                                    st_global_v8(to + 4 * (c0 + 32 * h + x), &o[h][x]);
-                            }
-                        }
-                    }
+                    store(b, c0 + 16);
                     __syncwarp();
                 }
                 if (at >= 0) {
