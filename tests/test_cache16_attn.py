@@ -213,3 +213,352 @@ def test_every_row(lens, cu, prefix, rows, Hq, Hkv, D, page, dt):
     o, lse = sdp.fwd_cache16(**b.args())
     assert sdp.poll_status() == sdp.SDP_OK
     b.check(o, lse)
+
+
+MORE = [
+    # more entries than a CTA has threads: each looks up several
+    ([3 + i % 50 for i in range(700)], [0], [], 1, 4, 1, 128, 16, "bf16"),
+    ([40 + i % 30 for i in range(1100)], list(range(0, 1101, 2)), [20 + g % 25 for g in range(550)], 2, 2, 1, 256, 16, "fp16"),
+    # a block whose last rows have no query, and pages of 80 tokens
+    ([1300, 1333, 1290], [0, 3], [1281], 5, 20, 1, 128, 80, "bf16"),
+    ([4097, 4200], [0, 2], [4096], 32, 8, 4, 128, 64, "fp16"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,cu,prefix,rows,Hq,Hkv,D,page,dt", MORE)
+def test_many_entries_and_ragged_blocks(lens, cu, prefix, rows, Hq, Hkv, D, page, dt):
+    b = Batch(lens, cu, prefix, rows, Hq, Hkv, D, page, DTYPES[dt])
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale,kscale,D", [(0.0, 1.0, 128), (-0.1, 1.0, 256), (0.5, 1.0, 128), (0.02, 16.0, 256), (1e-30, 1.0, 128)])
+def test_scales(scale, kscale, D):
+    """Scores of 0, of the other sign, and of hundreds, whose maximum moves from tile to tile."""
+    b = Batch([700, 900, 650], [0, 3], [600], 2, 8, 2, D, 64, torch.bfloat16, kscale=kscale)
+    o, lse = sdp.fwd_cache16(**b.args(), scale=scale)
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("up", [True, False])
+def test_scores_that_grow_or_fall_along_the_keys(D, up):
+    """Each tile's maximum above the one before by more than is let pass (or far below it)."""
+    b = Batch([2000, 1200], [0, 2], [1000], 1, 4, 1, D, 64, torch.bfloat16)
+    for k, v in b.rows_kv:
+        n = k.shape[0]
+        ramp = torch.arange(n if up else n - 1, -1 if not up else n + n, 1 if up else -1)[:n].double()
+        k[:, :, :] = k * 0.25
+        k[:, :, 7] = (ramp / 24 - (n / 24 if up else 0)).to(k.dtype)[:, None]
+    b.rows_kv[1][0][:1000] = b.rows_kv[0][0][:1000]
+    b.rows_kv[1][1][:1000] = b.rows_kv[0][1][:1000]
+    b.q[..., 7] = 16.0
+    page = b.k.shape[2]
+    for s, n in enumerate(b.lens):
+        t = torch.arange(1000, n)
+        ids = b.table[s, t // page].long()
+        b.k[ids, :, t % page] = b.rows_kv[s][0][1000:]
+    t = torch.arange(1000)
+    b.k[b.prefix_table[0, t // page].long(), :, t % page] = b.rows_kv[0][0][:1000]
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G", [(128, 1), (128, 4), (256, 16)])
+@pytest.mark.parametrize("n", [4, 130, 641])
+@pytest.mark.parametrize("shared", [False, True])
+def test_drafted_values_that_are_not_finite(D, G, n, shared):
+    """An infinity or a NaN in a drafted token's V reaches the rows that see it, in its channel, and no other; a NaN in its K
+    every channel of those rows."""
+    rows, P = 4, (n - 3) // 2 if shared else 0
+    b = Batch([n, n + 9], [0, 2] if P else [0], [P] if P else [], rows, G, 1, D, 16, torch.bfloat16)
+    page = 16
+    clean = [sdp.fwd_cache16(**b.args())[0].clone()]
+    assert sdp.poll_status() == sdp.SDP_OK
+
+    def at(s, t):
+        return int(b.table[s, t // page]), 0, t % page
+
+    marks = [(0, n - 3, 5, math.inf), (0, n - 2, 100, math.nan), (1, n + 9 - 1, 64, -math.inf), (1, n + 9 - 3, D - 1, math.nan)]
+    for s, t, c, x in marks:
+        b.v[at(s, t)][c] = x
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    want = clean[0].clone()
+    for s, t, c, x in marks:
+        first = t - (b.lens[s] - rows)
+        want[s, first:, :, c] = x
+    same = (o == want) | (o.isnan() & want.isnan())
+    assert same.all(), same.logical_not().nonzero()[:4]
+    # the last token's key: its row alone
+    for s, t, c, x in marks:
+        b.v[at(s, t)][c] = 0.5
+    before = sdp.fwd_cache16(**b.args())
+    b.k[at(0, n - 1)][3] = math.nan
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    assert o[0, -1].isnan().all() and lse[0, -1].isnan().all()
+    assert torch.equal(o[0, :-1], before[0][0, :-1]) and torch.equal(o[1], before[0][1])
+    assert torch.equal(lse[0, :-1], before[1][0, :-1]) and torch.equal(lse[1], before[1][1])
+
+
+def plain_batch(dtype=torch.bfloat16, **kw):
+    a = dict(lens=[500, 300, 420, 290], cu=[0, 3], prefix=[280], rows=1, Hq=8, Hkv=2, D=128, page=32, dtype=dtype)
+    a.update(kw)
+    return Batch(**a)
+
+
+@pytest.mark.gpu
+def test_outputs_workspace_and_strided_tables():
+    b = plain_batch()
+    a = b.args()
+    o, lse = sdp.fwd_cache16(**a)
+    b.check(o, lse)
+    # q without the row dimension; tables that are rows of wider ones
+    wide = torch.full((4, a["block_table"].shape[1] + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :-3] = a["block_table"]
+    pwide = torch.full((1, a["prefix_table"].shape[1] + 5), -1, dtype=torch.int32, device="cuda")
+    pwide[:, :-5] = a["prefix_table"]
+    need = sdp.cache16_workspace_bytes(4, 1, 8, 2, 128, torch.bfloat16, 1)
+    for off in (0, 16):
+        ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")[off:off + need]
+        out, l2 = torch.full_like(o[:, 0], 9), torch.full_like(lse[:, 0], 9)
+        got = sdp.fwd_cache16(**{**a, "q": a["q"][:, 0], "block_table": wide[:, :-3], "prefix_table": pwide[:, :-5]}, out=out, lse=l2,
+                              workspace=ws)
+        assert got[0] is out and got[1] is l2
+        assert torch.equal(out, o[:, 0]) and torch.equal(l2, lse[:, 0])
+    o2, none = sdp.fwd_cache16(**a, return_lse=False)
+    assert none is None and torch.equal(o2, o)
+    # one group of all
+    b = plain_batch(lens=[500, 300, 420], cu=[0, 3])
+    a = b.args()
+    o, lse = sdp.fwd_cache16(**a)
+    a["cu_groups"] = None
+    o2, l2 = sdp.fwd_cache16(**a)
+    assert torch.equal(o, o2) and torch.equal(lse, l2) and sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
+def test_no_sequences():
+    b = plain_batch()
+    a = b.args()
+    o, lse = sdp.fwd_cache16(a["q"][:0], a["cache"], a["cache_lens"][:0], a["block_table"][:0])
+    assert o.shape == (0, 1, 8, 128) and lse.shape == (0, 1, 8)
+
+
+@pytest.mark.gpu
+def test_bad_lengths_groups_and_pages_are_reported():
+    b = plain_batch()
+    for key, at, x in (("cache_lens", 1, -1), ("cache_lens", 1, 32 * b.table.shape[1] + 1), ("cache_lens", 1, -2 ** 31),
+                       ("cache_lens", 1, 2 ** 31 - 1)):
+        a = b.args()
+        a[key][at] = x
+        out, lse = torch.full_like(a["q"], 3), torch.full(a["q"].shape[:3], 3.0, device="cuda")
+        sdp.fwd_cache16(**a, out=out, lse=lse)
+        assert sdp.poll_status() == sdp.SDP_ERR_BAD_SEQLENS
+        assert (out[1] == 3).all() and (lse[1] == 3).all()  # as they were; the others are right
+        b.check(out, lse, only=(0, 2, 3))
+    full = plain_batch(own_pages=(0, 1, 2))  # every sequence's own pages are complete
+    for key, at, x in (("prefix_lens", 0, -5), ("prefix_lens", 0, 32 * b.prefix_table.shape[1] + 1), ("cu_groups", 1, 5),
+                       ("cu_groups", 0, -1), ("cu_groups", 0, 4)):
+        a = full.args()
+        a[key][at] = x
+        o, lse = sdp.fwd_cache16(**a)
+        assert sdp.poll_status() == sdp.SDP_ERR_BAD_SEQLENS
+        full.check(o, lse)  # what is not shared is read from their own
+    for key, at, x in (("block_table", (3, 2), -1), ("block_table", (0, 9), 1 << 30), ("prefix_table", (0, 1), 2 ** 31 - 1)):
+        a = b.args()
+        a[key][at] = x
+        o, lse = sdp.fwd_cache16(**a)
+        assert sdp.poll_status() == sdp.SDP_ERR_BAD_PAGES
+        b.check(o, lse, only={"prefix_table": (3,)}.get(key, tuple(s for s in range(4) if s != at[0])))
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+def test_refusals_of_the_binding():
+    b = plain_batch()
+    good = b.args()
+    q, c = good["q"], good["cache"]
+    for kw in (dict(q=q.half()), dict(q=q.float()), dict(q=q[..., :64]), dict(q=q.cpu()), dict(q=q[0]), dict(q=q.transpose(0, 1)),
+               dict(q=q.repeat(1, 40, 1, 1)), dict(q=torch.zeros(4, 1, 7, 128, device="cuda", dtype=q.dtype)),
+               dict(cache=(c.k,)), dict(cache=sdp.Cache16(c.k, c.v.half())), dict(cache=sdp.Cache16(c.k, c.v[:, :, :16])),
+               dict(cache_lens=good["cache_lens"].long()), dict(cache_lens=good["cache_lens"][:2]),
+               dict(block_table=good["block_table"].long()), dict(block_table=good["block_table"][:2]),
+               dict(block_table=good["block_table"].t()), dict(prefix_lens=None), dict(prefix_table=None),
+               dict(prefix_lens=good["prefix_lens"].long()), dict(prefix_lens=good["prefix_lens"].repeat(2)),
+               dict(cu_groups=good["cu_groups"][:1]), dict(cu_groups=good["cu_groups"].long()), dict(scale=math.nan),
+               dict(out=q.half()), dict(out=q[:2]), dict(lse=torch.zeros(4, 8, device="cuda")), dict(stream="x"),
+               dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")), dict(q=q.clone().requires_grad_())):
+        with pytest.raises((ValueError, sdp.SdpError)):
+            sdp.fwd_cache16(**{**good, **kw})
+    torch.cuda.synchronize()
+    assert sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_the_same_bits_each_time(D):
+    b = plain_batch(lens=[3000, 2500, 2900, 100], prefix=[2400], rows=2, D=D)
+    a = b.args()
+    o, lse = sdp.fwd_cache16(**a)
+    load = torch.randn(4096, 4096, device="cuda")
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        with torch.cuda.stream(side):  # SMs that are taken for a while
+            load = torch.tanh(load @ load)
+        o2, l2 = sdp.fwd_cache16(**a)
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    assert sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
+def test_streams_and_two_graphs_at_once():
+    bs = [plain_batch(seed=s, lens=[1500, 1300, 1420, 900 + s], prefix=[1280]) for s in range(2)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    graphs, outs = [], []
+    for b, st in zip(bs, streams):
+        a = b.args()
+        torch.cuda.synchronize()
+        ws = torch.empty(sdp.cache16_workspace_bytes(4, 1, 8, 2, 128, torch.bfloat16, 1), dtype=torch.uint8, device="cuda")
+        want = sdp.fwd_cache16(**a, stream=st)
+        st.synchronize()
+        b.check(*want)
+        out, lse = torch.zeros_like(a["q"]), torch.zeros(4, 1, 8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            sdp.fwd_cache16(**a, out=out, lse=lse, workspace=ws)
+        graphs.append((g, a, ws))
+        outs.append((out, lse, want))
+    for _ in range(20):
+        for (g, _, _), st, (out, lse, _) in zip(graphs, streams, outs):
+            with torch.cuda.stream(st):
+                out.zero_()
+                lse.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    assert sdp.poll_status() == sdp.SDP_OK
+    for out, lse, want in outs:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_waits_that_run_out(D):
+    """No copy is issued: every wait gives up after its limit, the status says so, and the next call is right."""
+    b = plain_batch(D=D)
+    a = b.args()
+    want = sdp.fwd_cache16(**a)
+    assert sdp.poll_status() == sdp.SDP_OK
+    old = sdp.set_wait_timeout_ms(20)
+    sdp.set_debug_flags(1)
+    try:
+        sdp.fwd_cache16(**a)
+        assert sdp.poll_status() == sdp.SDP_ERR_DEVICE_TIMEOUT
+    finally:
+        sdp.set_debug_flags(0)
+        sdp.set_wait_timeout_ms(old)
+    o, lse = sdp.fwd_cache16(**a)
+    assert sdp.poll_status() == sdp.SDP_OK and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+def test_rows_past_32_bits_of_the_pool():
+    """Pages whose first element lies beyond 2^32: written there and read there."""
+    Hkv, page, D, n = 8, 128, 128, 300
+    pages = (1 << 32) // (Hkv * page * D) + 40
+    cache = sdp.Cache16(*(torch.empty(pages, Hkv, page, D, dtype=torch.float16, device="cuda") for _ in range(2)))
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(2 * n, Hkv, D, generator=g).half() for _ in range(2))
+    table = torch.tensor([[pages - 1, pages - 30, pages - 7], [pages - 2, 0, pages - 9]], dtype=torch.int32)
+    lens = torch.tensor([n, n], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n, 2 * n], dtype=torch.int32, device="cuda")
+    sdp.cache16_append(cache, k.cuda(), v.cuda(), cu, lens, table.cuda())
+    b = Batch([n, n], [0], [], 1, 8, Hkv, D, page, torch.float16)
+    b.rows_kv = [(k[:n], v[:n]), (k[n:], v[n:])]
+    o, lse = sdp.fwd_cache16(b.q.cuda(), cache, lens, table.cuda())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("rows,D", [(1, 128), (3, 256)])
+def test_a_captured_decoding_loop(dt, rows, D):
+    """Prompts are appended once for the group and once a sequence; then one captured step appends each sequence's next tokens
+    and attends over all of them, replayed while lengths grow. Every step against 64 bits, from what the cache holds."""
+    dtype, Hq, Hkv, page, P, steps = DTYPES[dt], 8, 2, 16, 75, 9
+    starts = [75, 83, 90, 75]
+    nseq, most = len(starts), max(starts) + rows * steps
+    g = torch.Generator().manual_seed(D + rows)
+    per = -(-most // page)
+    prefix_pages = -(-P // page)
+    pool = nseq * per + prefix_pages
+    order = torch.randperm(pool, generator=g).int()
+    prefix_table = order[:prefix_pages][None].cuda()
+    table = order[prefix_pages:].view(nseq, per).clone()
+    table[:, :P // page] = order[:P // page]  # the prefix's full pages; the one that it ends in is each sequence's own
+    table = table.cuda()
+    cache = sdp.cache16_empty(pool, Hkv, D, page, dtype)
+    rope = sdp.rope_table(sdp.rope_inv_freq(64), device="cuda")
+    w = (1 + 0.1 * torch.randn(D, generator=g)).to(dtype).cuda()
+
+    def i32(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    def fused(tokens):
+        return torch.randn(tokens, Hq + 2 * Hkv, D, generator=g).to(dtype).cuda()
+
+    def parts(x):
+        return dict(k=x[:, Hq:Hq + Hkv], v=x[:, Hq + Hkv:])
+
+    prompt = fused(P)
+    sdp.cache16_append(cache, **parts(prompt), cu_seqlens=i32([0, P]), cache_lens=i32([P]), block_table=prefix_table, rope=rope, k_weight=w)
+    own = [n - P for n in starts]
+    rest = fused(sum(own))
+    cu = i32([0, *torch.tensor(own).cumsum(0).tolist()])
+    sdp.cache16_append(cache, **parts(rest), cu_seqlens=cu, cache_lens=i32(starts), block_table=table, rope=rope, k_weight=w)
+
+    lens, x = i32(starts), fused(nseq * rows)
+    cu_new = torch.arange(0, nseq * rows + 1, rows, dtype=torch.int32, device="cuda")
+    plens = i32([P])
+    out = torch.zeros(nseq, rows, Hq, D, dtype=dtype, device="cuda")
+    lse = torch.zeros(nseq, rows, Hq, device="cuda")
+    q_out = torch.zeros(nseq * rows, Hq, D, dtype=dtype, device="cuda")
+    ws = torch.empty(sdp.cache16_workspace_bytes(nseq, rows, Hq, Hkv, D, dtype, 1), dtype=torch.uint8, device="cuda")
+
+    def step():
+        lens.add_(rows)
+        sdp.cache16_append(cache, **parts(x), cu_seqlens=cu_new, cache_lens=lens, block_table=table, rope=rope, q=x[:, :Hq], q_weight=w,
+                           k_weight=w, q_out=q_out)
+        sdp.fwd_cache16(q_out.view(nseq, rows, Hq, D), cache, lens, table, prefix_table, plens, out=out, lse=lse, workspace=ws)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step()
+    b = Batch([1] * nseq, [0], [], rows, Hq, Hkv, D, page, dtype)
+    for i in range(steps):
+        x.copy_(fused(nseq * rows))
+        graph.replay()
+        assert sdp.poll_status() == sdp.SDP_OK
+        b.lens = [n + rows * (i + 1) for n in starts]
+        assert lens.tolist() == b.lens
+        b.q = q_out.view(nseq, rows, Hq, D).cpu()
+        b.rows_kv = []
+        for s, n in enumerate(b.lens):
+            t = torch.arange(n)
+            ids = torch.where(t < P, prefix_table[0].cpu().long()[(t // page).clamp(max=prefix_pages - 1)], table[s].cpu().long()[t // page])
+            b.rows_kv.append((cache.k.cpu()[ids, :, t % page], cache.v.cpu()[ids, :, t % page]))
+            # the newest values are there as they came
+            assert torch.equal(b.rows_kv[s][1][n - rows:], x[s * rows:(s + 1) * rows, Hq + Hkv:].cpu())
+        b.check(out, lse)
