@@ -173,29 +173,31 @@ __device__ __forceinline__ Span span_of(const Cache16Params &p, int e)
     return r;
 }
 
-template <int D>
-__device__ __forceinline__ long long entry_length(const Span &s)
-{
-    return s.tiles > 0 ? static_cast<long long>(s.problems) * (s.tiles + OVERHEAD<D>) : 0;
-}
+// The host keeps the positions of all entries, and so an entry's, in 31 bits. (Offsets of groups that are not in order could
+// pass that all the same: sums stop there.)
+constexpr unsigned MOST = 0x7fffffffu;
 
-// (Out of line: some 130 instructions.)
-static __device__ __noinline__ long long quotient(long long a, long long b) { return a / b; }
+template <int D>
+__device__ __forceinline__ unsigned entry_length(const Span &s)
+{
+    return s.tiles > 0 ? static_cast<unsigned>(s.problems) * static_cast<unsigned>(s.tiles + OVERHEAD<D>) : 0u;
+}
 
 // Positions cut into n runs: run i begins at floor(total * i / n).
 struct Cut {
-    long long total, q;
-    int r, n;
-    __device__ __forceinline__ Cut(long long positions, int most) : total(positions)
+    unsigned total, q, r, n;
+    __device__ __forceinline__ Cut(unsigned positions, unsigned most) : total(positions)
     {
-        n = total < most ? static_cast<int>(total) : most;
-        const int d = max(n, 1);
-        // (a 64-bit division takes a few hundred cycles of a launch's first microseconds)
-        q = total <= 0xffffffffll ? static_cast<uint32_t>(total) / static_cast<uint32_t>(d) : quotient(total, d);
-        r = static_cast<int>(total - q * d);
+        n = min(total, most);
+        q = total / max(n, 1u);
+        r = total - q * n;
     }
-    __device__ __forceinline__ long long start(int i) const { return i * q + i * r / n; }
-    __device__ __forceinline__ int run_of(long long x) const { return static_cast<int>(quotient((x + 1) * n - 1, total)); }
+    __device__ __forceinline__ unsigned start(unsigned i) const { return i * q + i * r / n; }
+    // The run of position x. (Once a problem that several runs share, out of a tile's way.)
+    __device__ __forceinline__ int run_of(unsigned x) const
+    {
+        return static_cast<int>((static_cast<unsigned long long>(x + 1) * n - 1) / total);
+    }
 };
 
 constexpr int DEST_DIRECT = -1, DEST_ROWS = -2;  // else the part's number
@@ -214,17 +216,29 @@ struct __align__(16) Unit {
     __device__ __forceinline__ bool prefix() const { return table < 0; }
 };
 
+// The sum of the lanes up to one's own, MOST at most.
+__device__ __forceinline__ unsigned sum_to_lane(unsigned x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned y = __shfl_up_sync(FULL, x, d);
+        x = min(x + (lane >= d ? y : 0u), MOST);
+    }
+    return x;
+}
+
 // The runs, as a CTA sees them: `begin` by all threads of the CTA, `start` and `next` by one warp.
 template <int D, int THREADS>
 struct Runs {
     // what `begin` leaves in shared memory (where the copies' ring is later, but for `start` to have read it)
     struct Shared {
-        long long prefix[THREADS], sum[THREADS / 32];
+        unsigned prefix[THREADS], sum[THREADS / 32];
         Span first[THREADS];  // thread e's first entry, where that is e
     };
     int entries, per;
     Cut cut{0, 1};
-    long long upto;  // lane w: the entries' lengths before warp w's
+    unsigned upto;  // lane w: the entries' lengths before warp w's
 
     // The lengths of all entries, summed up: each thread has some consecutive ones. Ends with __syncthreads().
     __device__ __forceinline__ void begin(const Cache16Params &p, Shared &sh)
@@ -233,57 +247,44 @@ struct Runs {
         entries = p.ngroups + p.nseq;
         per = (entries + THREADS - 1) / THREADS;
         const int e0 = min(entries, tid * per), e1 = min(entries, e0 + per);
-        long long sum = 0;
+        unsigned sum = 0;
 #pragma unroll 1
         for (int e = e0; e < e1; ++e) {
             const Span s = span_of(p, e);
             if (e == tid)
                 sh.first[e] = s;
-            sum += entry_length<D>(s);
+            sum = min(sum + entry_length<D>(s), MOST);
             if (s.bad && e < p.ngroups && blockIdx.x == 0)
                 atomicCAS(p.status, 0u, kBadSeqlens);
         }
-        long long incl = sum;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long x = __shfl_up_sync(FULL, incl, d);
-            if (lane >= d)
-                incl += x;
-        }
+        const unsigned incl = sum_to_lane(sum);
         sh.prefix[tid] = incl - sum;  // within the warp
         if (lane == 31)
             sh.sum[tid >> 5] = incl;
         __syncthreads();
         // the warps' sums, a lane each
-        const long long of_warp = lane < THREADS / 32 ? sh.sum[lane] : 0;
-        upto = of_warp;
-#pragma unroll
-        for (int d = 1; d < THREADS / 32; d <<= 1) {
-            const long long x = __shfl_up_sync(FULL, upto, d);
-            if (lane >= d)
-                upto += x;
-        }
-        cut = Cut(__shfl_sync(FULL, upto, THREADS / 32 - 1), p.sms);
-        upto -= of_warp;
+        const unsigned of_warp = lane < THREADS / 32 ? sh.sum[lane] : 0u;
+        const unsigned all = sum_to_lane(of_warp);
+        cut = Cut(__shfl_sync(FULL, all, 31), p.sms);
+        upto = all - of_warp;
     }
 
     // The walk over run `run`, problem by problem, by a whole warp.
-    int left;         // positions left in the run (a run of 2^31 tiles would take half an hour)
+    int left;         // positions left in the run
     int e, base;      // entry; the lanes have entries base .. base + 31
-    long long skip;   // positions of entry e before the run
+    unsigned skip;    // positions of entry e before the run
     Span mine, at;    // the lane's entry; entry e
     int in, b, block, heads, hb, kv;  // position in the problem; its block, KV head and block of heads, and both as one
 
     __device__ __forceinline__ void start(const Cache16Params &p, const Shared &sh)
     {
         const int lane = threadIdx.x & 31;
-        const int run = static_cast<int>(blockIdx.x);
-        const int over = run * cut.r / cut.n;  // (start(run), and start(run + 1) with no division of its own)
-        const long long x = run * cut.q + over;
-        left = static_cast<int>(cut.q) + (run * cut.r - over * cut.n + cut.r >= cut.n ? 1 : 0);
+        const unsigned run = blockIdx.x, over = run * cut.r / cut.n;  // (start(run); start(run + 1) needs no division of its own)
+        const unsigned x = run * cut.q + over;
+        left = static_cast<int>(cut.q + (run * cut.r - over * cut.n + cut.r >= cut.n ? 1u : 0u));
         // the last warp, and the last thread of it, whose entries start at or before x
         const int w0 = 31 - __clz(__ballot_sync(FULL, lane < THREADS / 32 && upto <= x));
-        const long long before = __shfl_sync(FULL, upto, w0);
+        const unsigned before = __shfl_sync(FULL, upto, w0);
         const unsigned hit = __ballot_sync(FULL, before + sh.prefix[w0 * 32 + lane] <= x);
         const int owner = w0 * 32 + 31 - __clz(hit);
         skip = x - before - sh.prefix[owner];
@@ -322,19 +323,24 @@ struct Runs {
                 kv = heads = b = hb = in = 0;
                 block = e < p.ngroups ? p.toks_p : p.toks_o;
                 if (skip > 0) {  // the run's first problem
-                    const long long all = static_cast<long long>(len) * (at.blocks * p.Hkv * p.head_blocks);
+                    const unsigned all = static_cast<unsigned>(len) * static_cast<unsigned>(at.blocks * p.Hkv * p.head_blocks);
                     if (skip >= all) {
                         skip -= all;
                         kv = p.Hkv;
                         continue;
                     }
-                    const int first = skip <= 0x7fffffffll ? static_cast<int>(skip) / len : static_cast<int>(quotient(skip, len));
-                    in = static_cast<int>(skip - static_cast<long long>(first) * len);
+                    kv = heads = static_cast<int>(skip) / len;
+                    in = static_cast<int>(skip) - heads * len;
                     skip = 0;
-                    heads = first / at.blocks;
-                    b = first - heads * at.blocks;
-                    kv = heads / p.head_blocks;
-                    hb = heads - kv * p.head_blocks;
+                    if (at.blocks > 1) {
+                        const int first = heads;
+                        kv = heads = first / at.blocks;
+                        b = first - heads * at.blocks;
+                    }
+                    if (p.head_blocks > 1) {
+                        kv = heads / p.head_blocks;
+                        hb = heads - kv * p.head_blocks;
+                    }
                 }
             }
             // the problem's positions [in, in + take)

@@ -19,7 +19,8 @@ struct Shape {
 // Sections of the workspace begin on 32 bytes of it, after at most 16 bytes that its own start lacks.
 long long align32(long long x) { return (x + 31) / 32 * 32; }
 
-int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups, Shape *sh)
+// keys, prefix_keys: the most that a sequence's table and a prefix's can hold.
+int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups, long long keys, long long prefix_keys, Shape *sh)
 {
     if (dtype != SDP_FP16 && dtype != SDP_BF16)
         return SDP_ERR_UNSUPPORTED;
@@ -42,6 +43,11 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
     sh->blocks_p = (rows + sh->toks_p - 1) / sh->toks_p;
     const int most = ngroups > 0 ? static_cast<int>(std::min<long long>(sh->toks_p, tokens)) : sh->toks_o;
     sh->part_rows = most * sh->heads;
+    // 31 bits for the positions that the work is cut by, whatever the lengths: tiles, and what the problems' ends count
+    auto positions = [](long long k) { return static_cast<double>(k / sdp::c16::TILE + 1 + sdp::c16::OVERHEAD<128>); };
+    const double own_blocks = static_cast<double>(nseq) * sh->blocks_o, shared_blocks = static_cast<double>(tokens) / sh->toks_p + ngroups;
+    if ((own_blocks * positions(keys) + (ngroups > 0 ? shared_blocks * positions(prefix_keys) : 0.0)) * Hkv * sh->head_blocks > INT32_MAX)
+        return SDP_ERR_OVERFLOW;
     int dev = 0;
     const int rc = sdp::current_device(&dev, &sh->sms);
     if (rc != SDP_OK)
@@ -64,7 +70,7 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
 extern "C" long long sdp_fwd_cache16_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups)
 {
     Shape sh;
-    const int rc = shape_of(nseq, rows, Hq, Hkv, D, dtype, ngroups, &sh);
+    const int rc = shape_of(nseq, rows, Hq, Hkv, D, dtype, ngroups, 0, 0, &sh);
     return rc != SDP_OK ? rc : sh.bytes;
 }
 
@@ -98,7 +104,8 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
         (ngroups > 0 && static_cast<long long>(prefix_pages) * page_size > INT32_MAX - 256) || num_pages > INT32_MAX / std::max(Hkv, 1))
         return SDP_ERR_OVERFLOW;
     Shape sh;
-    int rc = shape_of(nseq, rows, Hq, Hkv, D, dtype, ngroups, &sh);
+    int rc = shape_of(nseq, rows, Hq, Hkv, D, dtype, ngroups, static_cast<long long>(max_pages) * page_size,
+                      static_cast<long long>(prefix_pages) * page_size, &sh);
     if (rc != SDP_OK)
         return rc;
     if (workspace_bytes < static_cast<unsigned long long>(sh.bytes))

@@ -163,37 +163,20 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     // What follows may be launched: it finds no room beside a CTA of this kernel (its registers and shared memory), so it
     // starts on SMs that have none or whose CTA has ended, and waits there for the last one before it reads.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (threadIdx.x == 0) {
-        for (int b = 0; b < QB; ++b) {
-            ptx::mbar_init(q_full0 + 8u * b, 1);
-            ptx::mbar_init(q_free0 + 8u * b, 1);
+    if (warp == 15) {  // (the first warps have entries to look up)
+        // one arrival each, but for p_full, o_free and sum_free, where four warps arrive, sum_full (eight) and unit_free
+        constexpr int P0 = 2 * QB + 2 * NS + NB, P1 = P0 + 2 * NB, SUM = P1 + O_DONE_RING + 2;
+        for (int i = lane; i < PL::NBARS; i += 32) {
+            const bool four = (i >= P0 && i < P1) || i == SUM || i == SUM + 2;
+            const bool readers = i >= SUM + 4 + PL::UNITS && i < SUM + 4 + 2 * PL::UNITS;  // unit_free: the warps that read it
+            ptx::mbar_init(q_full0 + 8u * i, four ? 4 : i == SUM + 1 ? 8 : readers ? 15 : 1);
         }
-        for (int s = 0; s < NS; ++s) {
-            ptx::mbar_init(slot_full0 + 8u * s, 1);
-            ptx::mbar_init(slot_empty0 + 8u * s, 1);
+        if (lane == 0) {
+            waits->abort = 0;
+            waits->status = p.status;
+            waits->timeout_ns = p.timeout_ns;
         }
-        for (int i = 0; i < NB; ++i) {
-            ptx::mbar_init(s_full0 + 8u * i, 1);
-            ptx::mbar_init(p_full0 + 16u * i, 4);  // one arrival a softmax warp
-            ptx::mbar_init(p_full0 + 16u * i + 8u, 4);
-        }
-        for (int i = 0; i < O_DONE_RING; ++i)
-            ptx::mbar_init(o_done0 + 8u * i, 1);
-        ptx::mbar_init(final0, 1);
-        ptx::mbar_init(final0 + 8u, 1);
-        ptx::mbar_init(o_free, 4);
-        ptx::mbar_init(sum_full, 8);
-        ptx::mbar_init(sum_free, 4);
-        ptx::mbar_init(odd_full, 1);
-        for (int i = 0; i < PL::UNITS; ++i) {
-            ptx::mbar_init(unit_full0 + 8u * i, 1);
-            ptx::mbar_init(unit_free0 + 8u * i, 15);  // the warps that read it
-        }
-        for (int i = 0; i < 8; ++i)
-            ptx::mbar_init(max_full0 + 8u * i, 1);
-        waits->abort = 0;
-        waits->status = p.status;
-        waits->timeout_ns = p.timeout_ns;
+        __syncwarp();
         ptx::fence_barrier_init();
     }
     if (warp == 4 && lane == 0) {
@@ -213,7 +196,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     runs.begin(p, sums);
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    if (run >= runs.cut.n) {  // nothing left for this one
+    if (blockIdx.x >= runs.cut.n) {  // nothing left for this one
         if (warp == 5)
             ptx::tmem_dealloc(tmem, L::TMEM_COLS);
         return;

@@ -60,6 +60,7 @@ def c_call(**kw):
     (dict(pp=1 << 27), sdp.SDP_ERR_OVERFLOW),
     (dict(P=1 << 30, Hkv=8), sdp.SDP_ERR_OVERFLOW),
     (dict(nseq=1 << 29), sdp.SDP_ERR_OVERFLOW),
+    (dict(nseq=1 << 20, mp=1 << 20, ng=0), sdp.SDP_ERR_OVERFLOW),  # tiles of all problems
 ])
 def test_c_call_refuses_before_any_launch(kw, code):
     from gqa_flash_attention_gb300 import build, serving
