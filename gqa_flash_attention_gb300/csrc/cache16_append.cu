@@ -13,8 +13,16 @@ template <int D, bool BF16>
 cudaError_t launch(const RopeParams &p, const CacheDest &c, bool w32, bool interleaved, unsigned blocks, cudaStream_t st)
 {
     auto go = [&](auto kern) {
-        kern<<<blocks, 32 * kWarps, 0, st>>>(p, c);
-        return cudaGetLastError();
+        cudaLaunchAttribute early{};
+        early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        early.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t config{};
+        config.gridDim = dim3(blocks);
+        config.blockDim = dim3(32 * kWarps);
+        config.stream = st;
+        config.attrs = &early;
+        config.numAttrs = 1;
+        return cudaLaunchKernelEx(&config, kern, p, c);
     };
     if (w32)
         return interleaved ? go(qk_norm_rope_kernel<D, BF16, true, false, true, true>)

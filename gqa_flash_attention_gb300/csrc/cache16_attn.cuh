@@ -36,9 +36,9 @@
 // Two tiles at a time of queries that share a tile of K and V (CTA pairs) would halve the copies; one tile's O and S buffers
 // fill tensor memory at D = 256.
 //
-// 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 49 us, where HBM alone takes 24;
-// 256 behind 16384, 32 heads over 2, D = 256: 137 us, where the tensor cores alone take 72; eight of 16384 tokens that share
-// nothing, D = 256: 55.5 us (4.9 TB/s), where HBM takes 40. A launch needs some 10000 cycles (5 us) before its first copy
+// 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 48 us, where HBM alone takes 24;
+// 256 behind 16384, 32 heads over 2, D = 256: 134 us, where the tensor cores alone take 72; eight of 16384 tokens that share
+// nothing, D = 256: 53 us (5.0 TB/s), where HBM takes 40. A launch needs some 10000 cycles (5 us) before its first copy
 // and the join 4 to 8 us after the last tile.
 //
 // Keys outside [lo, hi) of a problem share its first and last tiles. Their scores are replaced before any arithmetic, whatever
@@ -160,9 +160,6 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     const int lane = threadIdx.x & 31;
     const int run = static_cast<int>(blockIdx.x);
 
-    // What follows may be launched: it finds no room beside a CTA of this kernel (its registers and shared memory), so it
-    // starts on SMs that have none or whose CTA has ended, and waits there for the last one before it reads.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 15) {  // (the first warps have entries to look up)
         // one arrival each, but for p_full, o_free and sum_free, where four warps arrive, sum_full (eight) and unit_free
         constexpr int P0 = 2 * QB + 2 * NS + NB, P1 = P0 + 2 * NB, SUM = P1 + O_DONE_RING + 2;
@@ -189,6 +186,11 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         ptx::tmem_alloc(ptx::smem_addr(tmem_holder), L::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    // Up to here the CTA has run beside the end of what is before it on the stream (the append, or another call's join, which let
+    // it start). What follows may be launched from here on, as its own first reads are of what was there for this kernel; it
+    // finds no room beside a CTA, so it starts where there is none or it has ended, and waits there for the last one.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     using R = Runs<D, THREADS>;
     typename R::Shared &sums = *reinterpret_cast<typename R::Shared *>(smem + PL::RING_OFF);
     R runs;
@@ -712,30 +714,30 @@ cudaError_t launch_cache16_attn(const Cache16Maps &m, const Cache16Params &p, cu
     const cudaError_t e = set_smem_once(cache16_attn_kernel<D, BF16>, PL::SMEM_BYTES, done);
     if (e != cudaSuccess)
         return e;
-    // The blocks of the join start where the attention's CTAs end, not when the last one has.
+    // Both start where CTAs of the kernel before them end (if that one lets them), not when the last one has.
     cudaLaunchAttribute early{};
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
-    auto launch = [&](auto kern, unsigned grid, int threads, int bytes, bool follows, const auto &...args) {
+    auto launch = [&](auto kern, unsigned grid, int threads, int bytes, const auto &...args) {
         cudaLaunchConfig_t config{};
         config.gridDim = dim3(grid);
         config.blockDim = dim3(threads);
         config.dynamicSmemBytes = bytes;
         config.stream = st;
         config.attrs = &early;
-        config.numAttrs = follows ? 1 : 0;
+        config.numAttrs = 1;
         return cudaLaunchKernelEx(&config, kern, args...);
     };
     const cudaError_t f =
-        launch(cache16_attn_kernel<D, BF16>, p.sms, c16::THREADS, PL::SMEM_BYTES, false, m.q_prefix, m.q_own, m.k, m.v, p);
+        launch(cache16_attn_kernel<D, BF16>, p.sms, c16::THREADS, PL::SMEM_BYTES, m.q_prefix, m.q_own, m.k, m.v, p);
     if (f != cudaSuccess)
         return f;
     const unsigned rows = static_cast<unsigned>(p.nseq * p.n * p.Hq);
     constexpr int WARPS = c16::JOIN_THREADS / 32;
     // a row a warp once that still gives every SM two blocks
     return rows >= 2u * p.sms * WARPS
-               ? launch(cache16_join_kernel<D, BF16, 1>, (rows + WARPS - 1) / WARPS, c16::JOIN_THREADS, 0, true, p)
-               : launch(cache16_join_kernel<D, BF16, WARPS>, rows, c16::JOIN_THREADS, 0, true, p);
+               ? launch(cache16_join_kernel<D, BF16, 1>, (rows + WARPS - 1) / WARPS, c16::JOIN_THREADS, 0, p)
+               : launch(cache16_join_kernel<D, BF16, WARPS>, rows, c16::JOIN_THREADS, 0, p);
 }
 
 // One per (head dim, dtype).

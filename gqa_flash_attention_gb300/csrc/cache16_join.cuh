@@ -29,6 +29,8 @@ __global__ void __launch_bounds__(c16::JOIN_THREADS) cache16_join_kernel(const _
     using namespace c16;
     constexpr int V = D / 128;  // float4 a lane
     __shared__ float4 y_all[SHARE][32 * V];
+    // (what is launched early by this reads nothing before this kernel has ended)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int all = p.nseq * p.n * p.Hq;
     const int row = SHARE == 1 ? blockIdx.x * (JOIN_THREADS / 32) + warp : blockIdx.x;

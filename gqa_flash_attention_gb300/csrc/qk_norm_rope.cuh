@@ -145,6 +145,10 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     constexpr int LPR = D / 8;     // lanes a row
     constexpr int RPP = 32 / LPR;  // rows a pass
     __shared__ float2 cs_all[kWarps][D / 2];
+    if constexpr (CACHE) {  // launched while the kernel before it ends; the attention over the cache may be likewise
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int runs = (p.passes + p.per_warp - 1) / p.per_warp;
     const long long item = static_cast<long long>(blockIdx.x) * kWarps + warp;

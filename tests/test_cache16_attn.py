@@ -563,3 +563,43 @@ def test_a_captured_decoding_loop(dt, rows, D):
             # the newest values are there as they came
             assert torch.equal(b.rows_kv[s][1][n - rows:], x[s * rows:(s + 1) * rows, Hq + Hkv:].cpu())
         b.check(out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_steps_that_follow_each_other_at_once(D):
+    """Appends and attentions with nothing else between them, so that each is launched while the one before it ends, with one
+    workspace for all: the bits of the same steps with a wait after each call."""
+    Hq, Hkv, page, P, steps, dtype = 8, 2, 32, 400, 24, torch.bfloat16
+    starts = [400, 640, 401, 1500]
+    g = torch.Generator().manual_seed(D)
+    per = -(-(max(starts) + steps) // page)
+    table = torch.randperm(4 * per, generator=g).int().view(4, per)
+    table[:, :P // page] = table[0, :P // page]
+    ptable = table[:1, :-(-P // page)].contiguous().cuda()
+    table = table.cuda()
+    rope = sdp.rope_table(sdp.rope_inv_freq(D), device="cuda")
+    first = (torch.randn(2, 4 * per, Hkv, page, D, generator=g) * 0.7).to(dtype).cuda()
+    x = torch.randn(steps, 4, Hq + 2 * Hkv, D, generator=g).to(dtype).cuda()
+    lens = [torch.tensor([n + i + 1 for n in starts], dtype=torch.int32, device="cuda") for i in range(steps)]
+    cu = torch.arange(5, dtype=torch.int32, device="cuda")
+    plens = torch.tensor([P], dtype=torch.int32, device="cuda")
+    ws = torch.empty(sdp.cache16_workspace_bytes(4, 1, Hq, Hkv, D, dtype, 1), dtype=torch.uint8, device="cuda")
+    results = []
+    for wait in (True, False):
+        cache = sdp.Cache16(first[0].clone(), first[1].clone())
+        q = torch.zeros(steps, 4, Hq, D, dtype=dtype, device="cuda")
+        o, lse = torch.zeros_like(q), torch.zeros(steps, 4, Hq, device="cuda")
+        torch.cuda.synchronize()
+        for i in range(steps):
+            sdp.cache16_append(cache, x[i, :, Hq:Hq + Hkv], x[i, :, Hq + Hkv:], cu, lens[i], table, rope=rope, q=x[i, :, :Hq], q_out=q[i])
+            if wait:
+                torch.cuda.synchronize()
+            sdp.fwd_cache16(q[i], cache, lens[i], table, ptable, plens, out=o[i], lse=lse[i], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        assert sdp.poll_status() == sdp.SDP_OK
+        results.append((q, o, lse, cache.k, cache.v))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert not results[0][1].isnan().any()
