@@ -609,6 +609,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             arrive(sum_full);
             g0 += n;
         }
+        ptx::tmem_wait_ld();  // (where a wait ran out)
     } else {
         // --------------------------------------- rows' ends: O over l, to the output or to the workspace
         const int w4 = warp & 3, row = w4 * 32 + lane;
