@@ -29,6 +29,11 @@
 // in flight; the token's R/2 cosines and sines are computed once for the run, spread over the lanes,
 // and read back from shared memory. 39253 tokens of 34 heads at D = 256 take 233 us, 86 % of the copy
 // rate. (With the weights applied and fp32 values shuffled row by row they took 348 us.)
+//
+// Appending (34332 tokens of 36 heads at D = 256: 219 us, 85 % of the copy rate; 3095 of 96 heads at D = 128: 32 us, 69 %) adds
+// the look-up of a token's place, whose trips to memory run beside the first rows' loads, the position's and the
+// frequencies' (one after the other, 34.4 us for the second). Rows loaded one at a time, as they are consumed, instead of
+// kPassUnroll at once: 275 us for the first.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -92,49 +97,58 @@ __device__ __forceinline__ void load_weights(const void *base, int c0, float (&w
     }
 }
 
-// A row's destination in the cache: its place in head 0's rows of the pool ([pages * Hkv * page_size] rows), and whether
-// that is to be written.
+// Where a token goes in the cache.
 struct Place {
-    long long row;
     int position;  // in its sequence; -1: the token is in no sequence (or in a bad one)
+    int id, at;    // the page, as the table has it, and the place in it
 };
 
-// Where `token` goes. Called by a whole warp: its sequence is searched by all lanes together, 32 candidates a step (two
-// trips to memory for 1024 sequences). Status codes for bad offsets and lengths, and for pages outside the pool.
+// Where `token` goes. Called by a whole warp: its sequence is searched by all lanes together, 32 candidates a step, and what
+// belongs to the last 31 comes in the same trip to memory. (A short call's time is its chain of such trips: this one, the
+// table's, and then the rows' way out.) Status codes for bad offsets and lengths.
 __device__ __forceinline__ Place locate(const CacheDest &c, int token, int tokens)
 {
     const int lane = threadIdx.x & 31;
-    int lo = 0;
-    for (int len = c.nseq; len > 1;) {  // the last sequence that begins at or before the token lies in [lo, lo + len)
-        const int step = (len + 31) / 32;
-        const bool before = lane * step < len && __ldg(c.cu + lo + lane * step) <= token;
+    int lo = 0, n = c.nseq;  // the last sequence that begins at or before the token lies in [lo, lo + n)
+    while (n > 31) {
+        const int step = (n + 31) / 32;
+        const bool before = lane * step < n && __ldg(c.cu + lo + lane * step) <= token;
         const unsigned m = __ballot_sync(FULL, before);
         const int used = m == 0u ? 0 : (31 - __clz(m)) * step;
         lo += used;
-        len = min(step, len - used);
+        n = min(step, n - used);
     }
-    Place r{-1, -1};
-    const int first = __ldg(c.cu + lo), end = __ldg(c.cu + lo + 1), len = __ldg(c.lens + lo);
+    const int mine = __ldg(c.cu + lo + min(lane, n)), my_len = __ldg(c.lens + lo + min(lane, n - 1));
+    const unsigned m = __ballot_sync(FULL, lane < n && mine <= token);
+    const int used = m == 0u ? 0 : 31 - __clz(m);
+    const int first = __shfl_sync(FULL, mine, used), end = __shfl_sync(FULL, mine, used + 1);
+    const int len = __shfl_sync(FULL, my_len, used);
+    Place r{-1, -1, 0};
     if (token < first || token >= end)
         return r;  // in no sequence: left as it is
-    const int slots = c.max_pages;
     const bool ok = first >= 0 && end <= tokens && len >= end - first;
     const int place = ok ? token - first + (len - (end - first)) : 0;  // below len
     const int slot = place / c.page_size;
-    if (!ok || slot >= slots) {
+    if (!ok || slot >= c.max_pages) {
         if (lane == 0)
             atomicCAS(c.status, 0u, kBadSeqlens);
         return r;
     }
     r.position = place;
-    const int id = __ldg(c.table + lo * c.table_stride + slot);
-    if (id < 0 || id >= c.num_pages) {
-        if (lane == 0)
-            atomicCAS(c.status, 0u, kBadPages);
-        return r;
-    }
-    r.row = static_cast<long long>(id) * c.Hkv * c.page_size + (place - slot * c.page_size);
+    r.id = __ldg(c.table + (lo + used) * c.table_stride + slot);  // (looked at by `row_of`: the angles are computed meanwhile)
+    r.at = place - slot * c.page_size;
     return r;
+}
+
+// Its place in head 0's rows of the pool ([pages * Hkv * page_size] rows), or -1 and a status code where the page is outside.
+__device__ __forceinline__ long long row_of(const CacheDest &c, const Place &p)
+{
+    if (p.id < 0 || p.id >= c.num_pages) {
+        if ((threadIdx.x & 31) == 0)
+            atomicCAS(c.status, 0u, kBadPages);
+        return -1;
+    }
+    return static_cast<long long>(p.id) * c.Hkv * c.page_size + p.at;
 }
 
 // CACHE: k's rows go to their pages, v's are copied to theirs (a third segment of a token's passes), and a token's
@@ -201,7 +215,21 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
         open(q_first);
     else
         open_v();
-    Place place{0, 0};
+    // and so do those of the frequencies (as many as half of the shorter heads has) and of the position, where it is given
+    const int half = p.R / 2;
+    [[maybe_unused]] const bool turned = half > 0 && (!CACHE || pass0 < c.passes_k);
+    unsigned long long turns[2] = {0, 0};
+    long long given = 0;
+    if (CACHE && turned) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (lane + 32 * x < half)
+                turns[x] = __ldg(p.turns + lane + 32 * x);
+        const long long at = s * p.ps[1];
+        if (p.positions != nullptr)
+            given = c.positions_64 != 0 ? static_cast<const long long *>(p.positions)[at] : static_cast<const int *>(p.positions)[at];
+    }
+    Place place{0, 0, 0};
     if constexpr (CACHE) {
         if (blockIdx.x == 0)  // all offsets: a token of a sequence with bad ones may belong to none
             for (int i = threadIdx.x; i < c.nseq; i += 32 * kWarps) {
@@ -214,15 +242,14 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
             return;
     }
 
-    const int half = p.R / 2;
-    if (half > 0 && (!CACHE || pass0 < c.passes_k)) {
+    if (turned) {
         const long long at = b * p.ps[0] + s * p.ps[1];
-        const bool wide = CACHE ? c.positions_64 != 0 : POS64;
-        const long long pos = CACHE && p.positions == nullptr ? place.position
-                              : wide                         ? static_cast<const long long *>(p.positions)[at]
-                                                             : static_cast<const int *>(p.positions)[at];
+        const long long pos = CACHE ? (p.positions == nullptr ? place.position : given)
+                              : POS64 ? static_cast<const long long *>(p.positions)[at]
+                                      : static_cast<const int *>(p.positions)[at];
         for (int i = lane; i < half; i += 32) {
-            const unsigned long long turn = static_cast<unsigned long long>(pos) * __ldg(p.turns + i);
+            const unsigned long long per = CACHE && i < 64 ? (i < 32 ? turns[0] : turns[1]) : __ldg(p.turns + i);
+            const unsigned long long turn = static_cast<unsigned long long>(pos) * per;
             float sn, c;
             sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 4.656612873077393e-10f, &sn, &c);  // 2^-31
             cs[i] = make_float2(c * p.mscale, sn * p.mscale);
@@ -325,9 +352,10 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
             dst = p.q_out + b * p.qos[0] + s * p.qos[1] + h0 * p.qos[2] + c0;
             dst_step = p.qos[2] * RPP;
         } else if constexpr (CACHE) {
-            dst = c.k + (place.row + static_cast<long long>(h0) * c.page_size) * D + c0;
+            const long long row = row_of(c, place);
+            dst = c.k + (row + static_cast<long long>(h0) * c.page_size) * D + c0;
             dst_step = static_cast<long long>(c.page_size) * D * RPP;
-            if (place.row < 0)
+            if (row < 0)
                 live = 0;  // the page is not there
         } else {
             dst = p.k_out + b * p.kos[0] + s * p.kos[1] + h0 * p.kos[2] + c0;
@@ -400,13 +428,16 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     }
     if constexpr (CACHE) {
         const int passes = pass1 - max(pass0, c.passes_k);
-        if (passes <= 0 || place.row < 0)
+        if (passes <= 0)
+            return;
+        const long long row = row_of(c, place);
+        if (row < 0)
             return;
         if (pass0 < c.passes_k)
             open_v();
         const int h0 = max(0, pass0 - c.passes_k) * RPP + sub;
         int live = min(p.Hkv, (pass1 - c.passes_k) * RPP) - h0;
-        uint16_t *dst = c.v_pool + (place.row + static_cast<long long>(h0) * c.page_size) * D + c0;
+        uint16_t *dst = c.v_pool + (row + static_cast<long long>(h0) * c.page_size) * D + c0;
         const long long dst_step = static_cast<long long>(c.page_size) * D * RPP;
         for (int pass = 0; pass < passes; pass += kPassUnroll) {
             uint4 now[kPassUnroll];
