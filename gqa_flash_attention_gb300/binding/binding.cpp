@@ -525,7 +525,6 @@ PyObject *cache16_append(PyObject *const *a)
     int64_t ps = 0;
     bool wide = false;
     if (positions) {
-        check(a[6] != Py_None, "positions need a rotation");
         check(cuda_index(*positions) == dev && positions->dim() == 1 && positions->size(0) == tokens &&
                   (positions->scalar_type() == at::kInt || positions->scalar_type() == at::kLong),
               "positions must be an int32 or int64 tensor [tokens] on the inputs' device");

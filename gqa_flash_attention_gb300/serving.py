@@ -312,8 +312,9 @@ def cache16_append(cache: Cache16, k: torch.Tensor, v: torch.Tensor, cu_seqlens:
     k, v: [tokens, Hkv, D] and q (or None): [tokens, Hq, D] of the cache's dtype with free token and head strides, as views
     of a fused projection: rows cu_seqlens[i] .. cu_seqlens[i + 1] - 1 become the last tokens of sequence i, as
     cache4_append has them. rope (rope_table's), weights, eps and interleaved are qk_norm_rope's, with its results;
-    positions: int32 or int64 [tokens], by default each token's place in its sequence. Returns q's rows: a contiguous
-    tensor, or q_out, which may be q itself; None without q. Rows in no sequence, and those of bad offsets and
+    positions: int32 or int64 [tokens], by default each token's place in its sequence; without rope nothing is rotated by
+    them (a layer of a model that rotates in others). Returns q's rows: a contiguous tensor, or q_out, which may be q itself;
+    None without q. Rows in no sequence, and those of bad offsets and
     lengths, are left out; those and pages outside the pool show in poll_status(). Enqueued on `stream` (default: the
     current stream), not synchronised.
     """

@@ -362,7 +362,7 @@ int sdp_fwd_cache4(const void *q, const void *k_codes, const void *k_scales, con
  *   k, v        device, dtype [tokens, Hkv, D] likewise
  *   cu_seqlens, cache_lens  as sdp_cache4_append. Rows in no sequence are left out, q's too
  *   positions   device, int32 or (positions_64) int64 at stride p_st: each token's position for the rotation; NULL:
- *               its place in its sequence
+ *               its place in its sequence. Not read where rot_dim is 0
  *   turns, rot_dim (0: no rotation), mscale, q_weight, k_weight (NULL: no norm), weight_fp32, eps, interleaved
  * Bad offsets and lengths (SDP_ERR_BAD_SEQLENS: the sequence's rows are left out) and pages outside the pool
  * (SDP_ERR_BAD_PAGES: k's and v's rows are) are found by the kernel and reported by the next sdp_poll_status. A page that

@@ -238,3 +238,20 @@ def test_append_in_place_and_no_sequences():
     sdp.cache16_append(c, k, v, i32(0), i32(), table[:0])
     empty = sdp.cache16_append(c, k[:0], v[:0], i32(0, 0, 0), lens, table, q=q[:0])
     assert empty.shape == (0, 2, 128) and torch.equal(c.k, before) and sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("norm", [False, True])
+def test_positions_without_a_rotation_change_nothing(norm):
+    """As a model passes them to every layer, of which some rotate nothing."""
+    c, q, k, v, table = small()
+    cu, lens = i32(0, 4, 8), i32(9, 40)
+    w = torch.linspace(0.5, 1.5, 128, device="cuda").half() if norm else None
+    want = sdp.cache16_append(c, k, v, cu, lens, table, q=q, q_weight=w, k_weight=w)
+    before = c.k.clone()
+    for dtype in (torch.int32, torch.int64):
+        c.k.zero_()
+        got = sdp.cache16_append(c, k, v, cu, lens, table, q=q, q_weight=w, k_weight=w,
+                                 positions=torch.arange(1000, 1008, device="cuda", dtype=dtype))
+        assert torch.equal(got, want) and torch.equal(c.k, before)
+    assert sdp.poll_status() == sdp.SDP_OK
