@@ -73,7 +73,7 @@ struct Plan {
     static constexpr int NBARS = 2 * QB + 2 * NS + 3 * L::NSBUF + O_DONE_RING + 2 + 4 + 2 * UNITS + 8;
     static constexpr int RING_OFF = QB * L::Q_BYTES, V_OFF = RING_OFF + NK * K_SLOT;
     static constexpr int BAR_OFF = V_OFF + NV * V_SLOT;
-    static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, -, mask of keys that are not finite, -, Waits
+    static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, -, mask of keys that are not finite, whether O holds anything, Waits
     static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;      // the rows' maxima so far; of a unit, their m and l from the two groups of softmax warps
     static constexpr int UNIT_OFF = SUM_OFF + 4 * TILE * 4;
     static constexpr int SMEM_BYTES = UNIT_OFF + UNITS * static_cast<int>(sizeof(Unit));
@@ -83,11 +83,19 @@ struct Plan {
     static_assert(sizeof(typename Runs<D, THREADS>::Shared) <= BAR_OFF - RING_OFF, "the sums of the problems' lengths");
 };
 
-// Eight words to a 32-byte boundary: a whole sector of a row.
-__device__ __forceinline__ void st_global_v8(void *at, const uint32_t *w)
+// Eight words to a 32-byte boundary, a whole sector of a row, if `live`.
+__device__ __forceinline__ void st_global_v8(void *at, const uint32_t *w, uint32_t live)
 {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %9, 0;\n\t@p st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t}" ::"l"(at),
+                 "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(live)
+                 : "memory");
+}
+
+// Four, to 16 bytes.
+__device__ __forceinline__ void st_global_v4(void *at, const uint32_t *w, uint32_t live)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(at), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(live)
                  : "memory");
 }
 
@@ -100,13 +108,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
                  : "memory");
 }
 
-template <bool BF16, int N>
-__device__ __forceinline__ uint32_t pack_of(const uint32_t (&s)[N], int i)
-{
-    return pack2<BF16>(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-}
-
-__device__ __forceinline__ uint64_t f2_of(const uint32_t (&s)[32], int i)
+template <int N>
+__device__ __forceinline__ uint64_t f2_of(const uint32_t (&s)[N], int i)
 {
     return ptx::f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
 }
@@ -379,11 +382,6 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             for (int j = 0; j < n; ++j) {
                 const int gj = g0 + j;
                 const int buf = gj % NB;
-                if (!(ok = wait_all(p_full0 + 16u * buf, (gj / NB) & 1, SITE_P_FULL)))
-                    break;
-                // a unit's first PV overwrites O: the previous unit's rows must have been read
-                if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
-                    break;
                 // Rows of the tile that hold keys. The product takes the steps of 16 rows that have any; what else these
                 // hold, before the first key or behind the last, is zeroed.
                 const int key0 = un.tile0 + j * TILE;
@@ -392,6 +390,29 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 const bool ragged = r1 > r0 && ((r0 | r1) & 15) != 0;
                 const int a0 = max(r0, own - key0), a1 = un.prefix() || p.n == 1 ? 0 : r1;  // keys that some rows do not see
                 const uint32_t a_tmem = tmem + L::TM_S + buf * TILE;
+                // (before P is there: V lands while the softmax is at work)
+                if (ragged || a1 > a0) {
+                    int at = slot;
+                    uint32_t at_ph = ph;
+#pragma unroll 1
+                    for (int v0 = 0; ok && v0 < TILE; v0 += PL::VK) {
+                        auto in = [&](int x) { return max(0, min(x - v0, PL::VK)); };
+                        const int z0 = in(kk0 * 16), y0 = in(r0), y1 = in(r1), z1 = in(kk1 * 16), b0 = in(a0), b1 = in(a1);
+                        if ((z0 < y0 || y1 < z1 || b0 < b1) && (ok = wait_all(slot_full0 + 8u * (PL::NK + at), at_ph, SITE_SLOT_FULL)))
+                            odd |= clean_rows<BF16, D / 64>(s_v + at * PL::V_SLOT, PL::VK * 128, z0, y0, y1, z1, b0, b1, key0 + v0 - own);
+                        if (++at == PL::NV) {
+                            at = 0;
+                            at_ph ^= 1u;
+                        }
+                    }
+                    if (!ok)
+                        break;
+                }
+                if (!(ok = wait_all(p_full0 + 16u * buf, (gj / NB) & 1, SITE_P_FULL)))
+                    break;
+                // a unit's first PV overwrites O: the previous unit's rows must have been read
+                if (j == 0 && k > 0 && !(ok = wait_all(o_free, (k - 1) & 1, SITE_O_DONE)))
+                    break;
 #pragma unroll 1
                 for (int v0 = 0; v0 < TILE; v0 += PL::VK) {
                     if (v0 == TILE / 2 && !(ok = wait_all(p_full0 + 16u * buf + 8u, (gj / NB) & 1, SITE_P_FULL)))
@@ -399,11 +420,6 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                     if (!(ok = wait_all(slot_full0 + 8u * (PL::NK + slot), ph, SITE_SLOT_FULL)))
                         break;
                     ptx::tc_fence_after();
-                    if (ragged || a1 > a0) {
-                        auto in = [&](int x) { return max(0, min(x - v0, PL::VK)); };
-                        odd |= clean_rows<BF16, D / 64>(s_v + slot * PL::V_SLOT, PL::VK * 128, in(kk0 * 16), in(r0), in(r1), in(kk1 * 16),
-                                                        in(a0), in(a1), key0 + v0 - own);
-                    }
                     const uint64_t vslot = dv + static_cast<uint64_t>((slot * PL::V_SLOT) >> 4);
                     const int q0 = max(kk0, v0 / 16), q1 = min(kk1, (v0 + PL::VK) / 16);
                     if (q1 - q0 == PL::VK / 16) {
@@ -431,8 +447,10 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             }
             if (!ok)
                 break;
-            if (lane == 0)
-                *odd_keys = odd;  // the last unit's has been read: its O is free
+            if (lane == 0) {  // the last unit's have been read: its O is free
+                *odd_keys = odd;
+                odd_keys[1] = onto;
+            }
             arrive(odd_full);
             g0 += n;
         }
@@ -629,50 +647,65 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
             if (!(ok = wait_all(o_done0 + 8u * (last % O_DONE_RING), (last / O_DONE_RING) & 1, SITE_O_DONE)) ||
                 !(ok = wait_all(odd_full, k & 1, SITE_O_DONE)))
                 break;
-            const uint32_t odd = *odd_keys;
+            const uint32_t odd = *odd_keys, onto = odd_keys[1];
             if (w4 * 32 < un.toks * p.heads) {
                 ptx::tc_fence_after();
-                const bool none = l == 0.f;  // the row saw no key
-                const float inv = 1.f / l;
+                const bool none = l == 0.f;  // the row saw no key, and its O is 0
+                const float inv = none ? 0.f : 1.f / l;
                 // the row of q and o, -1 where there is none
                 const int at = row_tok < un.toks && row_head < un.live ? (un.q_tok + row_tok) * p.Hq + un.head + row_head : -1;
                 const bool slot = un.dest >= 0, direct = un.dest == DEST_DIRECT;
                 float *const part = slot ? p.parts + un.dest * part_floats<D>(p.part_rows) : un.prefix() ? p.rows_p : p.rows_o;
                 char *const to = direct ? reinterpret_cast<char *>(p.o + static_cast<long long>(at) * D)
                                         : reinterpret_cast<char *>(part + static_cast<long long>(slot ? row : at) * D);
-                // (rolled, 16 channels at a time: run once a unit, straight code is fetched as it runs, at some 9 cycles an instruction)
-                uint32_t a[16], b[16];
-                auto store = [&](uint32_t (&o)[16], int c0) {
-                    if (at < 0)
-                        return;
-#pragma unroll
-                    for (int x = 0; x < 16; ++x)
-                        o[x] = none ? 0u : __float_as_uint(__uint_as_float(o[x]) * inv);
-#pragma unroll
-                    for (int x = 0; x < 16; x += 8) {
-                        if (direct)
-                            reinterpret_cast<uint4 *>(to + 2 * c0)[x / 8] =
-                                make_uint4(pack_of<BF16>(o, x), pack_of<BF16>(o, x + 2), pack_of<BF16>(o, x + 4), pack_of<BF16>(o, x + 6));
-                        else
-                            st_global_v8(to + 4 * (c0 + x), &o[x]);
-                    }
-                };
-                tmem_ld16(t_o, a);
+                if (onto == 0u) {  // no product was made
+                    const uint32_t zeros[16] = {};
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                    for (int c0 = 0; c0 < D; c0 += 16)
+                        ptx::tmem_st16(t_o + c0, zeros);
+                    ptx::tmem_wait_st();
+                }
+                // 16 channels at a time in loops that the instruction buffers hold: straight code, run once a unit, is fetched as it
+                // runs, at some 9 cycles an instruction, and the next unit's first product waits for this.
+                auto read = [&](int c0, uint32_t (&o)[16]) {
+                    tmem_ld16(t_o + c0, o);
                     ptx::tmem_wait_ld();
-                    tmem_ld16(t_o + c0 + 16, b);
-                    store(a, c0);
-                    __syncwarp();
-                    ptx::tmem_wait_ld();
-                    if (c0 + 32 < D) {
-                        tmem_ld16(t_o + c0 + 32, a);
-                    } else {  // the next unit's product may begin
+                    if (c0 + 16 == D) {
                         ptx::tc_fence_before();
                         arrive(o_free);
                     }
-                    store(b, c0 + 16);
-                    __syncwarp();
+                };
+                const uint64_t inv2 = ptx::f2_pack(inv, inv);
+                const uint32_t live = at >= 0 ? 1u : 0u;
+                if (direct) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t o[16], w[8];
+                        read(c0, o);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            float y0, y1;
+                            ptx::f2_unpack(mul2(f2_of(o, 2 * x), inv2), y0, y1);
+                            w[x] = pack2<BF16>(y0, y1);
+                        }
+                        st_global_v4(to + 2 * c0, w, live);  // (o lies on 16 bytes, the workspace's rows on 32)
+                        st_global_v4(to + 2 * c0 + 16, w + 4, live);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D; c0 += 16) {
+                        uint32_t o[16], w[16];
+                        read(c0, o);
+#pragma unroll
+                        for (int x = 0; x < 16; x += 2) {
+                            float y0, y1;
+                            ptx::f2_unpack(mul2(f2_of(o, x), inv2), y0, y1);
+                            w[x] = __float_as_uint(y0);
+                            w[x + 1] = __float_as_uint(y1);
+                        }
+                        st_global_v8(to + 4 * c0, w, live);
+                        st_global_v8(to + 4 * c0 + 32, w + 8, live);
+                    }
                 }
                 if (at >= 0) {
                     if (odd != 0u)
