@@ -39,10 +39,9 @@ struct Cache16Params {
 namespace c16 {
 
 constexpr int TILE = 128;    // keys of a tile
-// Tiles that a problem's start and end cost as much as. (64 x 8k and 60 in four groups at D = 128 with 1, 2, 3, 4, 5: 56 and 70 us,
-// 51 and 65, 49 and 60, 51 and 61, 54 and 62; 256 x 16k at D = 256 with 1, 2, 3: 168, 144 and 145.)
-template <int D>
-constexpr int OVERHEAD = D == 128 ? 3 : 2;
+// Tiles that a problem's start and end cost as much as. (1, 2, 3: 60 in four groups 56.0, 56.1, 56.6 us, 129 sequences of 30 keys
+// behind 5851, D = 128, 39, 43, 49; 256 x 16k at D = 256 129.6, 132.7 with 1 and 2, 205 of 100 keys there 74, 70.)
+constexpr int OVERHEAD = 1;
 constexpr unsigned FULL = 0xffffffffu;
 
 // What a CTA's waits share, in shared memory.
@@ -177,10 +176,9 @@ __device__ __forceinline__ Span span_of(const Cache16Params &p, int e)
 // pass that all the same: sums stop there.)
 constexpr unsigned MOST = 0x7fffffffu;
 
-template <int D>
 __device__ __forceinline__ unsigned entry_length(const Span &s)
 {
-    return s.tiles > 0 ? static_cast<unsigned>(s.problems) * static_cast<unsigned>(s.tiles + OVERHEAD<D>) : 0u;
+    return s.tiles > 0 ? static_cast<unsigned>(s.problems) * static_cast<unsigned>(s.tiles + OVERHEAD) : 0u;
 }
 
 // Positions cut into n runs: run i begins at floor(total * i / n).
@@ -229,7 +227,7 @@ __device__ __forceinline__ unsigned sum_to_lane(unsigned x)
 }
 
 // The runs, as a CTA sees them: `begin` by all threads of the CTA, `start` and `next` by one warp.
-template <int D, int THREADS>
+template <int THREADS>
 struct Runs {
     // what `begin` leaves in shared memory (where the copies' ring is later, but for `start` to have read it)
     struct Shared {
@@ -253,7 +251,7 @@ struct Runs {
             const Span s = span_of(p, e);
             if (e == tid)
                 sh.first[e] = s;
-            sum = min(sum + entry_length<D>(s), MOST);
+            sum = min(sum + entry_length(s), MOST);
             if (s.bad && e < p.ngroups && blockIdx.x == 0)
                 atomicCAS(p.status, 0u, kBadSeqlens);
         }
@@ -319,7 +317,7 @@ struct Runs {
                 at.toks = __shfl_sync(FULL, mine.toks, from);
                 if (at.tiles == 0)
                     continue;
-                const int len = at.tiles + OVERHEAD<D>;
+                const int len = at.tiles + OVERHEAD;
                 kv = heads = b = hb = in = 0;
                 block = e < p.ngroups ? p.toks_p : p.toks_o;
                 if (skip > 0) {  // the run's first problem
@@ -344,8 +342,8 @@ struct Runs {
                 }
             }
             // the problem's positions [in, in + take)
-            const int take = min(left, at.tiles + OVERHEAD<D> - in);
-            const int t0 = max(0, in - OVERHEAD<D>), t1 = in + take - OVERHEAD<D>;
+            const int take = min(left, at.tiles + OVERHEAD - in);
+            const int t0 = max(0, in - OVERHEAD), t1 = in + take - OVERHEAD;
             left -= take;
             in = 0;
             const bool prefix = e < p.ngroups;
@@ -501,62 +499,30 @@ __device__ __forceinline__ Tile tile_of(const Cache16Params &p, const Unit &un, 
     return Tile{j * (TILE >> p.box_log2), keys > 0 ? (keys + p.box - 1) >> p.box_log2 : 0, plane, off};
 }
 
-// A tile's copies, in D / C slots. False when a wait ran out.
-template <int D, int C>
-__device__ __forceinline__ bool copy_tile(const Cache16Params &p, const CUtensorMap *map, Ring &r, Waits *waits, const Tile &t)
+// A tile's copies. A slot of K has 64 channels of all keys, one of V all channels of VK keys; a box has 64 channels, and a lane
+// has a box. (One place for both: what a unit's copies run through is fetched from behind the instruction cache each time
+// where units are short. A loop over the boxes took 130 cycles a box, lanes of their own take 55.) False when a wait ran out.
+template <int D, int VK>
+__device__ __forceinline__ bool copy_tile(const Cache16Params &p, const CUtensorMap *map, bool of_k, Ring &r, Waits *waits, const Tile &t)
 {
+    const int lane = threadIdx.x & 31;
+    const int rows = t.n << p.box_log2, keys = of_k ? TILE : VK, box_log2 = min(p.box_log2, of_k ? 7 : 6);
+    const int slot_bytes = of_k ? TILE * 128 : VK * D * 2, across = of_k ? 0 : D == 128 ? 1 : 2;  // 2^across boxes side by side
+    static_assert(TILE == 128 && VK == 64, "the largest box");
+    const int key = (lane >> across) << box_log2, box = lane & ((1 << across) - 1);  // this lane's box
 #pragma unroll 1
-    for (int x = 0; x < D; x += C) {
+    for (int s = 0; s < (of_k ? D / 64 : TILE / VK); ++s) {
         if (!wait_warp(r.empty0 + 8u * r.slot, r.ph ^ 1u, waits, 2 /* a slot that does not empty */, 1))
             return false;
         const uint32_t full = r.full0 + 8u * r.slot;
-        ptx::mbar_arrive_expect_tx_w(full, t.n * p.box * (2 * C));
-        uint32_t dst = r.base + r.slot * (C * 256);
-#pragma unroll 1
-        for (int i = 0; i < t.n; i += 2) {
-            const int z0 = __shfl_sync(FULL, t.plane, t.first + i), y0 = __shfl_sync(FULL, t.off, t.first + i);
-            const int z1 = __shfl_sync(FULL, t.plane, t.first + i + 1), y1 = __shfl_sync(FULL, t.off, t.first + i + 1);
-#pragma unroll
-            for (int b = 0; b < C / 64; ++b)
-                ptx::tma_load_3d_w(dst + b * 16384, map, full, x + 64 * b, y0, z0);
-            if (i + 1 < t.n) {
-#pragma unroll
-                for (int b = 0; b < C / 64; ++b)
-                    ptx::tma_load_3d_w(dst + p.box * 128 + b * 16384, map, full, x + 64 * b, y1, z1);
-            }
-            dst += 2 * p.box * 128;
-        }
-        r.armed |= 1u << r.slot;
-        r.armed_par = (r.armed_par & ~(1u << r.slot)) | (r.ph << r.slot);
-        if (++r.slot == r.slots) {
-            r.slot = 0;
-            r.ph ^= 1u;
-        }
-    }
-    return true;
-}
-
-// Of V, by keys: slots of KEYS keys with all their channels, in boxes of KEYS keys or p.box.
-template <int D, int KEYS>
-__device__ __forceinline__ bool copy_tile_by_keys(const Cache16Params &p, const CUtensorMap *map, Ring &r, Waits *waits,
-                                                  const Tile &t)
-{
-    const int rows = t.n * p.box, box = min(p.box, KEYS);
-#pragma unroll 1
-    for (int k0 = 0; k0 < TILE; k0 += KEYS) {
-        if (!wait_warp(r.empty0 + 8u * r.slot, r.ph ^ 1u, waits, 2, 1))
-            return false;
-        const uint32_t full = r.full0 + 8u * r.slot;
-        ptx::mbar_arrive_expect_tx_w(full, max(0, min(KEYS, rows - k0)) * (2 * D));  // (rows is a multiple of the boxes)
-        const uint32_t dst = r.base + r.slot * (KEYS * 2 * D);
-#pragma unroll 1
-        for (int k = k0; k < min(k0 + KEYS, rows); k += box) {
-            const int z = __shfl_sync(FULL, t.plane, t.first + (k >> p.box_log2));
-            const int y = __shfl_sync(FULL, t.off, t.first + (k >> p.box_log2)) + (k & (p.box - 1));
-#pragma unroll
-            for (int b = 0; b < D / 64; ++b)
-                ptx::tma_load_3d_w(dst + b * (KEYS * 128) + (k - k0) * 128, map, full, 64 * b, y, z);
-        }
+        const int k0 = of_k ? 0 : s * VK, n = max(0, min(rows - k0, keys));  // (rows is a multiple of the boxes)
+        ptx::mbar_arrive_expect_tx_w(full, n << (7 + across));
+        const int from = t.first + ((k0 + key) >> p.box_log2);
+        const int z = __shfl_sync(FULL, t.plane, from & 31), y = __shfl_sync(FULL, t.off, from & 31) + ((k0 + key) & (p.box - 1));
+        __syncwarp();
+        if (key < n)
+            ptx::tma_load_3d(r.base + r.slot * slot_bytes + key * 128 + box * (keys * 128), map, full, (of_k ? s : box) * 64, y, z);
+        __syncwarp();
         r.armed |= 1u << r.slot;
         r.armed_par = (r.armed_par & ~(1u << r.slot)) | (r.ph << r.slot);
         if (++r.slot == r.slots) {

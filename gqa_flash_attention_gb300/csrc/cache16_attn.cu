@@ -44,7 +44,7 @@ int shape_of(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups,
     const int most = ngroups > 0 ? static_cast<int>(std::min<long long>(sh->toks_p, tokens)) : sh->toks_o;
     sh->part_rows = most * sh->heads;
     // 31 bits for the positions that the work is cut by, whatever the lengths: tiles, and what the problems' ends count
-    auto positions = [](long long k) { return static_cast<double>(k / sdp::c16::TILE + 1 + sdp::c16::OVERHEAD<128>); };
+    auto positions = [](long long k) { return static_cast<double>(k / sdp::c16::TILE + 1 + sdp::c16::OVERHEAD); };
     const double own_blocks = static_cast<double>(nseq) * sh->blocks_o, shared_blocks = static_cast<double>(tokens) / sh->toks_p + ngroups;
     if ((own_blocks * positions(keys) + (ngroups > 0 ? shared_blocks * positions(prefix_keys) : 0.0)) * Hkv * sh->head_blocks > INT32_MAX)
         return SDP_ERR_OVERFLOW;

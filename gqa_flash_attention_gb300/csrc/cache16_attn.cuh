@@ -80,7 +80,7 @@ struct Plan {
     static_assert(HOLDER_OFF % 8 == 0 && HOLDER_OFF + 24 + sizeof(Waits) <= BAR_OFF + BAR_AREA, "barrier area");
     static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
     static_assert(sizeof(Unit) % 16 == 0 && UNIT_OFF % 16 == 0, "unit ring");
-    static_assert(sizeof(typename Runs<D, THREADS>::Shared) <= BAR_OFF - RING_OFF, "the sums of the problems' lengths");
+    static_assert(sizeof(Runs<THREADS>::Shared) <= BAR_OFF - RING_OFF, "the sums of the problems' lengths");
 };
 
 // Eight words to a 32-byte boundary, a whole sector of a row, if `live`.
@@ -164,12 +164,12 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     const int run = static_cast<int>(blockIdx.x);
 
     if (warp == 15) {  // (the first warps have entries to look up)
-        // one arrival each, but for p_full, o_free and sum_free, where four warps arrive, sum_full (eight) and unit_free
+        // one arrival each, but for p_full, o_free and sum_free, where four warps arrive, sum_full (eight) and unit_free (all)
         constexpr int P0 = 2 * QB + 2 * NS + NB, P1 = P0 + 2 * NB, SUM = P1 + O_DONE_RING + 2;
         for (int i = lane; i < PL::NBARS; i += 32) {
             const bool four = (i >= P0 && i < P1) || i == SUM || i == SUM + 2;
-            const bool readers = i >= SUM + 4 + PL::UNITS && i < SUM + 4 + 2 * PL::UNITS;  // unit_free: the warps that read it
-            ptx::mbar_init(q_full0 + 8u * i, four ? 4 : i == SUM + 1 ? 8 : readers ? 15 : 1);
+            const bool readers = i >= SUM + 4 + PL::UNITS && i < SUM + 4 + 2 * PL::UNITS;  // unit_free: all warps
+            ptx::mbar_init(q_full0 + 8u * i, four ? 4 : i == SUM + 1 ? 8 : readers ? 16 : 1);
         }
         if (lane == 0) {
             waits->abort = 0;
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     // finds no room beside a CTA, so it starts where there is none or it has ended, and waits there for the last one.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    using R = Runs<D, THREADS>;
-    typename R::Shared &sums = *reinterpret_cast<typename R::Shared *>(smem + PL::RING_OFF);
+    using R = Runs<THREADS>;
+    R::Shared &sums = *reinterpret_cast<R::Shared *>(smem + PL::RING_OFF);
     R runs;
     ptx::tc_fence_before();
     runs.begin(p, sums);
@@ -224,24 +224,12 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         return un.n >= 0;
     };
 
-    if (warp == 4) {
-        // ------------------------------------------ the run's units, for all warps, and the copies of Q and K
-        Ring r{s_k, slot_full0, slot_empty0, PL::NK, 0, 0, 0, 0};
+    if (warp == 4 || warp == 7) {
+        // ------------------------------------------ the copies of Q and K (warp 4), and of V
+        const bool of_k = warp == 4;
+        Ring r{of_k ? s_k : s_v, slot_full0 + (of_k ? 0u : 8u * PL::NK), slot_empty0 + (of_k ? 0u : 8u * PL::NK), of_k ? PL::NK : PL::NV, 0, 0, 0, 0};
         uint32_t q_armed = 0, q_par = 0;
         int longest = 1;  // of the units so far: its end may be what is waited for
-        runs.start(p, sums);
-        auto publish = [&](int i, Unit &un) -> bool {  // unit i; false at the end or when a wait ran out
-            un = runs.next(p);
-            const int at = i % PL::UNITS;
-            if (i >= PL::UNITS && !wait_all(unit_free0 + 8u * at, (i / PL::UNITS - 1) & 1, SITE_Q_FULL, longest))
-                return false;
-            longest = max(longest, un.n);
-            if (lane == 0) {
-                ring[at] = un;
-                ptx::mbar_arrive(unit_full0 + 8u * at);
-            }
-            return un.n >= 0;
-        };
         const int tiles = p.box / 4;  // of a batch of 32 boxes
         Unit un, next_un;
         un.n = 0;
@@ -250,16 +238,19 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
 #pragma unroll 1
         for (int k = -1;; ++k) {
             const int b = k % QB;
-            if (k >= QB && !wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL, longest))
-                break;
-            if (k >= 0 && !p.no_copies) {
-                ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, (un.prefix() ? p.toks_p : p.toks_o) * p.heads * D * 2);
+            if (of_k && k >= 0) {
+                if (k >= QB && !wait_all(q_free0 + 8u * b, ((k - QB) / QB) & 1, SITE_Q_FULL, longest))
+                    break;
+                longest = max(longest, un.n);
+                if (!p.no_copies) {
+                    ptx::mbar_arrive_expect_tx_w(q_full0 + 8u * b, (un.prefix() ? p.toks_p : p.toks_o) * p.heads * D * 2);
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c)
-                    ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, un.prefix() ? &tm_qp : &tm_qo, q_full0 + 8u * b, c * 64,
-                                       un.head, un.q_tok);
-                q_armed |= 1u << b;
-                q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
+                    for (int c = 0; c < D / 64; ++c)
+                        ptx::tma_load_3d_w(s_q0 + b * L::Q_BYTES + c * L::BOX_BYTES, un.prefix() ? &tm_qp : &tm_qo, q_full0 + 8u * b, c * 64,
+                                           un.head, un.q_tok);
+                    q_armed |= 1u << b;
+                    q_par = (q_par & ~(1u << b)) | (((k / QB) & 1u) << b);
+                }
             }
             int j = 0;
             bool ok = true, more = true;
@@ -269,11 +260,11 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 // the next batch's pages, of this unit or of the one behind it, are looked up while this one is copied
                 const bool same = end < un.n;
                 if (!same)
-                    more = publish(k + 1, next_un);
+                    more = take(k + 1, next_un);
                 next = pages_of(p, same ? un : next_un, same ? end / tiles : 0);
 #pragma unroll 1
                 for (; ok && j < end; ++j)
-                    ok = p.no_copies || copy_tile<D, PL::KC>(p, &tm_k, r, waits, tile_of(p, un, j, plane, off));
+                    ok = p.no_copies || copy_tile<D, PL::VK>(p, of_k ? &tm_k : &tm_v, of_k, r, waits, tile_of(p, un, j, plane, off));
                 now = next;
             } while (ok && j < un.n);
             if (!ok || !more)
@@ -284,34 +275,6 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         for (int b = 0; b < QB; ++b)
             if (q_armed & (1u << b))
                 wait_own(q_full0 + 8u * b, (q_par >> b) & 1u, waits);
-        land(r, waits);
-    } else if (warp == 7) {
-        // ------------------------------------------ the copies of V
-        Ring r{s_v, slot_full0 + 8u * PL::NK, slot_empty0 + 8u * PL::NK, PL::NV, 0, 0, 0, 0};
-        const int tiles = p.box / 4;
-        Unit un, next_un;
-        un.n = 0;
-        Pages now{}, next{};
-#pragma unroll 1
-        for (int k = -1;; ++k) {
-            int j = 0;
-            bool ok = true, more = true;
-#pragma unroll 1
-            do {
-                const int plane = planes_of(p, un, now), off = now.off, end = min(un.n, j + tiles);
-                const bool same = end < un.n;
-                if (!same)
-                    more = take(k + 1, next_un);
-                next = pages_of(p, same ? un : next_un, same ? end / tiles : 0);
-#pragma unroll 1
-                for (; ok && j < end; ++j)
-                    ok = p.no_copies || copy_tile_by_keys<D, PL::VK>(p, &tm_v, r, waits, tile_of(p, un, j, plane, off));
-                now = next;
-            } while (ok && j < un.n);
-            if (!ok || !more)
-                break;
-            un = next_un;
-        }
         land(r, waits);
     } else if (warp == 5) {
         // ------------------------------------------- S = Q K^T issuer
@@ -629,14 +592,36 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         }
         ptx::tmem_wait_ld();  // (where a wait ran out)
     } else {
-        // --------------------------------------- rows' ends: O over l, to the output or to the workspace
+        // --------------------------------------- rows' ends: O over l, to the output or to the workspace; and the run's units, looked
+        // up ahead by warp 11, whose rows are the last that a small unit has
         const int w4 = warp & 3, row = w4 * 32 + lane;
         const int row_tok = row / p.heads, row_head = row - row_tok * p.heads;
         const uint32_t t_o = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + L::TM_O;
         bool ok = true;
         int g0 = 0;
         Unit un;
-        for (int k = 0; ok && take(k, un); ++k) {
+        int published = 0, longest = 1;  // units, and the tiles of the longest: its end may be what is waited for
+        bool more = warp == 11;
+        if (more)
+            runs.start(p, sums);
+        for (int k = 0;; ++k) {
+#pragma unroll 1
+            for (; more && published < k + PL::UNITS; ++published) {
+                const Unit next = runs.next(p);
+                const int at = published % PL::UNITS;
+                if (published >= PL::UNITS && !wait_all(unit_free0 + 8u * at, (published / PL::UNITS - 1) & 1, SITE_Q_FULL, longest)) {
+                    ok = false;
+                    break;
+                }
+                more = next.n >= 0;
+                longest = max(longest, next.n);
+                if (lane == 0) {
+                    ring[at] = next;
+                    ptx::mbar_arrive(unit_full0 + 8u * at);
+                }
+            }
+            if (!ok || !take(k, un))
+                break;
             const int n = un.n, last = g0 + n - 1;
             if (threadIdx.x == 8 * 32 && un.join >= 0)
                 (un.prefix() ? p.joins_p : p.joins_o)[un.join] = make_int2(run, runs.parts_of(un.after));

@@ -324,6 +324,14 @@ __device__ __forceinline__ void tma_load_3d_w(uint32_t dst, const CUtensorMap *m
                  : "memory");
 }
 
+// The same by the calling thread.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
 // 3-D tiled load into this CTA's shared memory whose completion is counted on
 // a barrier that may live in the peer CTA (shared::cluster address).
 __device__ __forceinline__ void tma_load_3d_pair_w(uint32_t dst, const CUtensorMap *map, uint32_t bar_cluster, int x,
