@@ -25,7 +25,7 @@
 // the other, the rows' maxima, goes from tile to tile through shared memory between the two passes. P is handed over in
 // halves, so that its product with V begins while the second one is computed. What remains is the chain S -> softmax -> PV ->
 // S of the tile that takes the same buffer (2 at D = 256, which leaves no tensor memory for a third, 3 at D = 128): 1700
-// cycles a tile at D = 128, 3200 at D = 256, where shared memory's 128 bytes a cycle alone would need 2560 (S reads Q and
+// cycles a tile at D = 128, 3050 at D = 256, where shared memory's 128 bytes a cycle alone would need 2560 (S reads Q and
 // K, PV reads V, the copies write both). HBM's share is 2800 and 5600 cycles a tile that nobody else reads.
 //
 // Work split: the problems' tiles are numbered through, groups first, and cut into equal runs, one a CTA, a problem's start
@@ -36,10 +36,16 @@
 // Two tiles at a time of queries that share a tile of K and V (CTA pairs) would halve the copies; one tile's O and S buffers
 // fill tensor memory at D = 256.
 //
-// 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 48 us, where HBM alone takes 24;
-// 256 behind 16384, 32 heads over 2, D = 256: 134 us, where the tensor cores alone take 72; eight of 16384 tokens that share
-// nothing, D = 256: 53 us (5.0 TB/s), where HBM takes 40. A launch needs some 10000 cycles (5 us) before its first copy
-// and the join 4 to 8 us after the last tile.
+// What a problem's start and end cost. Each runs through some 30 KB of code once (look-up, copies, masks, cleaning, rows' ends), and
+// with sixteen warps at seven kinds of work that is more than the instruction cache nearest them keeps: straight code then
+// takes some 10 cycles an instruction, and what counts is how much of it there is, and on whose way. So units are looked up
+// ahead by a warp that has time (on the copier's own way a problem of one tile took 8000 cycles, so 5000), both copiers
+// run through one place, each box of a slot is a lane's, and the rows' ends are two loops of a few lines.
+//
+// 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 45 us, where HBM alone takes 24;
+// 256 behind 16384, 32 heads over 2, D = 256: 129 us, where the tensor cores alone take 72; eight of 16384 tokens that share
+// nothing, D = 256: 52 us (5.1 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 39 us, HBM 14. A launch
+// needs some 9000 cycles (5 us) before its first copy and the join 4 to 8 us after the last tile.
 //
 // Keys outside [lo, hi) of a problem share its first and last tiles. Their scores are replaced before any arithmetic, whatever
 // they hold (NaN too); their rows of V are zeroed in shared memory or left out of the product. A drafted token's V is seen by
@@ -63,7 +69,7 @@ struct Plan {
     static constexpr int UNITS = 4;              // units looked up ahead
     // K and V have rings of their own, so that whoever waits for a slot has seen what it held before: its barrier is one phase
     // away at most. A slot of K has 128 keys by KC channels, one of V VK keys by all channels. At D = 256, where 160 KB are 1.25
-    // tiles, 256 x 16k took 137 us with 4 and 3 slots; with V in 5 slots of 32 keys 144, with K in 2 of 128 channels 141.
+    // tiles, 256 x 16k took 137 us (129 since) with 4 and 3 slots; with V in 5 slots of 32 keys 144, with K in 2 of 128 channels 141.
     static constexpr int KC = 64, VC = D, VK = 64;
     static constexpr int NK = 4, NV = D == 128 ? 5 : 3, NS = NK + NV;
     static constexpr int K_SLOT = KC * 256, V_SLOT = VC * VK * 2;
