@@ -44,7 +44,7 @@
 //
 // 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 45 us, where HBM alone takes 24;
 // 256 behind 16384, 32 heads over 2, D = 256: 129 us, where the tensor cores alone take 72; eight of 16384 tokens that share
-// nothing, D = 256: 52 us (5.1 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 39 us, HBM 14. A launch
+// nothing, D = 256: 51 us (5.2 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 39 us, HBM 14. A launch
 // needs some 9000 cycles (5 us) before its first copy and the join 4 to 8 us after the last tile.
 //
 // Keys outside [lo, hi) of a problem share its first and last tiles. Their scores are replaced before any arithmetic, whatever
@@ -69,9 +69,10 @@ struct Plan {
     static constexpr int UNITS = 4;              // units looked up ahead
     // K and V have rings of their own, so that whoever waits for a slot has seen what it held before: its barrier is one phase
     // away at most. A slot of K has 128 keys by KC channels, one of V VK keys by all channels. At D = 256, where 160 KB are 1.25
-    // tiles, 256 x 16k took 137 us (129 since) with 4 and 3 slots; with V in 5 slots of 32 keys 144, with K in 2 of 128 channels 141.
+    // tiles, 8 x 16k takes 51.4 us with 6 and 2 slots and 52.4 with 4 and 3 (256 x 16k 130.5 with both); with V in 5 slots of 32 keys
+    // 256 x 16k took 144 us where it took 137, with K in 2 of 128 channels 141.
     static constexpr int KC = 64, VC = D, VK = 64;
-    static constexpr int NK = 4, NV = D == 128 ? 5 : 3, NS = NK + NV;
+    static constexpr int NK = D == 128 ? 4 : 6, NV = D == 128 ? 5 : 2, NS = NK + NV;
     static constexpr int K_SLOT = KC * 256, V_SLOT = VC * VK * 2;
     static constexpr int BAR_AREA = 512;
     // q_full[QB], q_free[QB], slot_full[NS], slot_empty[NS], s_full[NB], p_full[NB][2], o_done[ring], final[2], o_free,
@@ -759,7 +760,8 @@ cudaError_t launch_cache16_attn(const Cache16Maps &m, const Cache16Params &p, cu
         return f;
     const unsigned rows = static_cast<unsigned>(p.nseq * p.n * p.Hq);
     constexpr int WARPS = c16::JOIN_THREADS / 32;
-    // a row a warp once that still gives every SM two blocks
+    // A row a warp once that still gives every SM two blocks: 2048 rows of 64 x 8k in 45.3 us (a row a block: 47.3), 8192 of 256 x 16k in
+    // 130 (140); below, a row a block: 256 rows of 8 x 16k, nine parts each, in 52.4 us (a row a warp: 54.5).
     return rows >= 2u * p.sms * WARPS
                ? launch(cache16_join_kernel<D, BF16, 1>, (rows + WARPS - 1) / WARPS, c16::JOIN_THREADS, 0, p)
                : launch(cache16_join_kernel<D, BF16, WARPS>, rows, c16::JOIN_THREADS, 0, p);
