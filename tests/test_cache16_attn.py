@@ -603,3 +603,43 @@ def test_steps_that_follow_each_other_at_once(D):
     for a, b in zip(*results):
         assert torch.equal(a, b)
     assert not results[0][1].isnan().any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [16, 48, 96, 160, 272, 1024, 4096])
+@pytest.mark.parametrize("D", [128, 256])
+def test_page_sizes(page, D):
+    """Boxes of 16 to 128 keys, pages that tiles straddle and pages that hold many."""
+    b = Batch([page + 5, 3 * page - 1, 2 * page, 700], [0, 3], [page - 3], 2, 6, 2, D, page, torch.float16)
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+def test_several_host_threads():
+    """Calls from threads of their own on streams of their own, workspaces from the allocator: each gets its own results."""
+    import threading
+    bs = [plain_batch(seed=s, lens=[700, 600 + s, 650], cu=[0, 3], prefix=[512]) for s in range(4)]
+    args = [b.args() for b in bs]
+    want = [tuple(t.clone() for t in sdp.fwd_cache16(**a)) for a in args]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(50):
+                o, lse = sdp.fwd_cache16(**args[i])
+                st.synchronize()
+                if not (torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])):
+                    wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and sdp.poll_status() == sdp.SDP_OK
+    for b, w in zip(bs, want):
+        b.check(*w)
