@@ -229,17 +229,19 @@ __device__ __forceinline__ unsigned sum_to_lane(unsigned x)
 // The runs, as a CTA sees them: `begin` by all threads of the CTA, `start` and `next` by one warp.
 template <int THREADS>
 struct Runs {
-    // what `begin` leaves in shared memory (where the copies' ring is later, but for `start` to have read it)
+    // What `begin` leaves in shared memory for `start`, where the copies' ring is later: the warp that reads it is the one that lets
+    // copies begin.
     struct Shared {
-        unsigned prefix[THREADS], sum[THREADS / 32];
+        unsigned prefix[THREADS];
         Span first[THREADS];  // thread e's first entry, where that is e
     };
     int entries, per;
     Cut cut{0, 1};
     unsigned upto;  // lane w: the entries' lengths before warp w's
 
-    // The lengths of all entries, summed up: each thread has some consecutive ones. Ends with __syncthreads().
-    __device__ __forceinline__ void begin(const Cache16Params &p, Shared &sh)
+    // The lengths of all entries, summed up: each thread has some consecutive ones. `sums` has a word a warp, which every warp
+    // reads behind the only __syncthreads(), when another may be copying already: no copy lands there.
+    __device__ __forceinline__ void begin(const Cache16Params &p, Shared &sh, unsigned *sums)
     {
         const int tid = threadIdx.x, lane = tid & 31;
         entries = p.ngroups + p.nseq;
@@ -258,10 +260,10 @@ struct Runs {
         const unsigned incl = sum_to_lane(sum);
         sh.prefix[tid] = incl - sum;  // within the warp
         if (lane == 31)
-            sh.sum[tid >> 5] = incl;
+            sums[tid >> 5] = incl;
         __syncthreads();
         // the warps' sums, a lane each
-        const unsigned of_warp = lane < THREADS / 32 ? sh.sum[lane] : 0u;
+        const unsigned of_warp = lane < THREADS / 32 ? sums[lane] : 0u;
         const unsigned all = sum_to_lane(of_warp);
         cut = Cut(__shfl_sync(FULL, all, 31), p.sms);
         upto = all - of_warp;

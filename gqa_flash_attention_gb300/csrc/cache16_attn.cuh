@@ -83,11 +83,13 @@ struct Plan {
     static constexpr int HOLDER_OFF = BAR_OFF + 8 * NBARS;  // TMEM address, -, mask of keys that are not finite, whether O holds anything, Waits
     static constexpr int SUM_OFF = BAR_OFF + BAR_AREA;      // the rows' maxima so far; of a unit, their m and l from the two groups of softmax warps
     static constexpr int UNIT_OFF = SUM_OFF + 4 * TILE * 4;
-    static constexpr int SMEM_BYTES = UNIT_OFF + UNITS * static_cast<int>(sizeof(Unit));
+    static constexpr int TOTALS_OFF = UNIT_OFF + UNITS * static_cast<int>(sizeof(Unit));  // of the entries of each warp (Runs::begin)
+    static constexpr int SMEM_BYTES = TOTALS_OFF + THREADS / 32 * 4;
     static_assert(HOLDER_OFF % 8 == 0 && HOLDER_OFF + 24 + sizeof(Waits) <= BAR_OFF + BAR_AREA, "barrier area");
     static_assert(SMEM_BYTES <= L::SMEM_LIMIT, "shared memory");
     static_assert(sizeof(Unit) % 16 == 0 && UNIT_OFF % 16 == 0, "unit ring");
     static_assert(sizeof(Runs<THREADS>::Shared) <= BAR_OFF - RING_OFF, "the sums of the problems' lengths");
+    static_assert(TOTALS_OFF >= V_OFF + NV * V_SLOT, "copies land below");
 };
 
 // Eight words to a 32-byte boundary, a whole sector of a row, if `live`.
@@ -205,7 +207,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
     R::Shared &sums = *reinterpret_cast<R::Shared *>(smem + PL::RING_OFF);
     R runs;
     ptx::tc_fence_before();
-    runs.begin(p, sums);
+    runs.begin(p, sums, reinterpret_cast<unsigned *>(smem + PL::TOTALS_OFF));
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     if (blockIdx.x >= runs.cut.n) {  // nothing left for this one
