@@ -261,6 +261,7 @@ struct Runs {
         sh.prefix[tid] = incl - sum;  // within the warp
         if (lane == 31)
             sums[tid >> 5] = incl;
+        ptx::fence_proxy_async_smem();  // (these stores come before the copies that land on `sh`)
         __syncthreads();
         // the warps' sums, a lane each
         const unsigned of_warp = lane < THREADS / 32 ? sums[lane] : 0u;
@@ -293,6 +294,8 @@ struct Runs {
         mine = per == 1 ? sh.first[of_lane] : span_of(p, of_lane);
         e = base - 1;
         kv = p.Hkv;  // done with entry e
+        ptx::fence_proxy_async_smem();  // and so do these reads: lane 0 publishes the first unit behind them
+        __syncwarp();
     }
 
     // The next unit.

@@ -102,7 +102,7 @@ __device__ __forceinline__ void bulk_wait_group_read_all()
     asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
-// Order this thread's generic-proxy shared-memory writes before later async-proxy reads.
+// Order this thread's generic-proxy shared-memory accesses before later async-proxy ones (a product's reads, a copy's writes).
 __device__ __forceinline__ void fence_proxy_async_smem()
 {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
