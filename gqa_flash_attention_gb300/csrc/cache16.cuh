@@ -43,6 +43,9 @@ constexpr int TILE = 128;    // keys of a tile
 // behind 5851, D = 128, 39, 43, 49; 256 x 16k at D = 256 129.6, 132.7 with 1 and 2, 205 of 100 keys there 74, 70.)
 constexpr int OVERHEAD = 1;
 constexpr unsigned FULL = 0xffffffffu;
+// How far behind a problem's last key the first key of a box is formed: boxes are looked up 32 at a time, from a tile that has
+// keys on, and have TILE keys at most. All keys that tables and prefixes could hold end that much below 2^31.
+constexpr int KEYS_BEHIND = 32 * TILE;
 
 // What a CTA's waits share, in shared memory.
 struct Waits {

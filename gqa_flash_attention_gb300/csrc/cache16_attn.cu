@@ -99,9 +99,10 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
         !is_aligned(lse, 4) || !is_aligned(block_table, 4) || !is_aligned(cache_lens, 4) || !is_aligned(prefix_table, 4) ||
         !is_aligned(prefix_lens, 4) || !is_aligned(cu_groups, 4) || !is_aligned(workspace, 16))
         return SDP_ERR_ALIGNMENT;
-    // 31 bits for key indexes up to two tiles past the end, and for a page's row of heads
-    if (static_cast<long long>(max_pages) * page_size > INT32_MAX - 256 ||
-        (ngroups > 0 && static_cast<long long>(prefix_pages) * page_size > INT32_MAX - 256) || num_pages > INT32_MAX / std::max(Hkv, 1))
+    // 31 bits for the indexes of keys, and of those looked up behind the last one, and for a page's row of heads
+    constexpr long long most = INT32_MAX - sdp::c16::KEYS_BEHIND;
+    if (static_cast<long long>(max_pages) * page_size > most ||
+        (ngroups > 0 && static_cast<long long>(prefix_pages) * page_size > most) || num_pages > INT32_MAX / std::max(Hkv, 1))
         return SDP_ERR_OVERFLOW;
     Shape sh;
     int rc = shape_of(nseq, rows, Hq, Hkv, D, dtype, ngroups, static_cast<long long>(max_pages) * page_size,

@@ -406,7 +406,7 @@ int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_siz
  * (SDP_ERR_DEVICE_TIMEOUT). Errors, streams and the status word's first-call allocation as sdp_fwd. Two kernels are enqueued
  * on `stream`; they, and sdp_cache16_append's, may be launched while what is before them on the stream ends, and read and
  * write nothing before it has. Rows, and 128-key tiles that all sequences' tables and prefixes could hold for every KV head, are counted in
- * 31 bits (SDP_ERR_OVERFLOW). The workspace size depends on the current device; a negative value is a status code.
+ * 31 bits, and max_pages * page_size and prefix_pages * page_size end 4096 below 2^31 (SDP_ERR_OVERFLOW). The workspace size depends on the current device; a negative value is a status code.
  */
 long long sdp_fwd_cache16_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups);
 int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,

@@ -5,7 +5,18 @@ import pytest
 import torch
 
 import gqa_flash_attention_gb300 as sdp
-from test_cache16_attn import Batch
+from test_cache16_attn import Batch, c_call
+
+
+@pytest.mark.parametrize("kw", [
+    # a box is looked up from up to 32 tiles behind the last key on: the largest tables that leave those no room
+    dict(page=128, mp=(2 ** 31 - 384) // 128), dict(page=128, pp=(2 ** 31 - 384) // 128),
+    dict(page=128, mp=(2 ** 31 - 4096) // 128), dict(page=128, pp=(2 ** 31 - 4096) // 128),
+    dict(page=16, mp=(2 ** 31 - 4096) // 16), dict(page=2 ** 30 - 512, mp=2, ng=0)])
+def test_tables_of_almost_two_to_the_31_keys_are_refused(kw):
+    from gqa_flash_attention_gb300 import build
+    build.build()
+    assert c_call(**{**dict(nseq=1, Hq=1, Hkv=1), **kw}) == sdp.SDP_ERR_OVERFLOW
 
 
 @pytest.mark.gpu
