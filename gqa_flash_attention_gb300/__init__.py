@@ -354,7 +354,8 @@ def set_debug_flags(flags: int) -> int:
     persistent kernel would run; 32: variable-length launches on the full grid
     instead of the compact tile list; 64: never the two-tile CTA-pair kernel at
     head dim 128; 128: the two-tile CTA-pair kernel (two query tiles per CTA,
-    64-key steps) for dense non-causal head-dim-128 launches whose units pair.
+    64-key steps) for dense non-causal head-dim-128 launches whose units pair;
+    256: fwd_cache16's warps are given no work (each one's first wait runs out).
     4, 16 and 32 give bit-identical results; 2, 8 and 128 switch kernels that
     compute the same function.
     """

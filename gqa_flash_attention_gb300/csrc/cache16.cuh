@@ -32,7 +32,7 @@ struct Cache16Params {
     int2 *joins_o, *joins_p;  // of each problem its first run and its parts (1: whole)
     unsigned int *status;
     unsigned long long timeout_ns;
-    int no_copies;  // test hook: no copy is issued, every wait runs out
+    int no_copies, no_units;  // test hooks: no copy is issued, no unit is published; every wait runs out
     float c;        // scale * log2(e), not 0
 };
 

@@ -165,6 +165,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     p.joins_p = reinterpret_cast<int2 *>(ws + sh.joins_p);
     p.timeout_ns = sdp::wait_timeout_ns();
     p.no_copies = sdp::debug_flags() & 1;
+    p.no_units = sdp::debug_flags() & 256;
     p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
     if (p.c == 0.f)
         p.c = 1e-37f;  // scores of 0, where those that a row does not see are still -inf

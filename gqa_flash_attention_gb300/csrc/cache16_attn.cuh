@@ -224,10 +224,12 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         if (lane == 0)
             ptx::mbar_arrive(bar);
     };
-    auto take = [&](int i, Unit &un) -> bool {  // unit i; false at the end or when a wait ran out
+    auto take = [&](int i, Unit &un) -> bool {  // unit i; false, and a unit without tiles, at the end or when a wait ran out
         const int at = i % PL::UNITS;
-        if (!wait_all(unit_full0 + 8u * at, (i / PL::UNITS) & 1, SITE_Q_FULL))
+        if (!wait_all(unit_full0 + 8u * at, (i / PL::UNITS) & 1, SITE_Q_FULL)) {
+            un.n = -1;  // (the copiers look its pages up before they leave)
             return false;
+        }
         un = ring[at];
         arrive(unit_free0 + 8u * at);
         return un.n >= 0;
@@ -610,7 +612,7 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         int g0 = 0;
         Unit un;
         int published = 0, longest = 1;  // units, and the tiles of the longest: its end may be what is waited for
-        bool more = warp == 11;
+        bool more = warp == 11 && p.no_units == 0;
         if (more)
             runs.start(p, sums);
         for (int k = 0;; ++k) {

@@ -482,7 +482,8 @@ unsigned int sdp_set_wait_timeout_ms(unsigned int ms);
  * kernel. Bit 7: at head dim 128, run dense non-causal launches whose two-tile
  * units pair up on the two-tile CTA-pair kernel (two 128-row query tiles per
  * CTA, 64-key softmax steps; the same function, rounded differently), even
- * below one wave of CTAs. Returns the previous flags.
+ * below one wave of CTAs. Bit 8: sdp_fwd_cache16's warps are given no work, so that
+ * each one's first wait runs out. Returns the previous flags.
  */
 int sdp_set_debug_flags(int flags);
 

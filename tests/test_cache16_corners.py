@@ -36,3 +36,23 @@ def test_starts_of_many_entries(D):
     assert sdp.poll_status() == sdp.SDP_OK
     for o, lse in outs:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [128, 256])
+def test_waits_for_the_first_unit_that_run_out(D):
+    """No unit is published: every warp gives up before it has one, looks nothing up, and the next call is right."""
+    b = Batch([500, 300, 420, 290], [0, 3], [280], 1, 8, 2, D, 32, torch.bfloat16)
+    a = b.args()
+    want = sdp.fwd_cache16(**a)
+    assert sdp.poll_status() == sdp.SDP_OK
+    old = sdp.set_wait_timeout_ms(20)
+    sdp.set_debug_flags(256)
+    try:
+        sdp.fwd_cache16(**a)
+        assert sdp.poll_status() == sdp.SDP_ERR_DEVICE_TIMEOUT
+    finally:
+        sdp.set_debug_flags(0)
+        sdp.set_wait_timeout_ms(old)
+    o, lse = sdp.fwd_cache16(**a)
+    assert sdp.poll_status() == sdp.SDP_OK and torch.equal(o, want[0]) and torch.equal(lse, want[1])
