@@ -102,13 +102,14 @@ __device__ __forceinline__ int2 group_range(const Cache16Params &p, int g)
     return p.cu_groups == nullptr ? make_int2(0, p.nseq) : make_int2(__ldg(p.cu_groups + g), __ldg(p.cu_groups + g + 1));
 }
 
-// The prefix of group g, whose sequences are [r.x, r.y). A group of one sequence has nothing to share.
+// The prefix of group g, whose sequences are [r.x, r.y). A single sequence's is read from the prefix's pages too: its own need
+// not hold it, and how many sequences a group has is known on the device alone.
 __device__ __forceinline__ Share prefix_of(const Cache16Params &p, int g, int2 r)
 {
     const int P = __ldg(p.prefix_lens + g);
     const bool order = 0 <= r.x && r.x <= r.y && r.y <= p.nseq;
     Share s{g, 0, !order || P < 0 || P > p.prefix_pages * p.page_size};  // the host keeps the product in 31 bits
-    if (!s.bad && r.y - r.x > 1)
+    if (!s.bad && r.y > r.x)
         s.P = P;
     return s;
 }

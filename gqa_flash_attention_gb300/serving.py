@@ -348,8 +348,9 @@ def fwd_cache16(q: torch.Tensor, cache: Cache16, cache_lens: torch.Tensor, block
     Sequences cu_groups[g] .. cu_groups[g + 1] - 1 have their first prefix_lens[g] tokens in common, in the pages of
     prefix_table[g] (int32 [groups, pages]; for one group of all sequences cu_groups may be None). These are read
     and multiplied once for the whole group, and entries of its sequences' block tables for pages that the prefix fills are
-    not read, except of sequences shorter than the prefix and rows - 1 more, which go through their own pages. A
-    prefix may end inside a page. All on the device: a captured step stays valid when lengths and tables change.
+    not read, except of sequences shorter than the prefix and rows - 1 more, which go through their own pages; the last
+    sequence left of a group is no exception. A prefix may end inside a page. All on the device: a captured step stays valid
+    when lengths, groups and tables change.
 
     Returns (o like q, lse fp32 without the last dimension, or None); a row that sees no key gives 0 and -inf. workspace: a
     contiguous CUDA tensor of cache16_workspace_bytes, not used by another call that may overlap; when None it comes

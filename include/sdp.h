@@ -388,7 +388,8 @@ int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_siz
  * find them in L2), and each sequence's own pages supply the rest: entries of its block table for pages that the prefix
  * fills are not read. A prefix may end inside a page; the sequence's own page there need not hold the prefix's tokens.
  * A sequence whose first row does not see the whole prefix (shorter than prefix + rows - 1, or empty: a padded batch) goes
- * through its own pages alone, and so does a group of one sequence, so block tables are to be complete for those.
+ * through its own pages alone, so block tables are to be complete for those. A group may have any number of sequences: one
+ * alone has its prefix read from prefix_table likewise.
  *
  * q, o   device, dtype [nseq, rows, Hq, D] contiguous; lse fp32 [nseq, rows, Hq] or NULL.
  *        The rows' own keys must be in the cache (append first).

@@ -1,11 +1,17 @@
 """Corners of the 16-bit paged cache: the start of a call whose entries fill every thread, limits of the arguments, offsets that
 no row belongs to, groups that shrink to one sequence, values that are not finite, many heads behind a prefix."""
 
+import math
+
 import pytest
 import torch
 
 import gqa_flash_attention_gb300 as sdp
-from test_cache16_attn import Batch, c_call
+from test_cache16_attn import DTYPES, Batch, c_call
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
 @pytest.mark.parametrize("kw", [
@@ -56,3 +62,40 @@ def test_waits_for_the_first_unit_that_run_out(D):
         sdp.set_wait_timeout_ms(old)
     o, lse = sdp.fwd_cache16(**a)
     assert sdp.poll_status() == sdp.SDP_OK and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("prefix", [64, 75, 600])
+@pytest.mark.parametrize("rows,D", [(1, 128), (3, 256)])
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+def test_groups_of_one_sequence(prefix, rows, D, dt):
+    """Their prefixes are read from the prefix's pages, as those of larger groups: their own tables have none for the pages
+    that it fills, and where it ends inside a page their own page holds NaN and infinities up to there."""
+    b = Batch([prefix + 70, prefix + rows - 1, prefix + 1000], [0, 3], [prefix], rows, 8, 2, D, 16, DTYPES[dt])
+    assert (b.table[:, :prefix // 16] == -7).all()
+    a = b.args()
+    a["prefix_table"], a["prefix_lens"] = a["prefix_table"].repeat(3, 1), i32(prefix, prefix, prefix)
+    a["cu_groups"] = i32(0, 1, 2, 3)
+    o, lse = sdp.fwd_cache16(**a)
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+def test_a_captured_step_whose_group_shrinks_to_one():
+    b = Batch([300, 333, 290], [0, 3], [139], 2, 8, 2, 128, 48, torch.bfloat16)
+    a = b.args()
+    out, lse = torch.zeros_like(a["q"]), torch.zeros(a["q"].shape[:-1], device="cuda")
+    ws = torch.empty(sdp.cache16_workspace_bytes(3, 2, 8, 2, 128, torch.bfloat16, 1), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sdp.fwd_cache16(**a, out=out, lse=lse, workspace=ws)
+    for left in (3, 2, 1, 0):  # sequences: the others end, and their places are padding
+        a["cu_groups"][1] = left
+        a["cache_lens"][left:] = 0
+        out.fill_(5)
+        graph.replay()
+        assert sdp.poll_status() == sdp.SDP_OK
+        b.check(out, lse, only=range(left))
+        assert (out[left:] == 0).all() and (lse[left:] == -math.inf).all()
