@@ -10,6 +10,10 @@ namespace sdp {
 namespace c16 {
 
 constexpr int JOIN_THREADS = 128;
+// A part's weight beside the largest is positive, however small: an infinity among its values (of a drafted token, where add_odd
+// has put it onto the part) stays one, as in a row that is not joined. 2^-149 of bf16's largest value is 2^-21, of a sum that is
+// divided by 1 or more.
+constexpr float LEAST = 0x1p-149f;
 
 // Where a row's parts of one problem are: the word the problem's first run left, and the row's place in a part.
 struct Parts {
@@ -115,10 +119,10 @@ __global__ void __launch_bounds__(c16::JOIN_THREADS) cache16_join_kernel(const _
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)
             top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
-        const float next = fmaxf(mx, top), by = mx == -INFINITY ? 0.f : ptx::ex2(mx - next);
+        const float next = fmaxf(mx, top), by = mx == -INFINITY ? 0.f : fmaxf(ptx::ex2(mx - next), LEAST);
         mx = next;
         // 1: the part holds 0, or NaN
-        const float w = (m == -INFINITY ? 1.f : ptx::ex2(m - mx)) * l;
+        const float w = (m == -INFINITY ? 1.f : fmaxf(ptx::ex2(m - mx), LEAST)) * l;
         float total = w;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1)

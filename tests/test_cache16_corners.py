@@ -99,3 +99,30 @@ def test_a_captured_step_whose_group_shrinks_to_one():
         assert sdp.poll_status() == sdp.SDP_OK
         b.check(out, lse, only=range(left))
         assert (out[left:] == 0).all() and (lse[left:] == -math.inf).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D,G,P", [(128, 4, 300), (256, 16, 300), (128, 1, 12000)])
+def test_an_infinite_draft_behind_a_prefix_of_far_larger_scores(D, G, P):
+    """The prefix's keys score 2^250 times the others in weight, which leaves those no fp32 weight at all: an infinity or a NaN in
+    a drafted token's V, whose weight is positive, decides its channel of the rows that see it all the same."""
+    rows, page, loud = 3, 16, 11.0 * math.sqrt(D)
+    b = Batch([P + 9, P + 40], [0, 2], [P], rows, G, 1, D, page, torch.bfloat16)
+    b.q[..., 7] = 16.0
+    t = torch.arange(P)
+    b.k[b.prefix_table[0, t // page].long(), :, t % page, 7] = loud
+    for s, n in enumerate(b.lens):
+        t = torch.arange(P, n)
+        b.k[b.table[s, t // page].long(), :, t % page, 7] = 0
+        b.rows_kv[s][0][:P, :, 7], b.rows_kv[s][0][P:, :, 7] = loud, 0
+    want, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(want, lse)
+    for s, back, c, x in ((0, 2, 5, math.inf), (0, 1, 9, math.nan), (1, 1, 64, -math.inf), (1, 3, D - 1, math.inf)):
+        t = b.lens[s] - back
+        b.v[int(b.table[s, t // page]), 0, t % page, c] = x
+        want[s, rows - back:, :, c] = x
+    o, l2 = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK and torch.equal(l2, lse)
+    same = (o == want) | (o.isnan() & want.isnan())
+    assert same.all(), same.logical_not().nonzero()[:4]
