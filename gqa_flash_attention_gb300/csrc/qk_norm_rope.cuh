@@ -231,12 +231,14 @@ __global__ void __launch_bounds__(32 * kWarps) qk_norm_rope_kernel(const RopePar
     }
     Place place{0, 0, 0};
     if constexpr (CACHE) {
-        if (blockIdx.x == 0)  // all offsets: a token of a sequence with bad ones may belong to none
-            for (int i = threadIdx.x; i < c.nseq; i += 32 * kWarps) {
+        if (blockIdx.x == 0) {  // all offsets: a token of a sequence with bad ones may belong to none
+            const int warps = static_cast<int>(min(static_cast<long long>(p.tokens) * runs, static_cast<long long>(kWarps)));  // with work
+            for (int i = threadIdx.x; i < c.nseq; i += 32 * warps) {
                 const int x = __ldg(c.cu + i), y = __ldg(c.cu + i + 1);
                 if (x < 0 || y < x || y > p.tokens)
                     atomicCAS(c.status, 0u, kBadSeqlens);
             }
+        }
         place = locate(c, token, p.tokens);
         if (place.position < 0)
             return;

@@ -126,3 +126,24 @@ def test_an_infinite_draft_behind_a_prefix_of_far_larger_scores(D, G, P):
     assert sdp.poll_status() == sdp.SDP_OK and torch.equal(l2, lse)
     same = (o == want) | (o.isnan() & want.isnan())
     assert same.all(), same.logical_not().nonzero()[:4]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("tokens,Hkv,D", [(1, 1, 128), (1, 1, 256), (1, 2, 256), (2, 1, 128), (3, 4, 128)])
+def test_appending_few_rows_checks_all_offsets(tokens, Hkv, D):
+    """A call of fewer than four warps' work: bad offsets of sequences that none of its rows belongs to are reported, wherever
+    they stand among the sequences'."""
+    nseq = 300
+    c = sdp.cache16_empty(8, Hkv, D, 16, torch.float16)
+    k = torch.ones(tokens, Hkv, D, dtype=torch.float16, device="cuda")
+    table = torch.zeros(nseq, 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((nseq,), 16, dtype=torch.int32, device="cuda")
+    good = torch.full((nseq + 1,), tokens, dtype=torch.int32, device="cuda")
+    good[0] = 0
+    sdp.cache16_append(c, k, k, good, lens, table)
+    assert sdp.poll_status() == sdp.SDP_OK
+    for at in range(1, nseq + 1):
+        cu = good.clone()
+        cu[at] = tokens + 1
+        sdp.cache16_append(c, k, k, cu, lens, table)
+        assert sdp.poll_status() == sdp.SDP_ERR_BAD_SEQLENS, at
