@@ -88,8 +88,9 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_table == nullptr || cache_lens == nullptr ||
         o == nullptr || workspace == nullptr)
         return SDP_ERR_INVALID_ARG;
+    const float c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // of powers of two
     if (num_pages <= 0 || page_size <= 0 || page_size % 16 != 0 || max_pages <= 0 || table_stride < 0 ||
-        !std::isfinite(scale) || o == q || o == k_cache || o == v_cache || ngroups < 0)
+        !std::isfinite(c) || o == q || o == k_cache || o == v_cache || ngroups < 0)
         return SDP_ERR_INVALID_ARG;
     if (ngroups > 0 && (prefix_table == nullptr || prefix_lens == nullptr || prefix_pages <= 0 || prefix_stride < 0 ||
                         (cu_groups == nullptr && ngroups != 1)))
@@ -166,9 +167,7 @@ extern "C" int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v
     p.timeout_ns = sdp::wait_timeout_ns();
     p.no_copies = sdp::debug_flags() & 1;
     p.no_units = sdp::debug_flags() & 256;
-    p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    if (p.c == 0.f)
-        p.c = 1e-37f;  // scores of 0, where those that a row does not see are still -inf
+    p.c = c != 0.f ? c : 1e-37f;  // (scores of 0, where those that a row does not see are still -inf)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (D == 128)

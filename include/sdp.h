@@ -400,7 +400,8 @@ int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_siz
  * workspace  device scratch of at least sdp_fwd_cache16_workspace_bytes, 16-byte aligned, not overlapping the other
  *        buffers and not shared with a call that may overlap on the GPU (two graphs replayed at once need two); its
  *        contents do not matter before and are unspecified after.
- * Scores, weights and sums are fp32; the weights are rounded to dtype for the product with V, as in sdp_fwd. The same call
+ * Scores, weights and sums are fp32; the weights are rounded to dtype for the product with V, as in sdp_fwd. scale * log2(e),
+ * which the scores are multiplied by, has to be finite in fp32 too (SDP_ERR_INVALID_ARG). The same call
  * gives the same bits. Keys and values that a row does not see may hold infinities or NaN. Bad lengths leave that
  * sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a bad prefix length or group is not shared, and reported the same; a
  * page outside the pool leaves rows unspecified (SDP_ERR_BAD_PAGES), a wait that runs out all rows

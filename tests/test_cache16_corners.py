@@ -25,6 +25,14 @@ def test_tables_of_almost_two_to_the_31_keys_are_refused(kw):
     assert c_call(**{**dict(nseq=1, Hq=1, Hkv=1), **kw}) == sdp.SDP_ERR_OVERFLOW
 
 
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.36e38, math.inf])
+def test_scales_that_leave_fp32_in_powers_of_two_are_refused(scale):
+    """They would be multiplied as infinities: a score of 0 as NaN."""
+    from gqa_flash_attention_gb300 import build
+    build.build()
+    assert c_call(scale=scale) == sdp.SDP_ERR_INVALID_ARG
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [128, 256])
 def test_starts_of_many_entries(D):
