@@ -476,6 +476,7 @@ Pool16 pool16_of(PyObject *cache, at::ScalarType type, int dev)
           "the cache must be [num_pages, Hkv, page_size, D] tensors of the inputs' dtype");
     check(k.is_contiguous() && v.is_contiguous() && cuda_index(k) == dev && cuda_index(v) == dev,
           "the cache must be contiguous on the inputs' device");
+    forward_only({&k, &v});
     return Pool16{k, v, size32(k.size(0), "num_pages"), size32(k.size(2), "page_size"), size32(k.size(1), "Hkv"),
                   size32(k.size(3), "D")};
 }

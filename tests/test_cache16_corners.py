@@ -155,3 +155,24 @@ def test_appending_few_rows_checks_all_offsets(tokens, Hkv, D):
         cu[at] = tokens + 1
         sdp.cache16_append(c, k, k, cu, lens, table)
         assert sdp.poll_status() == sdp.SDP_ERR_BAD_SEQLENS, at
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_caches_that_require_grad_are_refused(which):
+    """As learned prefixes would: no gradient would come back. Without grad mode they are as good as others."""
+    b = Batch([40, 50], [0], [], 1, 2, 1, 128, 16, torch.float16)
+    a = b.args()
+    want = sdp.fwd_cache16(**a)
+    getattr(a["cache"], which).requires_grad_()
+    new = dict(cu_seqlens=i32(0, 1, 1), cache_lens=a["cache_lens"], block_table=a["block_table"])
+    row = torch.ones(1, 1, 128, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        sdp.fwd_cache16(**a)
+    with pytest.raises(ValueError):
+        sdp.cache16_append(a["cache"], row, row, **new)
+    with torch.no_grad():
+        got = sdp.fwd_cache16(**a)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        sdp.cache16_append(a["cache"], row, row, **new)
+    assert sdp.poll_status() == sdp.SDP_OK
