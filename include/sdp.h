@@ -401,14 +401,16 @@ int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_siz
  *        buffers and not shared with a call that may overlap on the GPU (two graphs replayed at once need two); its
  *        contents do not matter before and are unspecified after.
  * Scores, weights and sums are fp32; the weights are rounded to dtype for the product with V, as in sdp_fwd. scale * log2(e),
- * which the scores are multiplied by, has to be finite in fp32 too (SDP_ERR_INVALID_ARG). The same call
- * gives the same bits. Keys and values that a row does not see may hold infinities or NaN. Bad lengths leave that
- * sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a bad prefix length or group is not shared, and reported the same; a
- * page outside the pool leaves rows unspecified (SDP_ERR_BAD_PAGES), a wait that runs out all rows
+ * which the scores are multiplied by, has to be finite in fp32 too (SDP_ERR_INVALID_ARG). The same call gives the same bits.
+ * Keys and values that a row does not see may hold infinities or NaN. An infinity in V gives one in its channel of the rows
+ * that see it, or a NaN where its weight, beside the row's largest, is too small for dtype (in fp16 below 2^-25).
+ * Bad lengths leave that sequence's rows unwritten (SDP_ERR_BAD_SEQLENS); a bad prefix length or group is not shared, and
+ * reported the same; a page outside the pool leaves rows unspecified (SDP_ERR_BAD_PAGES), a wait that runs out all rows
  * (SDP_ERR_DEVICE_TIMEOUT). Errors, streams and the status word's first-call allocation as sdp_fwd. Two kernels are enqueued
  * on `stream`; they, and sdp_cache16_append's, may be launched while what is before them on the stream ends, and read and
- * write nothing before it has. Rows, and 128-key tiles that all sequences' tables and prefixes could hold for every KV head, are counted in
- * 31 bits, and max_pages * page_size and prefix_pages * page_size end 4096 below 2^31 (SDP_ERR_OVERFLOW). The workspace size depends on the current device; a negative value is a status code.
+ * write nothing before it has. Rows, and 128-key tiles that all sequences' tables and prefixes could hold for every KV head,
+ * are counted in 31 bits, and max_pages * page_size and prefix_pages * page_size end 4096 below 2^31 (SDP_ERR_OVERFLOW).
+ * The workspace size depends on the current device; a negative value is a status code.
  */
 long long sdp_fwd_cache16_workspace_bytes(int nseq, int rows, int Hq, int Hkv, int D, int dtype, int ngroups);
 int sdp_fwd_cache16(const void *q, const void *k_cache, const void *v_cache, int num_pages, int page_size,

@@ -176,3 +176,39 @@ def test_caches_that_require_grad_are_refused(which):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         sdp.cache16_append(a["cache"], row, row, **new)
     assert sdp.poll_status() == sdp.SDP_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("lens,cu,prefix,rows,Hq,Hkv,D,page,dt", [
+    ([300, 333, 290], [0, 3], [139], 3, 200, 1, 128, 48, "bf16"),  # a prefix that ends inside a page
+    ([300, 333, 141, 2, 500], [0, 3, 4, 5], [139, 50, 480], 2, 400, 2, 256, 32, "fp16"),
+    ([900, 700], [0, 2], [640], 1, 129, 1, 256, 64, "bf16"),
+])
+def test_more_heads_than_a_block_behind_a_prefix(lens, cu, prefix, rows, Hq, Hkv, D, page, dt):
+    """More than 128 query heads a KV head: blocks of heads, the last one not full, in both kinds of problems and in the join."""
+    b = Batch(lens, cu, prefix, rows, Hq, Hkv, D, page, DTYPES[dt])
+    o, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    b.check(o, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["fp16", "bf16"])
+@pytest.mark.parametrize("D,G", [(128, 4), (256, 16)])
+def test_values_of_a_prefix_that_are_not_finite(D, G, dt):
+    """An infinity or a NaN in the V of a key that all rows see (with a weight that the 16-bit type holds) reaches its channel
+    of the rows of its group, and nothing else."""
+    page, P = 16, 200
+    b = Batch([230, 205, 900, 300], [0, 3], [P], 2, G, 1, D, page, DTYPES[dt])
+    want, lse = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK
+    for t, c, x in ((0, 3, math.inf), (130, D - 1, -math.inf), (P - 1, 64, math.nan)):
+        b.v[int(b.prefix_table[0, t // page]), 0, t % page, c] = x
+        want[:3, :, :, c] = x
+    t = 250  # one of the sequence in no group
+    b.v[int(b.table[3, t // page]), 0, t % page, 7] = math.inf
+    want[3, :, :, 7] = math.inf
+    o, l2 = sdp.fwd_cache16(**b.args())
+    assert sdp.poll_status() == sdp.SDP_OK and torch.equal(l2, lse)
+    same = (o == want) | (o.isnan() & want.isnan())
+    assert same.all(), same.logical_not().nonzero()[:4]
