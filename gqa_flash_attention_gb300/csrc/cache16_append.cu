@@ -77,7 +77,8 @@ extern "C" int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, i
 
     RopeParams p{};
     CacheDest c{};
-    // the split of the passes over warps is qk_norm_rope's, with v's passes behind k's
+    // The split of the passes over warps is qk_norm_rope's, with v's passes behind k's. (It counts on 32 warps an SM, of which 16 to 20
+    // are resident, and a token's last run may be short: 3095 tokens of 48 passes are runs of 30 and 18.)
     const int rpp = 256 / D;
     const long long passes_q = (Hq + static_cast<long long>(rpp) - 1) / rpp;
     const long long passes_kv = (Hkv + static_cast<long long>(rpp) - 1) / rpp;

@@ -33,8 +33,8 @@
 // that one run holds whole, and whose rows share no prefix, is written as it ends; what else there is, is joined
 // by cache16_join.cuh's kernel, which starts as CTAs end. Results do not depend on the order in which CTAs run.
 //
-// Two tiles at a time of queries that share a tile of K and V (CTA pairs) would halve the copies; one tile's O and S buffers
-// fill tensor memory at D = 256.
+// Blocks of 256 rows by CTA pairs, each CTA with its own 128 rows and half of every tile of K and V, would halve the copies and what
+// S and PV read of them: not built. (One CTA has no room for two blocks: one's O and S buffers fill tensor memory at D = 256.)
 //
 // What a problem's start and end cost. Each runs through some 30 KB of code once (look-up, copies, masks, cleaning, rows' ends), and
 // with sixteen warps at seven kinds of work that is more than the instruction cache nearest them keeps: straight code then
@@ -43,8 +43,8 @@
 // run through one place, each box of a slot is a lane's, and the rows' ends are two loops of a few lines.
 //
 // 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 45 us, where HBM alone takes 24;
-// 256 behind 16384, 32 heads over 2, D = 256: 129 us, where the tensor cores alone take 72; eight of 16384 tokens that share
-// nothing, D = 256: 51 us (5.2 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 39 us, HBM 14. A launch
+// 256 behind 16384, 32 heads over 2, D = 256: 130 us, where the tensor cores alone take 72; eight of 16384 tokens that share
+// nothing, D = 256: 52 us (5.2 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 40 us, HBM 14. A launch
 // needs some 9000 cycles (5 us) before its first copy and the join 4 to 8 us after the last tile.
 //
 // Keys outside [lo, hi) of a problem share its first and last tiles. Their scores are replaced before any arithmetic, whatever

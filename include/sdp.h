@@ -389,7 +389,7 @@ int sdp_cache16_append(void *k_cache, void *v_cache, int num_pages, int page_siz
  * fills are not read. A prefix may end inside a page; the sequence's own page there need not hold the prefix's tokens.
  * A sequence whose first row does not see the whole prefix (shorter than prefix + rows - 1, or empty: a padded batch) goes
  * through its own pages alone, so block tables are to be complete for those. A group may have any number of sequences: one
- * alone has its prefix read from prefix_table likewise.
+ * alone has its prefix read from prefix_table likewise (with a whole table of its own, prefix length 0 is the faster call).
  *
  * q, o   device, dtype [nseq, rows, Hq, D] contiguous; lse fp32 [nseq, rows, Hq] or NULL.
  *        The rows' own keys must be in the cache (append first).
