@@ -224,12 +224,10 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
         if (lane == 0)
             ptx::mbar_arrive(bar);
     };
-    auto take = [&](int i, Unit &un) -> bool {  // unit i; false, and a unit without tiles, at the end or when a wait ran out
+    auto take = [&](int i, Unit &un) -> bool {  // unit i; false at the end or when a wait ran out
         const int at = i % PL::UNITS;
-        if (!wait_all(unit_full0 + 8u * at, (i / PL::UNITS) & 1, SITE_Q_FULL)) {
-            un.n = -1;  // (the copiers look its pages up before they leave)
+        if (!wait_all(unit_full0 + 8u * at, (i / PL::UNITS) & 1, SITE_Q_FULL))
             return false;
-        }
         un = ring[at];
         arrive(unit_free0 + 8u * at);
         return un.n >= 0;
@@ -270,8 +268,8 @@ __global__ void __launch_bounds__(c16::THREADS, 1)
                 const int plane = planes_of(p, un, now), off = now.off, end = min(un.n, j + tiles);
                 // the next batch's pages, of this unit or of the one behind it, are looked up while this one is copied
                 const bool same = end < un.n;
-                if (!same)
-                    more = take(k + 1, next_un);
+                if (!same && !(more = take(k + 1, next_un)))
+                    next_un.n = -1;  // (also where a wait ran out and there is none: no page of it is looked up)
                 next = pages_of(p, same ? un : next_un, same ? end / tiles : 0);
 #pragma unroll 1
                 for (; ok && j < end; ++j)
