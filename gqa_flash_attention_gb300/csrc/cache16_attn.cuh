@@ -44,7 +44,7 @@
 //
 // 64 sequences behind 8192 shared tokens, 10 to 2000 of their own, 32 heads over 8, D = 128: 45 us, where HBM alone takes 24;
 // 256 behind 16384, 32 heads over 2, D = 256: 130 us, where the tensor cores alone take 72; eight of 16384 tokens that share
-// nothing, D = 256: 52 us (5.2 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 40 us, HBM 14. A launch
+// nothing, D = 256: 51 us (5.2 TB/s), where HBM takes 40; 32 behind 4001, 32 heads of their own, D = 128: 39 us, HBM 14. A launch
 // needs some 9000 cycles (5 us) before its first copy and the join 4 to 8 us after the last tile.
 //
 // Keys outside [lo, hi) of a problem share its first and last tiles. Their scores are replaced before any arithmetic, whatever
